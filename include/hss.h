@@ -397,6 +397,177 @@ hss_status hss_layer_step_static(const hss_dims* dims, const uint16_t* P, const 
                                  int32_t* victims, int32_t* dev_status, void* stream);
 
 /*
+ * Rotary positions (RoFormer's rotary embedding; the predictor pages take keys and queries as
+ * they come, so no page has a counterpart).  A head's first rot_dim elements are rotated in
+ * pairs, pair i of a token at position pos by the angle
+ *     a(pos, i) = 2 pi frac(pos * turns[i] / 2^64),
+ * where turns[i] is the pair's frequency as a 64-bit fixed-point fraction of a turn per
+ * position.  The product of two whole numbers modulo 2^64 is exact, so an angle is as good at
+ * position 2^40 as at 1 (a 32-bit frequency times a position of 131072 is off by up to 0.008
+ * radians), and a negative position turns back by the same angle (the transposed rotation,
+ * which the gradient of a rotated row needs).
+ */
+#define HSS_ROPE_HALF 0        /* pair i = elements (i, i + rot_dim / 2) */
+#define HSS_ROPE_INTERLEAVED 1 /* pair i = elements (2 i, 2 i + 1) */
+
+/* Frequencies f_i = base^(-2 i / rot_dim) radians per position, for longer contexts scaled as */
+#define HSS_ROPE_SCALE_NONE 0   /* f_i */
+#define HSS_ROPE_SCALE_LINEAR 1 /* f_i / factor (position interpolation) */
+#define HSS_ROPE_SCALE_BASE 2   /* f_i of base * factor^(rot_dim / (rot_dim - 2)); rot_dim > 2 */
+#define HSS_ROPE_SCALE_RAMP 3   /* w f_i + (1 - w) f_i / factor, with w going from 0 to 1 as the
+                                   turns over the original context, n_i = original_ctx f_i /
+                                   (2 pi), go from low to high: w = clamp((n_i - low) /
+                                   (high - low), 0, 1) */
+
+typedef struct hss_rope {
+    int32_t rot_dim; /* even, 2 .. 256 */
+    int32_t scaling; /* HSS_ROPE_SCALE_* */
+    double base;     /* > 0 */
+    double factor;   /* > 0 (SCALE_NONE ignores it) */
+    double original_ctx, low, high; /* SCALE_RAMP only: original_ctx > 0, low < high */
+} hss_rope;
+
+/* The table turns[rot_dim / 2] of a rope, computed on the host in double (a host array; the
+ * caller copies it to the device once).  HSS_ERR_INVALID_ARGUMENT for values outside the ranges
+ * above or not finite. */
+hss_status hss_rope_table(const hss_rope* rope, uint64_t* turns);
+
+/* What the layers of one step share in hss_rope_tokens. */
+typedef struct hss_rope_args {
+    hss_dims dims;
+    int32_t rot_dim;          /* even, 2 .. head_dim: elements past it are copied */
+    int32_t layout;           /* HSS_ROPE_HALF or HSS_ROPE_INTERLEAVED */
+    const uint64_t* turns;    /* device, [rot_dim / 2], 8-byte aligned */
+    float magnitude;          /* factor on the rotated elements (1: none) */
+    const int64_t* positions; /* device, [num_tokens], any sign */
+    const int64_t* slots;     /* device, [num_tokens], as in hss_write_kv_tokens; needed with a
+                                 cache, else may be NULL */
+    int64_t num_tokens;
+    int64_t q_stride, k_stride, v_stride; /* elements from token to token of Q, K and V:
+                                             multiples of 8, at least heads * head_dim (the rows of
+                                             a fused projection have them all alike) */
+    int32_t* dev_status;      /* device int32 or NULL */
+} hss_rope_args;
+
+/*
+ * Rotate the queries and keys of new tokens and write keys and values into the paged cache, in
+ * one launch:
+ *   Q_out[i][h]                 = R(positions[i]) Q[i][h]     (every query head)
+ *   K_out[i][h]                 = R(positions[i]) K[i][h]     (K_out != NULL; every kv head)
+ *   K_cache[slot / bs][slot % bs][h] = the same key           (K_cache != NULL; slot = slots[i])
+ *   V_cache[slot / bs][slot % bs][h] = V[i][h]                (V_cache != NULL)
+ * with y_a = m (x_a cos - x_b sin), y_b = m (x_b cos + x_a sin) for a pair (a, b), computed in
+ * fp32 and rounded once to bf16.
+ *   Q, K, V   device, token i's heads at i * stride, dense [heads, head_dim] bf16; 16-byte
+ *             aligned.  Each may be NULL if none of its outputs is asked for, and an output
+ *             needs its input.
+ *   Q_out     device, [num_tokens, num_q_heads, head_dim] bf16, 16-byte aligned, or NULL
+ *   K_out     device, [num_tokens, num_kv_heads, head_dim] bf16, 16-byte aligned, or NULL (the
+ *             rows hss_write_kv_tokens projects into A_g)
+ *   K_cache, V_cache  device, [max_blocks, block_size, num_kv_heads, head_dim] bf16, 16-byte
+ *             aligned: this layer's caches, or NULL
+ * A negative slot marks padding (the cache is left alone, Q_out and K_out are still written); a
+ * slot >= max_blocks * block_size is skipped and raises HSS_ERR_OUT_OF_RANGE in *dev_status and
+ * the library's device error word.  If two tokens name one slot, either may win.  No output may
+ * overlap an input.
+ */
+hss_status hss_rope_tokens(const hss_rope_args* args, const uint16_t* Q, const uint16_t* K,
+                           const uint16_t* V, uint16_t* Q_out, uint16_t* K_out,
+                           uint16_t* K_cache, uint16_t* V_cache, void* stream);
+
+/* What the layers of one step share in hss_attend_tree. */
+typedef struct hss_attend_args {
+    hss_dims dims;
+    const int32_t* q_offsets;   /* device, [num_seqs + 1]: sequence s owns the rows
+                                   q_offsets[s] .. q_offsets[s + 1] - 1, its tree's nodes */
+    int64_t total_q;            /* rows in all, q_offsets[num_seqs] */
+    int32_t max_q;              /* at least the largest tree's nodes */
+    int32_t mask_words;         /* 64-bit words of a row's mask (tree_mask != NULL: >= 1) */
+    const uint64_t* tree_mask;  /* device, [total_q, mask_words], 8-byte aligned, or NULL */
+    const int32_t* block_table; /* device, [total_blocks] physical block ids */
+    const int32_t* seq_offsets; /* device, [num_seqs + 1], as in hss_score_blocks */
+    const int32_t* ctx_len;     /* device, [num_seqs]: cached tokens before the tree */
+    int64_t total_blocks;
+    int32_t num_seqs;
+    float scale;                /* factor on the scores, finite; usually head_dim^-0.5 */
+    float decay;                /* factor on weights_in, finite */
+    void* workspace;            /* device, 256-byte aligned, hss_attend_tree_workspace_bytes(...);
+                                   zero it once before its first use.  Calls that share one must
+                                   not run at the same time. */
+    size_t workspace_bytes;
+    int32_t* dev_status;        /* device int32 or NULL */
+} hss_attend_args;
+
+/* Bytes of the workspace: enough for every call with these dims and counts, or smaller ones
+ * (0 if a count is negative or the dims are not valid). */
+size_t hss_attend_tree_workspace_bytes(const hss_dims* dims, int32_t num_seqs, int32_t max_q,
+                                       int64_t total_blocks, int32_t with_weights);
+
+/*
+ * Attention of a tree of drafted tokens over the paged cache, and of the single new token of an
+ * ordinary decode step (a tree of one node) or a chunk of prompt tokens (a chain).  Sequence s
+ * has ctx_len[s] cached tokens, which all its rows see, and then its tree's nodes: node j's key
+ * and value are in the cache at position ctx_len[s] + j (write them first, e.g. with
+ * hss_rope_tokens).  Row i sees node j if bit j % 64 of tree_mask[row][j / 64] is set (nodes past
+ * the mask's words are not seen), or, with tree_mask NULL, if j <= i (a chain).  Position p is
+ * token p % block_size of the sequence's table entry p / block_size.  Query head h reads kv
+ * head h / (num_q_heads / num_kv_heads).  Over the tokens that a row sees:
+ *   lse[row][h] = ln sum_p exp(scale q.k_p)
+ *   out[row][h] = sum_p exp(scale q.k_p - lse) v_p
+ *   weights_out[e] = decay * weights_in[e] + sum over the sequence's rows, all query heads and
+ *                    the tokens p of table entry e of exp(scale q.k_p - lse)
+ * A row that sees nothing gets out 0 and lse -inf and adds no weight.  Keys and values that no
+ * row of the tree sees, or that lie past the sequence's last token, may hold anything (NaN and
+ * infinities included); a node's NaN or infinite value reaches only the rows that see it.
+ *   Q        device, [total_q, num_q_heads, head_dim] bf16, 16-byte aligned
+ *   K_cache, V_cache  as in hss_rope_tokens
+ *   out      device, [total_q, num_q_heads, head_dim] bf16, 16-byte aligned
+ *   lse      device, [total_q, num_q_heads] f32, or NULL
+ *   weights_in   device, [total_blocks] f32, or NULL (zeros)
+ *   weights_out  device, [total_blocks] f32, or NULL (weights_in is then not read); it may be
+ *                weights_in
+ * Scores, softmax statistics and sums are fp32; the weights exp(s - m) enter the product with V
+ * rounded to bf16, the statistics and block weights take them unrounded.
+ * Supported: num_q_heads / num_kv_heads <= 128; num_seqs, max_q >= 0.  Device-side errors
+ * (*dev_status and the library's device error word): a block id outside [0, max_blocks) hides
+ * its tokens and raises HSS_ERR_OUT_OF_RANGE; so does a table too short for ctx_len + nodes (the
+ * tokens past it are hidden); a negative ctx_len counts as 0; a sequence with more than max_q
+ * rows raises HSS_ERR_INVALID_ARGUMENT and its rows past max_q are not written.
+ */
+hss_status hss_attend_tree(const hss_attend_args* args, const uint16_t* Q,
+                           const uint16_t* K_cache, const uint16_t* V_cache, uint16_t* out,
+                           float* lse, const float* weights_in, float* weights_out,
+                           void* stream);
+
+/*
+ * Eviction from the cache by accumulated attention weight: cut every sequence's table to its
+ * budget.  Sequence s (n entries) may lose its entries j with
+ *   keep_first <= j < n - keep_last     and, with ctx_len, only whole ones, j < ctx_len[s] / block_size;
+ * of these it loses the max(n - budgets[s], 0) (or all, if there are fewer) with the least
+ * (weight, index): -0 equals +0 and NaN ranks as +inf, as in hss_rank_victims.  The entries that
+ * stay keep their order:
+ *   new_offsets[num_seqs + 1]  the offsets of the shorter tables
+ *   new_table, new_weights     [total_blocks] the entries that stay, packed; the rest of the
+ *                              arrays is -1 and 0
+ *   new_ctx_len[s] = ctx_len[s] - block_size * entries lost   (ctx_len and new_ctx_len both
+ *                              given, or both NULL)
+ *   freed [total_blocks]       the physical ids that were lost, by sequence and index, packed;
+ *                              the rest is -1.  Sequence s's are at freed_offsets[s] ..
+ *                              freed_offsets[s + 1] - 1.
+ * All arrays are on the device: weights and new_weights f32, the others int32.  No output may
+ * overlap an input.  Budgets below 0 count as 0.  block_size > 0, keep_first, keep_last >= 0,
+ * total_blocks <= 2^30.
+ * The result is exact.
+ */
+hss_status hss_evict_blocks(const float* weights, const int32_t* block_table,
+                            const int32_t* seq_offsets, const int32_t* ctx_len,
+                            const int32_t* budgets, int32_t num_seqs, int64_t total_blocks,
+                            int32_t block_size, int32_t keep_first, int32_t keep_last,
+                            int32_t* new_table, int32_t* new_offsets, float* new_weights,
+                            int32_t* new_ctx_len, int32_t* freed, int32_t* freed_offsets,
+                            void* stream);
+
+/*
  * Failure-detection self-test.  Every pipeline wait in the tensor-core kernels gives up
  * after a time limit and reports HSS_ERR_DEVICE_TIMEOUT instead of hanging the GPU.  This
  * call launches one small kernel whose thread waits, with that same bounded wait, on a

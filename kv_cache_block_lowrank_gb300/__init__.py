@@ -36,6 +36,13 @@ HSS_PATH_DECODE = 1
 HSS_PATH_TCGEN05 = 2
 HSS_MAX_VICTIMS = 8192
 
+HSS_ROPE_HALF = 0
+HSS_ROPE_INTERLEAVED = 1
+HSS_ROPE_SCALE_NONE = 0
+HSS_ROPE_SCALE_LINEAR = 1
+HSS_ROPE_SCALE_BASE = 2
+HSS_ROPE_SCALE_RAMP = 3
+
 EXPORTED = (
     "hss_status_string", "hss_version", "hss_validate_dims", "hss_a_g_bytes", "hss_project_q",
     "hss_project_kv_blocks", "hss_score_blocks", "hss_rank_victims", "hss_read_device_error",
@@ -43,7 +50,8 @@ EXPORTED = (
     "hss_score_blocks_masked",
     "hss_layer_step_static_max_seqs", "hss_write_kv_tokens", "hss_score_rows",
     "hss_select_rows", "hss_self_test_wait_timeout", "hss_self_test_spread_wait",
-    "hss_layer_step_bound",
+    "hss_layer_step_bound", "hss_rope_table", "hss_rope_tokens", "hss_attend_tree",
+    "hss_attend_tree_workspace_bytes", "hss_evict_blocks",
 )
 
 
@@ -135,6 +143,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.hss_layer_step_bound.restype = i32
     lib.hss_layer_step_bound.argtypes = [ctypes.POINTER(hss_layer_step_args), i32, vp, vp, vp,
                                          vp, vp]
+    lib.hss_rope_table.restype = i32
+    lib.hss_rope_table.argtypes = [ctypes.POINTER(hss_rope), vp]
+    lib.hss_rope_tokens.restype = i32
+    lib.hss_rope_tokens.argtypes = [ctypes.POINTER(hss_rope_args)] + [vp] * 8
+    lib.hss_attend_tree_workspace_bytes.restype = sz
+    lib.hss_attend_tree_workspace_bytes.argtypes = [dp, i32, i32, i64, i32]
+    lib.hss_attend_tree.restype = i32
+    lib.hss_attend_tree.argtypes = [ctypes.POINTER(hss_attend_args)] + [vp] * 8
+    lib.hss_evict_blocks.restype = i32
+    lib.hss_evict_blocks.argtypes = [vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, vp, vp, vp, vp,
+                                     vp, vp, vp]
     _lib = lib
     return lib
 
@@ -328,6 +347,138 @@ class LayerStep:
         st = self._fn(self._ref, int(layer), _ptr(K_new), _ptr(Q), _ptr(scores), _ptr(victims),
                       _stream(stream))
         _check(st, "hss_layer_step_bound")
+
+
+class hss_rope(ctypes.Structure):
+    """Rotary frequencies and their scaling for longer contexts (hss_rope in hss.h)."""
+
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32),
+        ("scaling", ctypes.c_int32),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("original_ctx", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+    ]
+
+
+def hss_rope_table(rope: hss_rope, turns) -> None:
+    """turns[i] (host array of rot_dim / 2 64-bit words) = pair i's turns per position in 2^-64."""
+    _check(load().hss_rope_table(ctypes.byref(rope), _ptr(turns)), "hss_rope_table")
+
+
+class hss_rope_args(ctypes.Structure):
+    """What the layers of one step share in hss_rope_tokens (hss_rope_args in hss.h)."""
+
+    _fields_ = [
+        ("dims", hss_dims),
+        ("rot_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("turns", ctypes.c_void_p),
+        ("magnitude", ctypes.c_float),
+        ("positions", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("num_tokens", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("dev_status", ctypes.c_void_p),
+    ]
+
+
+class RopeTokens:
+    """hss_rope_tokens with what the layers of one step share bound once.
+
+    Each call rotates one layer's queries and keys and writes its keys and values into the
+    paged caches; what a call does not want is None.  The tensors bound here are kept alive.
+    """
+
+    def __init__(self, dims, rot_dim: int, layout: int, turns, magnitude: float, positions, slots,
+                 num_tokens: int, q_stride: int, k_stride: int, v_stride: int, dev_status=None):
+        self._fn = load().hss_rope_tokens
+        self._keep = (turns, positions, slots, dev_status)
+        self._args = hss_rope_args(
+            hss_dims.of(dims), int(rot_dim), int(layout), _ptr(turns), float(magnitude),
+            _ptr(positions), _ptr(slots), int(num_tokens), int(q_stride), int(k_stride),
+            int(v_stride), _ptr(dev_status))
+        self._ref = ctypes.byref(self._args)
+
+    def __call__(self, Q, K, V, Q_out, K_out, K_cache, V_cache, stream=None) -> None:
+        st = self._fn(self._ref, _ptr(Q), _ptr(K), _ptr(V), _ptr(Q_out), _ptr(K_out),
+                      _ptr(K_cache), _ptr(V_cache), _stream(stream))
+        _check(st, "hss_rope_tokens")
+
+
+class hss_attend_args(ctypes.Structure):
+    """What the layers of one step share in hss_attend_tree (hss_attend_args in hss.h)."""
+
+    _fields_ = [
+        ("dims", hss_dims),
+        ("q_offsets", ctypes.c_void_p),
+        ("total_q", ctypes.c_int64),
+        ("max_q", ctypes.c_int32),
+        ("mask_words", ctypes.c_int32),
+        ("tree_mask", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("seq_offsets", ctypes.c_void_p),
+        ("ctx_len", ctypes.c_void_p),
+        ("total_blocks", ctypes.c_int64),
+        ("num_seqs", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("decay", ctypes.c_float),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("dev_status", ctypes.c_void_p),
+    ]
+
+
+def hss_attend_tree_workspace_bytes(dims, num_seqs: int, max_q: int, total_blocks: int,
+                                    with_weights: bool) -> int:
+    return load().hss_attend_tree_workspace_bytes(ctypes.byref(hss_dims.of(dims)), int(num_seqs),
+                                                  int(max_q), int(total_blocks),
+                                                  int(bool(with_weights)))
+
+
+class AttendTree:
+    """hss_attend_tree with what the layers of one step share bound once.
+
+    Each call attends one layer's rows over its caches: out, and where asked for the rows'
+    lse and the blocks' accumulated weights.  The tensors bound here are kept alive.
+    """
+
+    def __init__(self, dims, q_offsets, total_q: int, max_q: int, tree_mask, mask_words: int,
+                 block_table, seq_offsets, ctx_len, num_seqs: int, total_blocks: int,
+                 scale: float, decay: float, workspace, workspace_bytes: int, dev_status=None):
+        self._fn = load().hss_attend_tree
+        self._keep = (q_offsets, tree_mask, block_table, seq_offsets, ctx_len, workspace,
+                      dev_status)
+        self._args = hss_attend_args(
+            hss_dims.of(dims), _ptr(q_offsets), int(total_q), int(max_q), int(mask_words),
+            _ptr(tree_mask), _ptr(block_table), _ptr(seq_offsets), _ptr(ctx_len),
+            int(total_blocks), int(num_seqs), float(scale), float(decay), _ptr(workspace),
+            int(workspace_bytes), _ptr(dev_status))
+        self._ref = ctypes.byref(self._args)
+
+    def __call__(self, Q, K_cache, V_cache, out, lse=None, weights_in=None, weights_out=None,
+                 stream=None) -> None:
+        st = self._fn(self._ref, _ptr(Q), _ptr(K_cache), _ptr(V_cache), _ptr(out), _ptr(lse),
+                      _ptr(weights_in), _ptr(weights_out), _stream(stream))
+        _check(st, "hss_attend_tree")
+
+
+def hss_evict_blocks(weights, block_table, seq_offsets, ctx_len, budgets, num_seqs: int,
+                     total_blocks: int, block_size: int, keep_first: int, keep_last: int,
+                     new_table, new_offsets, new_weights, new_ctx_len, freed, freed_offsets,
+                     stream=None) -> None:
+    """Cut every sequence's table to its budget, the blocks with the least weight going first."""
+    st = load().hss_evict_blocks(_ptr(weights), _ptr(block_table), _ptr(seq_offsets),
+                                 _ptr(ctx_len), _ptr(budgets), int(num_seqs), int(total_blocks),
+                                 int(block_size), int(keep_first), int(keep_last),
+                                 _ptr(new_table), _ptr(new_offsets), _ptr(new_weights),
+                                 _ptr(new_ctx_len), _ptr(freed), _ptr(freed_offsets),
+                                 _stream(stream))
+    _check(st, "hss_evict_blocks")
 
 
 def hss_layer_step_static_max_seqs() -> int:

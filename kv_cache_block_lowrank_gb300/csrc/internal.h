@@ -153,6 +153,55 @@ hss_status launch_select_rows(const float* scores, int32_t rows, int64_t n, int6
 hss_status launch_rank_victims(const float* scores, const int32_t* seq_offsets, int32_t num_seqs,
                                int64_t total, int32_t k, int32_t* victims, cudaStream_t stream);
 
+// ------------------------------------------------------------------- rotary writes
+struct RopeArgs {
+    const hss_rope_args* a;
+    const uint16_t* Q;
+    const uint16_t* K;
+    const uint16_t* V;
+    uint16_t* Q_out;
+    uint16_t* K_out;
+    uint16_t* K_cache;
+    uint16_t* V_cache;
+};
+hss_status launch_rope(const RopeArgs& r, cudaStream_t stream);
+
+// ------------------------------------------------------------------- tree attention
+struct AttendArgs {
+    const hss_attend_args* a;
+    const uint16_t* Q;
+    const uint16_t* K;
+    const uint16_t* V;
+    uint16_t* out;
+    float* lse;
+    const float* weights_in;
+    float* weights_out;
+};
+size_t attend_workspace_bytes(const hss_dims& d, int32_t num_seqs, int32_t max_q,
+                              int64_t total_blocks, bool with_weights);
+hss_status launch_attend(const AttendArgs& a, cudaStream_t stream);
+
+// ------------------------------------------------------------------- eviction
+struct EvictArgs {
+    const float* weights;
+    const int32_t* table;
+    const int32_t* seq_offsets;
+    const int32_t* ctx_len;
+    const int32_t* budgets;
+    int32_t num_seqs;
+    int64_t total;
+    int32_t block_size;
+    int32_t keep_first;
+    int32_t keep_last;
+    int32_t* new_table;
+    int32_t* new_offsets;
+    float* new_weights;
+    int32_t* new_ctx_len;
+    int32_t* freed;
+    int32_t* freed_offsets;
+};
+hss_status launch_evict(const EvictArgs& e, cudaStream_t stream);
+
 // ------------------------------------------------------------------- layer step
 // Every argument check of hss_layer_step, and the path it takes, decided before anything is
 // enqueued (hss_layer_step and hss_layer_step_static both run it first).
