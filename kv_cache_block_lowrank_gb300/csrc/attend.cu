@@ -1,21 +1,77 @@
-// attend.cu -- attention of a tree of drafted tokens over the paged cache.
+// attend.cu -- attention of a tree of drafted tokens over the paged cache, on tcgen05.
 //
-// One CTA takes 16 rows (node, query head of one kv head) of a sequence and walks the
-// sequence's tokens in tiles of 32 through shared memory, one pass with the running maximum and
-// sum of the softmax, everything in fp32.  The block weights come from a second kernel that
-// forms the scores of an entry's tokens again and adds exp(s - lse).
+// For one sequence and kv head, the rows are (node, query head of the group) pairs, and
+//   S = Q K^T,  P = exp2(c S - m),  O = P V,  l = sum P
+// runs over the sequence's tokens in tiles, one pass, with the softmax's running maximum m.  S
+// and O are tcgen05 products (M = 128 rows, a row per TMEM lane, so that one thread owns a row's
+// maximum and sum and no shuffle is needed); P goes back to tensor memory in bf16 and is the A
+// operand of the second product; K is its own K-major operand, V an MN-major one, both as TMA
+// leaves them.
+//
+// Roles of a CTA (10 warps, one CTA per SM):
+//   warp 0      looks up block ids, TMA: queries, then K and V tiles, two rings
+//   warp 1      TMEM allocation; one thread issues every product
+//   warps 2..9  two softmax groups of four warps.  With at most 128 rows the groups take a
+//               sequence's even and odd tiles, each with its own O, m and l (joined later, like
+//               any two pieces of a split sequence); with more rows they take two row tiles over
+//               the same K and V.  Either way one group's exponentials run under the other
+//               group's products.
+//
+// Split.  All (sequence, batch of row tiles, kv head, tile) units form one list, cut into equal
+// contiguous ranges: every SM gets the same number of tiles whatever the lengths are.  A range's
+// pieces of (sequence, batch, head) leave unnormalised O, m and l in the workspace and
+// join_kernel adds them up.  Row tiles beyond one (large trees, chunks) go to neighbouring CTAs
+// that walk the same range in step, so that K and V come from HBM once and from L2 to the rest.
+//
+// Block weights: the softmax thread has the sum of every 16 of its tokens anyway (l is their
+// sum); with weights it stores them beside m, and weights_kernel scales each by exp2(m - lse)
+// and adds them up over rows and heads once lse is known.  Nothing is computed twice, and no
+// float atomics: the same call gives the same bits.
+//
+// Masked places.  Tokens of the context need no mask; a tile that holds nodes, the end of the
+// sequence or a bad block id gets 32 visibility bits per 32 tokens and row.  A zero weight does
+// not silence an infinite or NaN value in a matrix product, so before such a tile's second
+// product the group clears the values past the end and any non-finite element of a node's
+// value, and join_kernel adds those elements to the rows that do see the node.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
 #include "ptx.cuh"
 
 namespace hss {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kRows = 16;
-constexpr int kTokens = 32;
+constexpr int kThreads = 320;
+constexpr int kRows = 128;          // UMMA M
+constexpr int kMetaRing = 16;       // bad-id bits of the tiles in flight
+constexpr uint32_t kTmemCols = 512;
+constexpr int kCtas = 152;          // GB300's SMs; the workspace does not depend on the device
+constexpr float kLazy = 8.0f;       // the maximum may lag by 2^8 before O is rescaled
+
+// Tokens per tile, softmax groups, ring depths: S takes 2 TILE columns of TMEM and every
+// group's O HD, 512 in all, and the rings what is left of 227 KB.
+template <int HD, int NQ>
+struct Cfg {
+    static constexpr int kTile = HD <= 128 ? 128 : 64;
+    static constexpr int kGroups = HD == 256 ? 1 : 2;
+    static constexpr int kStageBytes = kTile * HD * 2;
+    static constexpr int kQBytes = NQ * kRows * HD * 2;
+    static constexpr int kBudget = 232448 - 1024 - 1024 - kQBytes;
+    static constexpr int kStages = kBudget / kStageBytes < 12 ? kBudget / kStageBytes : 12;
+    static constexpr int kStagesK = (kStages + 1) / 2;
+    static constexpr int kStagesV = kStages / 2;
+    static constexpr int kSmemBytes = 2048 + kQBytes + (kStagesK + kStagesV) * kStageBytes;
+    static_assert(kStagesV >= 2, "two tiles of V in flight");
+    static_assert(2 * kTile + kGroups * HD <= 512, "tensor memory");
+    static_assert(kStagesV + 3 <= kMetaRing, "tiles in flight");
+};
 
 struct AttendParams {
-    const uint16_t* Q;
-    const uint16_t* K;
     const uint16_t* V;
     uint16_t* out;
     float* lse;
@@ -29,206 +85,1053 @@ struct AttendParams {
     int64_t max_blocks;
     int64_t total_blocks;
     int32_t mask_words, num_seqs, max_q, nq, nkv, g, bs;
-    float scale, decay;
+    int32_t box;         // tokens per TMA box: the largest power of two that divides bs
+    int32_t nodes_tile;  // nodes per row tile, 128 / g
+    int32_t members;     // CTAs per group: row tiles (or pairs of them) walked in step
+    int32_t groups;
+    int32_t rowcap;      // rows of a tile that can be in use
+    int32_t head_dim;
+    float c;             // |scale| log2(e), or 1 for scale 0
+    float pre;           // 1, or -1 / 0 for a negative / zero scale: scores are multiplied first
+    float decay;
     int32_t* dev_status;
     int32_t* lib_error;
+    // workspace
+    int64_t* header;     // [0] tiles in all, [1] tiles per group
+    int64_t* seq_tiles;  // [num_seqs] tiles before a sequence
+    int32_t* seq_items;  // [num_seqs] (batch, head) items before a sequence
+    float* part_o;       // [slot][row][head_dim]
+    float2* part_ml;     // [slot][row] (m, l)
+    int32_t* part_bad;   // [slot] a node's value was not finite
+    float* row_lse;      // [unit row tile][row], log2
+    float* sums;         // [tile][member][q tile][16-token granule][row]
+    float* sums_m;       // [tile][member][q tile][row]
 };
 
-__device__ __forceinline__ float bf(uint16_t x) {
-    return __uint_as_float(static_cast<uint32_t>(x) << 16);
-}
-
-struct Seq {
-    int64_t q0, e0, tokens;
-    int nodes, ctx;
+struct SeqInfo {
+    int q0, nodes, ctx, tokens, e0, end;
 };
 
-__device__ __forceinline__ Seq seq_of(const AttendParams& p, int s) {
-    Seq x;
-    x.q0 = p.q_offsets[s];
-    x.nodes = p.q_offsets[s + 1] - static_cast<int>(x.q0);
-    if (x.nodes > p.max_q) {
-        if (threadIdx.x == 0) raise_error(p.dev_status, p.lib_error, HSS_ERR_INVALID_ARGUMENT);
-        x.nodes = p.max_q;
-    }
-    x.e0 = p.seq_offsets[s];
-    const int64_t room = (p.seq_offsets[s + 1] - x.e0) * p.bs;
-    x.ctx = max(p.ctx_len[s], 0);
-    x.tokens = static_cast<int64_t>(x.ctx) + x.nodes;
-    if (x.tokens > room) {
-        if (threadIdx.x == 0) raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
-        x.tokens = room;
-    }
+__device__ __forceinline__ SeqInfo load_seq(const AttendParams& p, int s) {
+    SeqInfo x;
+    x.q0 = __ldg(p.q_offsets + s);
+    x.nodes = __ldg(p.q_offsets + s + 1) - x.q0;
+    x.e0 = __ldg(p.seq_offsets + s);
+    x.end = __ldg(p.seq_offsets + s + 1);
+    x.ctx = max(__ldg(p.ctx_len + s), 0);
+    x.nodes = min(max(x.nodes, 0), p.max_q);
+    const int64_t room = static_cast<int64_t>(x.end - x.e0) * p.bs;
+    const int64_t want = static_cast<int64_t>(x.ctx) + x.nodes;
+    x.tokens = static_cast<int>(min(min(room, want), static_cast<int64_t>(0x7FFFFF00)));
     return x;
 }
 
-__device__ __forceinline__ bool sees(const AttendParams& p, const Seq& x, int node, int64_t pos) {
-    if (pos >= x.tokens) return false;
-    if (pos < x.ctx) return true;
-    const int64_t j = pos - x.ctx;
-    if (p.mask == nullptr) return j <= node;
-    if (j >= 64 * static_cast<int64_t>(p.mask_words)) return false;
-    return (p.mask[(x.q0 + node) * p.mask_words + (j >> 6)] >> (j & 63)) & 1;
+// Row tiles of a sequence are `span` nodes each (NQ tiles of 128 rows); `members` of them form a
+// batch.  A chain's rows see nothing past themselves, so its earlier batches have fewer tiles.
+template <int TILE>
+__device__ __forceinline__ int tiles_upto(const AttendParams& p, const SeqInfo& x, int nodes) {
+    const int seen = p.mask == nullptr ? min(x.tokens - x.ctx, nodes) + x.ctx : x.tokens;
+    return (max(min(seen, x.tokens), 0) + TILE - 1) / TILE;
+}
+template <int TILE>
+__device__ __forceinline__ int batch_tiles(const AttendParams& p, const SeqInfo& x, int span,
+                                           int b) {
+    return tiles_upto<TILE>(p, x, min(x.nodes, (b + 1) * p.members * span));
+}
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+template <int TILE>
+__device__ __forceinline__ int64_t seq_tiles(const AttendParams& p, const SeqInfo& x, int span,
+                                             int nb) {
+    if (p.mask != nullptr || nb == 1)
+        return static_cast<int64_t>(nb) * p.nkv * (nb > 0 ? batch_tiles<TILE>(p, x, span, 0) : 0);
+    int64_t w = 0;
+    for (int b = 0; b < nb; ++b) w += batch_tiles<TILE>(p, x, span, b);
+    return w * p.nkv;
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const AttendParams p) {
-    extern __shared__ float smem[];
-    float* q = smem;                        // [kRows][HD]
-    float* k = q + kRows * HD;              // [kTokens][HD + 1]
-    float* v = k + kTokens * (HD + 1);      // [kTokens][HD]
-    float* w = v + kTokens * HD;            // [kRows][kTokens]; -1: not seen
-    int* good = reinterpret_cast<int*>(w + kRows * kTokens);
+struct Start {
+    int s, b, h, t, item0;
+    int64_t total, per;
+};
+
+// One piece of this CTA's range: tiles [ta, ta + n) of (sequence, head) for row tile rt.
+struct Segment {
+    SeqInfo x;
+    int h, rt, ta, n, item;
+    bool rows;  // the row tile exists
+    int64_t f;  // list index of tile ta
+};
+
+template <int TILE>
+struct Walk {
+    SeqInfo x;
+    int s, b, h, t, nb, rts, item0, member, span;
+    int64_t f, f1;
+
+    __device__ __forceinline__ void enter(const AttendParams& p) {
+        x = load_seq(p, s);
+        rts = ceil_div(x.nodes, span);
+        nb = ceil_div(rts, p.members);
+    }
+    __device__ __forceinline__ void begin(const AttendParams& p, const Start& st, int span_nodes) {
+        const int group = blockIdx.x / p.members;
+        member = blockIdx.x % p.members;
+        span = span_nodes;
+        f = min(st.total, group * st.per);
+        f1 = min(st.total, f + st.per);
+        s = st.s;
+        b = st.b;
+        h = st.h;
+        t = st.t;
+        item0 = st.item0;
+        if (f < f1) enter(p);
+    }
+    __device__ __forceinline__ bool next(const AttendParams& p, Segment& g) {
+        while (f < f1) {
+            const int n = nb > 0 ? batch_tiles<TILE>(p, x, span, b) : 0;
+            if (t < n) {
+                const int take = static_cast<int>(min(static_cast<int64_t>(n - t), f1 - f));
+                g.x = x;
+                g.h = h;
+                g.rt = b * p.members + member;
+                g.rows = g.rt < rts;
+                g.ta = t;
+                const int mine = g.rows ? tiles_upto<TILE>(p, x, min(x.nodes, (g.rt + 1) * span)) : 0;
+                g.n = max(0, min(t + take, mine) - t);
+                g.item = item0 + b * p.nkv + h;
+                g.f = f;
+                f += take;
+                t += take;
+                return true;
+            }
+            t = 0;
+            if (++h < p.nkv) continue;
+            h = 0;
+            if (++b < nb) continue;
+            b = 0;
+            item0 += nb * p.nkv;
+            if (++s >= p.num_seqs) break;
+            enter(p);
+        }
+        return false;
+    }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The wait for TMEM loads, with their uses held behind it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t* v) {
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i])::"memory");
+}
+
+// 64 visibility bits of a row for nodes 64 w ..
+__device__ __forceinline__ uint64_t node_word(const AttendParams& p, const SeqInfo& x, int node,
+                                              int w) {
+    if (p.mask == nullptr) {
+        const int past = node - 64 * w;  // nodes up to `node` are seen
+        return past < 0 ? 0 : (past >= 63 ? ~0ull : (2ull << past) - 1);
+    }
+    if (w >= p.mask_words) return 0;
+    return __ldg(p.mask + (static_cast<int64_t>(x.q0) + node) * p.mask_words + w);
+}
+
+// Visibility of the 32 tokens from position p0 on for a row.
+__device__ __forceinline__ uint32_t visible32(const AttendParams& p, const SeqInfo& x, int node,
+                                              int p0) {
+    uint32_t bits;
+    const int j0 = p0 - x.ctx;
+    if (j0 <= -32) {
+        bits = 0xFFFFFFFFu;
+    } else if (j0 < 0) {
+        bits = (static_cast<uint32_t>(node_word(p, x, node, 0)) << -j0) | ((1u << -j0) - 1);
+    } else {
+        const int w = j0 >> 6, sh = j0 & 63;
+        uint64_t v = node_word(p, x, node, w) >> sh;
+        if (sh > 32) v |= node_word(p, x, node, w + 1) << (64 - sh);
+        bits = static_cast<uint32_t>(v);
+    }
+    const int left = x.tokens - p0;
+    return left >= 32 ? bits : (left <= 0 ? 0u : bits & ((1u << left) - 1));
+}
+
+struct Barriers {
+    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], values;
+    uint32_t bad_ids[kMetaRing];  // per tile in flight: granules of 16 tokens with a bad id
+    int bad_value[2][2];          // [group][segment parity]: last segment with such a value
+    int abort;
+    uint32_t tmem;
+    Start start;
+    int64_t scan[kThreads / 32];
+    int scan_items[kThreads / 32];
+};
+
+template <int HD, int NQ>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const __grid_constant__ CUtensorMap map_q,
+                  const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v, const AttendParams p) {
+    using C = Cfg<HD, NQ>;
+    constexpr int TILE = C::kTile, NG = C::kGroups;
+    constexpr int SK = C::kStagesK, SV = C::kStagesV;
+    constexpr int kChunks = HD / 64;  // 128-byte columns of an operand row
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* sQ = smem;
+    uint8_t* sK = sQ + C::kQBytes;
+    uint8_t* sV = sK + SK * C::kStageBytes;
+    Barriers& bar = *reinterpret_cast<Barriers*>(sV + SV * C::kStageBytes);
+    static_assert(sizeof(Barriers) <= 1024, "barrier block");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int span = NQ * p.nodes_tile;
+
+    if (warp == 1) {
+        tmem_alloc(&bar.tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < SK; ++i) {
+            mbar_init(&bar.k_full[i], 1);
+            mbar_init(&bar.k_empty[i], 1);
+        }
+        for (int i = 0; i < SV; ++i) {
+            mbar_init(&bar.v_full[i], 1);
+            mbar_init(&bar.v_empty[i], 1);
+        }
+        mbar_init(&bar.q_full, 1);
+        mbar_init(&bar.q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.o_done[i], 1);
+            bar.bad_value[i][0] = bar.bad_value[i][1] = -1;
+        }
+        mbar_init(&bar.values, 8);
+        bar.abort = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&map_q);
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
     grid_dependency_wait();
     grid_launch_dependents();
-    const int tiles = (p.max_q * p.g + kRows - 1) / kRows;
-    const int tile = blockIdx.x % tiles;
-    const int h = blockIdx.x / tiles % p.nkv;
-    const int s = blockIdx.x / tiles / p.nkv;
-    const Seq x = seq_of(p, s);
-    const int row0 = tile * kRows, rows = x.nodes * p.g;
-    if (row0 >= rows) return;
-    const int tid = threadIdx.x, r = tid / 8, c = tid % 8;
-    const int row = row0 + r, node = row / p.g, head = h * p.g + row % p.g;
-    for (int i = tid; i < kRows * HD; i += kThreads) {
-        const int rr = row0 + i / HD;
-        q[i] = rr < rows ? bf(p.Q[((x.q0 + rr / p.g) * p.nq + h * p.g + rr % p.g) * HD + i % HD])
-                         : 0.0f;
-    }
-    float m = -INFINITY, l = 0.0f, acc[HD / 8];
-#pragma unroll
-    for (int i = 0; i < HD / 8; ++i) acc[i] = 0.0f;
-    for (int64_t t0 = 0; t0 < x.tokens; t0 += kTokens) {
-        __syncthreads();
-        for (int i = tid; i < kTokens * HD; i += kThreads) {
-            const int t = i / HD, d = i % HD;
-            const int64_t pos = t0 + t;
-            const int64_t id = pos < x.tokens ? p.table[x.e0 + pos / p.bs] : -1;
-            const bool ok = id >= 0 && id < p.max_blocks;
-            if (d == 0) {
-                good[t] = ok;
-                if (!ok && pos < x.tokens)
+
+    // Where this CTA's range of the list begins: a scan of the sequences' tiles.
+    {
+        const int each = ceil_div(p.num_seqs, kThreads);
+        const int s0 = min(static_cast<int>(threadIdx.x) * each, p.num_seqs);
+        const int s1 = min(s0 + each, p.num_seqs);
+        int64_t tiles = 0;
+        int items = 0;
+        for (int s = s0; s < s1; ++s) {
+            const SeqInfo x = load_seq(p, s);
+            const int nb = ceil_div(ceil_div(x.nodes, span), p.members);
+            tiles += seq_tiles<TILE>(p, x, span, nb);
+            items += nb * p.nkv;
+            if (blockIdx.x == 0) {
+                if (__ldg(p.q_offsets + s + 1) - x.q0 > p.max_q)
+                    raise_error(p.dev_status, p.lib_error, HSS_ERR_INVALID_ARGUMENT);
+                if (x.tokens < static_cast<int64_t>(x.ctx) + x.nodes)
                     raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
             }
-            const int64_t at = ((id * p.bs + pos % p.bs) * p.nkv + h) * HD + d;
-            k[t * (HD + 1) + d] = ok ? bf(p.K[at]) : 0.0f;
-            v[t * HD + d] = ok ? bf(p.V[at]) : 0.0f;
         }
-        __syncthreads();
-        float sc[kTokens / 8], top = m;
+        int64_t before = tiles;
+        int items_before = items;
 #pragma unroll
-        for (int i = 0; i < kTokens / 8; ++i) {
-            const int t = c + 8 * i;
-            float a = 0.0f;
-            for (int d = 0; d < HD; ++d) a += q[r * HD + d] * k[t * (HD + 1) + d];
-            const bool see = row < rows && good[t] && sees(p, x, node, t0 + t);
-            sc[i] = see ? a * p.scale : -INFINITY;
-            w[r * kTokens + t] = see ? 0.0f : -1.0f;
-            top = fmaxf(top, sc[i]);
-        }
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float shrink = expf(m - base);
-        float add = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kTokens / 8; ++i) {
-            const int t = c + 8 * i;
-            const float e = expf(sc[i] - base);
-            if (w[r * kTokens + t] >= 0.0f) {
-                w[r * kTokens + t] = e;
-                add += e;
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, before, m);
+            const int q = __shfl_up_sync(0xffffffffu, items_before, m);
+            if (lane >= m) {
+                before += o;
+                items_before += q;
             }
         }
+        if (lane == 31) {
+            bar.scan[warp] = before;
+            bar.scan_items[warp] = items_before;
+        }
+        tc_fence_before_sync();
+        __syncthreads();
+        tc_fence_after_sync();
+        before -= tiles;
+        items_before -= items;
+        int64_t total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) {
+                before += bar.scan[w];
+                items_before += bar.scan_items[w];
+            }
+            total += bar.scan[w];
+        }
+        const int64_t per = (total + p.groups - 1) / p.groups;
+        if (threadIdx.x == 0) {
+            bar.start.total = total;
+            bar.start.per = per;
+            if (blockIdx.x == 0) {
+                p.header[0] = total;
+                p.header[1] = per;
+            }
+        }
+        const int64_t f0 = blockIdx.x / p.members * per;
+        for (int s = s0; s < s1; ++s) {
+            const SeqInfo x = load_seq(p, s);
+            const int nb = ceil_div(ceil_div(x.nodes, span), p.members);
+            const int64_t n = seq_tiles<TILE>(p, x, span, nb);
+            if (blockIdx.x == 0) {
+                p.seq_tiles[s] = before;
+                p.seq_items[s] = items_before;
+            }
+            if (before <= f0 && f0 < before + n) {
+                int64_t o = f0 - before;
+                int b = 0, bt = batch_tiles<TILE>(p, x, span, 0);
+                while (o >= static_cast<int64_t>(bt) * p.nkv) {
+                    o -= static_cast<int64_t>(bt) * p.nkv;
+                    bt = batch_tiles<TILE>(p, x, span, ++b);
+                }
+                bar.start.s = s;
+                bar.start.b = b;
+                bar.start.h = static_cast<int>(o / bt);
+                bar.start.t = static_cast<int>(o % bt);
+                bar.start.item0 = items_before;
+            }
+            before += n;
+            items_before += nb * p.nkv;
+        }
+        __syncthreads();
+    }
+    const uint32_t tmem = bar.tmem;
+    volatile int* abort_flag = &bar.abort;
+    const int boxes = TILE / p.box;
+
+    Walk<TILE> walk;
+    walk.begin(p, bar.start, span);
+    Segment g;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- TMA producer
+        int64_t tile = 0;  // tiles issued by this CTA
+        int segs = 0;
+        bool ok = true;
+        const int my_box = lane % boxes, my_chunk = lane / boxes;
+        const bool loads = lane < boxes * kChunks;
+        // This lane's block id of tile t (its box), -1 past the sequence's tokens, -2 bad.
+        auto block_of = [&](const Segment& sg, int t) -> int {
+            const int pos = t * TILE + my_box * p.box;
+            if (!loads || pos >= sg.x.tokens) return -1;
+            const int id = __ldg(p.table + sg.x.e0 + pos / p.bs);
+            if (id < 0 || id >= p.max_blocks) {
+                raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
+                return -2;
+            }
+            return id;
+        };
+        auto load_tile = [&](const Segment& sg, const CUtensorMap* map, uint8_t* stage,
+                             uint64_t* full, int t, int id) {
+            if (lane == 0) mbar_arrive_expect_tx(full, C::kStageBytes);
+            __syncwarp();
+            if (loads) {
+                const int pos = t * TILE + my_box * p.box;
+                // an id outside the cache reads as zeros
+                tma_load_4d(stage + my_chunk * (TILE * 128) + my_box * (p.box * 128), map, full,
+                            my_chunk * 64, sg.h, pos % p.bs,
+                            id < 0 ? static_cast<int>(p.max_blocks) : id);
+            }
+            __syncwarp();
+        };
+        auto wait = [&](uint64_t* b, uint32_t parity) {
+            const bool got = mbar_wait(b, parity) && *abort_flag == 0;
+            return __all_sync(0xffffffffu, got) != 0;
+        };
+        while (ok && walk.next(p, g)) {
+            if (g.n == 0) continue;
+            if (segs > 0 && !(ok = wait(&bar.q_empty, (segs - 1) & 1))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar.q_full, NQ * kChunks * 128 * p.g * p.nodes_tile);
+                for (int q = 0; q < NQ; ++q)
+                    for (int ch = 0; ch < kChunks; ++ch)
+                        tma_load_3d(sQ + q * (kRows * HD * 2) + ch * (kRows * 128), &map_q,
+                                    &bar.q_full, ch * 64, g.h * p.g,
+                                    g.x.q0 + (g.rt * NQ + q) * p.nodes_tile);
+            }
+            __syncwarp();
+            ++segs;
+            // K runs one tile ahead of V, the order in which the products take them.
+            int id = block_of(g, g.ta), id_v = 0;
+            for (int i = 0; i <= g.n; ++i) {
+                if (i < g.n) {
+                    const int64_t n = tile + i;
+                    const int st = static_cast<int>(n % SK);
+                    const int ahead = i + 1 < g.n ? block_of(g, g.ta + i + 1) : -1;
+                    if (!(ok = wait(&bar.k_empty[st], static_cast<uint32_t>((n / SK) & 1) ^ 1u)))
+                        break;
+                    // bad ids of the tile, as granules of 16 tokens
+                    uint32_t bad = __ballot_sync(0xffffffffu, id == -2);
+                    if (bad != 0) {
+                        uint32_t bits = 0;
+                        for (int k = 0; k < TILE / 16; ++k)
+                            bits |= ((bad >> (16 * k / p.box)) & 1u) << k;
+                        bad = bits;
+                    }
+                    if (lane == 0) bar.bad_ids[n % kMetaRing] = bad;
+                    load_tile(g, &map_k, sK + st * C::kStageBytes, &bar.k_full[st], g.ta + i, id);
+                    const int keep = id;
+                    id = ahead;
+                    if (i == 0) {
+                        id_v = keep;
+                        continue;
+                    }
+                    const int64_t m = n - 1;
+                    const int sv = static_cast<int>(m % SV);
+                    if (!(ok = wait(&bar.v_empty[sv], static_cast<uint32_t>((m / SV) & 1) ^ 1u)))
+                        break;
+                    load_tile(g, &map_v, sV + sv * C::kStageBytes, &bar.v_full[sv], g.ta + i - 1,
+                              id_v);
+                    id_v = keep;
+                } else {
+                    const int64_t m = tile + i - 1;
+                    const int sv = static_cast<int>(m % SV);
+                    if (!(ok = wait(&bar.v_empty[sv], static_cast<uint32_t>((m / SV) & 1) ^ 1u)))
+                        break;
+                    load_tile(g, &map_v, sV + sv * C::kStageBytes, &bar.v_full[sv], g.ta + i - 1,
+                              id_v);
+                }
+            }
+            tile += g.n;
+        }
+        if (!ok) {
+            if (lane == 0) raise_error(p.dev_status, p.lib_error, HSS_ERR_DEVICE_TIMEOUT);
+            *abort_flag = 1;
+            // Whatever copies are in flight end within this: each full barrier is given time to
+            // complete its current phase before the CTA may leave.
+            for (int i = 0; i < SK; ++i) {
+                (void)mbar_wait_for(&bar.k_full[i], 0, 1000000);
+                (void)mbar_wait_for(&bar.k_full[i], 1, 1000000);
+            }
+            for (int i = 0; i < SV; ++i) {
+                (void)mbar_wait_for(&bar.v_full[i], 0, 1000000);
+                (void)mbar_wait_for(&bar.v_full[i], 1, 1000000);
+            }
+            (void)mbar_wait_for(&bar.q_full, 0, 1000000);
+            (void)mbar_wait_for(&bar.q_full, 1, 1000000);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- products
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, TILE);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, HD) | (1u << 16);  // V: MN-major
+            const uint64_t dq = smem_desc_kmajor(smem_u32(sQ), 128);
+            const uint64_t dk = smem_desc_kmajor(smem_u32(sK), 128);
+            const uint64_t dv = smem_desc_mnmajor(smem_u32(sV), TILE * 128);
+            int64_t tile = 0;
+            uint32_t segs = 0, np[2] = {0, 0};
+            bool ok = true;
+            while (ok && walk.next(p, g)) {
+                if (g.n == 0) continue;
+                if (!(ok = mbar_wait(&bar.q_full, segs & 1) && *abort_flag == 0)) break;
+                ++segs;
+                const int jobs = NQ * g.n;
+                auto score = [&](int i) -> bool {
+                    const int64_t n = tile + (NQ == 2 ? i >> 1 : i);
+                    const int st = static_cast<int>(n % SK), b = i & 1;
+                    if (!mbar_wait(&bar.k_full[st], static_cast<uint32_t>((n / SK) & 1)) ||
+                        *abort_flag)
+                        return false;
+                    tc_fence_after_sync();
+                    const uint64_t a = dq + (NQ == 2 ? b * (kRows * HD * 2 >> 4) : 0);
+                    const uint64_t k = dk + static_cast<uint64_t>(st) * (C::kStageBytes >> 4);
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
-        l = l * shrink + add;
-        m = top;
+                    for (int s = 0; s < HD / 16; ++s)
+                        umma_bf16(tmem + b * TILE, a + (s >> 2) * (kRows * 128 >> 4) + 2 * (s & 3),
+                                  k + (s >> 2) * (TILE * 128 >> 4) + 2 * (s & 3), idesc_s, s > 0);
+                    umma_commit(&bar.s_full[b]);
+                    if (NQ == 1 || b == 1) umma_commit(&bar.k_empty[st]);
+                    if (i == jobs - 1) umma_commit(&bar.q_empty);
+                    return true;
+                };
+                ok = score(0) && (jobs < 2 || score(1));
+                for (int i = 0; i < jobs && ok; ++i) {
+                    const int64_t n = tile + (NQ == 2 ? i >> 1 : i);
+                    const int st = static_cast<int>(n % SV), b = i & 1, w = NG == 2 ? b : 0;
+                    ok = mbar_wait(&bar.p_full[b], np[b] & 1) &&
+                         mbar_wait(&bar.v_full[st], static_cast<uint32_t>((n / SV) & 1)) &&
+                         *abort_flag == 0;
+                    if (!ok) break;
+                    ++np[b];
+                    tc_fence_after_sync();
+                    const uint64_t v = dv + static_cast<uint64_t>(st) * (C::kStageBytes >> 4);
+                    const bool first = i < NG;
+#pragma unroll
+                    for (int s = 0; s < TILE / 16; ++s)
+                        umma_bf16_ts(tmem + 2 * TILE + w * HD, tmem + b * TILE + 8 * s,
+                                     v + s * (16 * 128 >> 4), idesc_o, !first || s > 0);
+                    umma_commit(&bar.o_done[w]);
+                    if (NQ == 1 || b == 1) umma_commit(&bar.v_empty[st]);
+                    if (i + 2 < jobs) ok = score(i + 2);
+                }
+                tile += g.n;
+            }
+            if (!ok) {
+                raise_error(p.dev_status, p.lib_error, HSS_ERR_DEVICE_TIMEOUT);
+                *abort_flag = 1;
+            }
+        }
         __syncwarp();
+    } else if (NG == 2 || warp < 6) {
+        // ---------------------------------------------------------------- softmax
+        const int w = (warp - 2) >> 2;
+        const int quarter = warp & 3;
+        const int row = quarter * 32 + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t o_cols = lanes + 2 * TILE + w * HD;
+        const int gt = ((warp - 2) & 3) * 32 + lane;  // thread of the group
+        int64_t tile = 0;
+        uint32_t segs = 0, ns[2] = {0, 0}, nv = 0, values = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t* b, uint32_t parity) {
+            const bool got = mbar_wait(b, parity) && *abort_flag == 0;
+            return __all_sync(0xffffffffu, got) != 0;
+        };
+        while (ok && walk.next(p, g)) {
+            const SeqInfo& x = g.x;
+            const int first = (g.rt * NQ + (NQ == 2 ? w : 0)) * p.nodes_tile;
+            const int live = min(max(x.nodes - first, 0), p.nodes_tile) * p.g;
+            const bool warp_live = quarter * 32 < live;
+            const int node = first + row / p.g;
+            float m = -INFINITY, l = 0.0f;
+            int done = 0;
+            const int jobs = NQ * g.n;
+            for (int i = NG == 2 ? w : 0; i < jobs; i += NG) {
+                const int b = i & 1, ti = NQ == 2 ? i >> 1 : i;
+                const int64_t n = tile + ti;
+                const int pos0 = (g.ta + ti) * TILE;
+                if (!(ok = wait(&bar.s_full[b], ns[b] & 1))) break;
+                ++ns[b];
+                tc_fence_after_sync();
+                const uint32_t bad = *(volatile uint32_t*)&bar.bad_ids[n % kMetaRing];
+                const bool special = pos0 + TILE > x.ctx || bad != 0 || p.pre != 1.0f;
+                if (pos0 + TILE > x.ctx) {
+                    // Values past the end become zero; so do a node's non-finite elements.
+                    const int sv = static_cast<int>(n % SV);
+                    if (!(ok = wait(&bar.v_full[sv], static_cast<uint32_t>((n / SV) & 1)))) break;
+                    uint8_t* stage = sV + sv * C::kStageBytes;
+                    bool found = false;
+                    constexpr int all = TILE * kChunks;
+                    for (int k = gt + (NQ == 2 ? w * 128 : 0); k < all; k += NQ == 2 ? 256 : 128) {
+                        const int r = k % TILE, ch = k / TILE;
+                        if (pos0 + r < x.ctx) continue;
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) acc[i] *= shrink;
-        for (int t = 0; t < kTokens; ++t) {
-            const float e = w[r * kTokens + t];
-            if (e < 0.0f) continue;
+                        for (int e = 0; e < 8; ++e) {
+                            uint4* at = reinterpret_cast<uint4*>(
+                                stage + ch * (TILE * 128) + swizzled_offset(r, 16 * e, 128));
+                            if (pos0 + r >= x.tokens) {
+                                *at = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
+                            uint4 v = *at;
+                            uint32_t* u = &v.x;
+                            bool hit = false;
 #pragma unroll
-            for (int i = 0; i < HD / 8; ++i) acc[i] += e * v[t * HD + c + 8 * i];
+                            for (int d = 0; d < 4; ++d) {
+                                if ((u[d] & 0x7F80u) == 0x7F80u) {
+                                    u[d] &= 0xFFFF0000u;
+                                    hit = true;
+                                }
+                                if ((u[d] & 0x7F800000u) == 0x7F800000u) {
+                                    u[d] &= 0x0000FFFFu;
+                                    hit = true;
+                                }
+                            }
+                            if (hit) {
+                                *at = v;
+                                found = true;
+                            }
+                        }
+                    }
+                    if (found) {
+                        *(volatile int*)&bar.bad_value[w][segs & 1] = static_cast<int>(segs);
+                        if (NQ == 2)
+                            *(volatile int*)&bar.bad_value[w ^ 1][segs & 1] = static_cast<int>(segs);
+                    }
+                    fence_proxy_async_smem();
+                    if (NQ == 2) {  // both groups read the tile: both wait until all of it is fit
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.values);
+                        if (!(ok = wait(&bar.values, values & 1))) break;
+                        ++values;
+                    }
+                }
+                if (warp_live) {
+                    const uint32_t s_cols = lanes + b * TILE;
+                    uint32_t seen[TILE / 32];  // visibility, where it has to be looked at
+                    float top = -INFINITY;
+                    if (!special) {
+                        float part[TILE / 32];
+#pragma unroll
+                        for (int k = 0; k < TILE / 32; ++k)
+                            part[k] = tmem_ldred_max<32>(s_cols + 32 * k);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < TILE / 32; ++k) {
+                            order_after_wait(part[k]);
+                            top = fmaxf(top, part[k]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < TILE / 32; ++k) {
+                            uint32_t bits = row < live ? visible32(p, x, node, pos0 + 32 * k) : 0u;
+                            if ((bad >> (2 * k)) & 1) bits &= 0xFFFF0000u;
+                            if ((bad >> (2 * k)) & 2) bits &= 0x0000FFFFu;
+                            seen[k] = bits;
+                            uint32_t v[32];
+                            tmem_ld_32x32b_x32(s_cols + 32 * k, v);
+                            tmem_ld_wait_for(v);
+#pragma unroll
+                            for (int d = 0; d < 32; ++d)
+                                if ((bits >> d) & 1)
+                                    top = fmaxf(top, __uint_as_float(v[d]) * p.pre);
+                        }
+                    }
+                    top *= p.c;
+                    const bool grow = top > m + kLazy || m == -INFINITY;
+                    const float m_new = grow ? fmaxf(top, m) : m;
+                    if (__any_sync(0xffffffffu, grow && done > 0)) {
+                        if (!(ok = wait(&bar.o_done[w], (nv - 1) & 1))) break;
+                        tc_fence_after_sync();
+                        const float shrink =
+                            grow ? (m == -INFINITY ? 0.0f : ex2(m - m_new)) : 1.0f;
+                        l *= shrink;
+#pragma unroll
+                        for (int k = 0; k < HD; k += 32) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(o_cols + k, o);
+                            tmem_ld_wait_for(o);
+#pragma unroll
+                            for (int d = 0; d < 32; ++d)
+                                o[d] = __float_as_uint(__uint_as_float(o[d]) * shrink);
+                            tmem_st_32x32b_x32(o_cols + k, o);
+                        }
+                    }
+                    m = m_new;
+                    const float base = m == -INFINITY ? 0.0f : -m;
+                    float* sums = nullptr;
+                    if (p.sums != nullptr && row < p.rowcap) {
+                        const int64_t at =
+                            ((g.f + ti) * p.members + walk.member) * NQ + (NQ == 2 ? w : 0);
+                        sums = p.sums + at * (TILE / 16) * p.rowcap + row;
+                        p.sums_m[at * p.rowcap + row] = base;
+                    }
+                    // 32 scores at a time, the next 32 on their way meanwhile; their weights
+                    // take the place of scores that have been read.
+                    uint32_t v[2][32], packed[32];
+                    tmem_ld_32x32b_x32(s_cols, v[0]);
+#pragma unroll
+                    for (int k = 0; k < TILE / 32; ++k) {
+                        uint32_t* u = v[k & 1];
+                        tmem_ld_wait_for(u);
+                        if (k + 1 < TILE / 32)
+                            tmem_ld_32x32b_x32(s_cols + 32 * (k + 1), v[(k + 1) & 1]);
+                        if (special) {
+#pragma unroll
+                            for (int d = 0; d < 32; ++d)
+                                u[d] = (seen[k] >> d) & 1
+                                           ? __float_as_uint(__uint_as_float(u[d]) * p.pre)
+                                           : 0xFF800000u;
+                        }
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            float sum = 0.0f;
+#pragma unroll
+                            for (int d = 16 * q; d < 16 * q + 16; d += 2) {
+                                const float e0 = ex2(fmaf(__uint_as_float(u[d]), p.c, base));
+                                const float e1 = ex2(fmaf(__uint_as_float(u[d + 1]), p.c, base));
+                                sum += e0 + e1;
+                                packed[(k & 1) * 16 + d / 2] = pack_bf16x2(e0, e1);
+                            }
+                            l += sum;
+                            if (sums != nullptr) sums[(2 * k + q) * p.rowcap] = sum;
+                        }
+                        if (k & 1) tmem_st_32x32b_x32(s_cols + 16 * (k - 1), packed);
+                    }
+                    tmem_st_wait();
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[b]);
+                ++done;
+                ++nv;
+            }
+            if (!ok) break;
+            // What this piece of the sequence came to.
+            if (g.rows && warp_live) {
+                const int64_t slot =
+                    (static_cast<int64_t>(g.item + blockIdx.x / p.members) * p.members +
+                     walk.member) * 2 + w;
+                if (done > 0) {
+                    // (one group: the last product's scores may have been issued before the
+                    // product before it, so that one is waited for too)
+                    if (NG == 1 && done > 1 && !(ok = wait(&bar.o_done[w], nv & 1))) break;
+                    if (!(ok = wait(&bar.o_done[w], (nv - 1) & 1))) break;
+                    tc_fence_after_sync();
+                    float* to = p.part_o + (slot * p.rowcap + row) * HD;
+#pragma unroll
+                    for (int k = 0; k < HD; k += 32) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(o_cols + k, o);
+                        tmem_ld_wait_for(o);
+                        if (row < live) {
+#pragma unroll
+                            for (int d = 0; d < 32; d += 4)
+                                *reinterpret_cast<uint4*>(to + k + d) =
+                                    make_uint4(o[d], o[d + 1], o[d + 2], o[d + 3]);
+                        }
+                    }
+                    tc_fence_before_sync();
+                }
+                if (row < live) p.part_ml[slot * p.rowcap + row] = make_float2(m, l);
+                if (row == 0)
+                    p.part_bad[slot] = done > 0 && *(volatile int*)&bar.bad_value[w][segs & 1] ==
+                                                       static_cast<int>(segs);
+            }
+            if (g.n > 0) ++segs;
+            tile += g.n;
+        }
+        if (!ok) {
+            if (lane == 0) raise_error(p.dev_status, p.lib_error, HSS_ERR_DEVICE_TIMEOUT);
+            *abort_flag = 1;
         }
     }
-    if (row < rows) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t* o = p.out + ((x.q0 + node) * p.nq + head) * HD;
-#pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
-            const __nv_bfloat16 y = __float2bfloat16(acc[i] * inv);
-            o[c + 8 * i] = __bfloat16_as_ushort(y);
-        }
-        if (c == 0) p.lse[(x.q0 + node) * p.nq + head] = l == 0.0f ? -INFINITY : m + logf(l);
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
     }
 }
 
-__global__ void __launch_bounds__(kThreads) weights_kernel(const AttendParams p, int hd) {
-    __shared__ float part[kThreads / 32];
+// The list position of (batch, head) of a sequence and its length in tiles.
+template <int TILE>
+__device__ __forceinline__ void item_range(const AttendParams& p, const SeqInfo& x, int span,
+                                           int64_t seq0, int b, int h, int64_t& f, int& n) {
+    f = seq0;
+    if (p.mask != nullptr) {
+        n = batch_tiles<TILE>(p, x, span, b);
+        f += static_cast<int64_t>(b) * p.nkv * n;
+    } else {
+        for (int k = 0; k < b; ++k)
+            f += static_cast<int64_t>(p.nkv) * batch_tiles<TILE>(p, x, span, k);
+        n = batch_tiles<TILE>(p, x, span, b);
+    }
+    f += static_cast<int64_t>(h) * n;
+}
+
+// Joins the pieces of every row: one warp per row at a time, a CTA per (sequence, row tile,
+// head).
+template <int HD, int NQ>
+__global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row_tiles) {
+    using C = Cfg<HD, NQ>;
+    constexpr int TILE = C::kTile;
+    constexpr int kEach = HD / 32;  // elements of a row per lane, in pairs
+    const int span = NQ * p.nodes_tile;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t e = blockIdx.x;
+    const int rt = blockIdx.x % row_tiles;
+    const int h = blockIdx.x / row_tiles % p.nkv;
+    const int s = blockIdx.x / row_tiles / p.nkv;
+    const SeqInfo x = load_seq(p, s);
+    const int rows = min(max(x.nodes - rt * span, 0), span) * p.g;
+    if (rows == 0) return;
+    const int b = rt / p.members, member = rt % p.members;
+    int64_t f;
+    int n;
+    item_range<TILE>(p, x, span, p.seq_tiles[s], b, h, f, n);
+    const int64_t per = p.header[1];
+    const int64_t item = p.seq_items[s] + b * p.nkv + h;
+    const int64_t g0 = n > 0 ? f / per : 0, g1 = n > 0 ? (f + n - 1) / per : -1;
+    const int pieces = static_cast<int>(g1 - g0 + 1) * (NQ == 1 ? C::kGroups : 1);
+    for (int r = warp; r < rows; r += 8) {
+        const int node = rt * span + r / p.g, head = h * p.g + r % p.g;
+        const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
+        const int lr = r - qt * p.nodes_tile * p.g;
+        // piece k of the row -> slot
+        auto slot_of = [&](int k) -> int64_t {
+            const int grp = NQ == 1 && C::kGroups == 2 ? k >> 1 : k;
+            const int w = NQ == 2 ? qt : (C::kGroups == 2 ? k & 1 : 0);
+            return ((item + g0 + grp) * p.members + member) * 2 + w;
+        };
+        float top = -INFINITY;
+        int bad = 0;
+        for (int k = lane; k < pieces; k += 32) {
+            const int64_t sl = slot_of(k);
+            const float2 ml = p.part_ml[sl * p.rowcap + lr];
+            if (ml.y != 0.0f) top = fmaxf(top, ml.x);
+            bad |= p.part_bad[sl];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        bad = __any_sync(0xffffffffu, bad);
+        const float base = top == -INFINITY ? 0.0f : top;
+        float l = 0.0f, acc[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) acc[i] = 0.0f;
+        for (int k0 = 0; k0 < pieces; k0 += 32) {
+            float wt = 0.0f;
+            if (k0 + lane < pieces) {
+                const float2 ml = p.part_ml[slot_of(k0 + lane) * p.rowcap + lr];
+                wt = ml.y != 0.0f ? exp2f(ml.x - base) : 0.0f;
+                l += ml.y != 0.0f ? wt * ml.y : 0.0f;
+            }
+            const int here = min(32, pieces - k0);
+#pragma unroll 4
+            for (int k = 0; k < here; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, wt, k);
+                if (wk == 0.0f) continue;
+                const float2* o = reinterpret_cast<const float2*>(
+                    p.part_o + (slot_of(k0 + k) * p.rowcap + lr) * HD);
+#pragma unroll
+                for (int i = 0; i < kEach / 2; ++i) {
+                    const float2 v = o[lane + 32 * i];
+                    acc[2 * i] += wk * v.x;
+                    acc[2 * i + 1] += wk * v.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (bad) {
+            // Non-finite values of the nodes this row sees.
+            for (int j = 0; j < x.nodes; ++j) {
+                if (x.ctx + j >= x.tokens) break;
+                if (!((node_word(p, x, node, j >> 6) >> (j & 63)) & 1)) continue;
+                const int pos = x.ctx + j;
+                const int64_t id = p.table[x.e0 + pos / p.bs];
+                if (id < 0 || id >= p.max_blocks) continue;
+                const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                    p.V + ((id * p.bs + pos % p.bs) * p.nkv + h) * HD);
+#pragma unroll
+                for (int i = 0; i < kEach / 2; ++i) {
+                    const uint32_t u = v[lane + 32 * i];
+                    const float lo = __uint_as_float(u << 16);
+                    const float hi = __uint_as_float(u & 0xFFFF0000u);
+                    if (!isfinite(lo)) acc[2 * i] += lo;
+                    if (!isfinite(hi)) acc[2 * i + 1] += hi;
+                }
+            }
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t at = (static_cast<int64_t>(x.q0) + node) * p.nq + head;
+        uint32_t* to = reinterpret_cast<uint32_t*>(p.out + at * HD);
+#pragma unroll
+        for (int i = 0; i < kEach / 2; ++i)
+            to[lane + 32 * i] = l == 0.0f ? 0u : pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+        if (lane == 0) {
+            const float lse2 = l == 0.0f ? -INFINITY : base + log2f(l);
+            if (p.lse != nullptr) p.lse[at] = lse2 * 0.693147180559945309f;
+            if (p.sums != nullptr)
+                p.row_lse[((item * p.members + member) * NQ + qt) * p.rowcap + lr] = lse2;
+        }
+    }
+}
+
+// One warp per table entry: the sums of its granules over heads, row tiles and rows, each scaled
+// by its row's exp2(m - lse).
+template <int HD, int NQ>
+__global__ void __launch_bounds__(256) weights_kernel(const AttendParams p) {
+    using C = Cfg<HD, NQ>;
+    constexpr int TILE = C::kTile, kGran = TILE / 16;
+    const int span = NQ * p.nodes_tile;
+    const int lane = threadIdx.x & 31;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (e >= p.total_blocks) return;
     int lo = 0, hi = p.num_seqs;  // last s with seq_offsets[s] <= e
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (p.seq_offsets[mid] <= e) lo = mid; else hi = mid;
+        if (__ldg(p.seq_offsets + mid) <= e) lo = mid; else hi = mid;
     }
-    const Seq x = seq_of(p, lo);
-    const int64_t id = p.table[e], pos0 = (e - x.e0) * p.bs;
+    const SeqInfo x = load_seq(p, lo);
+    const int rts = ceil_div(x.nodes, span);
+    const int64_t seq0 = p.seq_tiles[lo];
+    const int item0 = p.seq_items[lo];
+    const int64_t pos0 = (e - x.e0) * p.bs;
     float sum = 0.0f;
-    if (id >= 0 && id < p.max_blocks) {
-        const int all = x.nodes * p.nq * p.bs;
-        for (int i = threadIdx.x; i < all; i += kThreads) {
-            const int t = i % p.bs, hq = i / p.bs % p.nq, node = i / p.bs / p.nq;
-            if (!sees(p, x, node, pos0 + t)) continue;
-            const uint16_t* q = p.Q + ((x.q0 + node) * p.nq + hq) * hd;
-            const uint16_t* k = p.K + ((id * p.bs + t) * p.nkv + hq / p.g) * hd;
-            float a = 0.0f;
-            for (int d = 0; d < hd; ++d) a += bf(q[d]) * bf(k[d]);
-            sum += expf(a * p.scale - p.lse[(x.q0 + node) * p.nq + hq]);
+    if (pos0 < x.tokens) {
+        const int left = static_cast<int>(min(static_cast<int64_t>(p.bs), x.tokens - pos0));
+        const int gr0 = static_cast<int>(pos0 / 16), grains = (left + 15) / 16;
+        for (int h = 0; h < p.nkv; ++h) {
+            for (int rt = 0; rt < rts; ++rt) {
+                const int b = rt / p.members, member = rt % p.members;
+                int64_t f;
+                int n;
+                item_range<TILE>(p, x, span, seq0, b, h, f, n);
+                const int mine = tiles_upto<TILE>(p, x, min(x.nodes, (rt + 1) * span));
+                const int rows = min(x.nodes - rt * span, span) * p.g;
+                const int64_t unit = (static_cast<int64_t>(item0 + b * p.nkv + h) * p.members +
+                                      member) * NQ;
+                for (int i = lane; i < rows * grains; i += 32) {
+                    const int r = i % rows, gr = gr0 + i / rows;
+                    const int t = gr / kGran;
+                    if (t >= mine) continue;
+                    const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
+                    const int lr = r - qt * p.nodes_tile * p.g;
+                    const int64_t at = ((f + t) * p.members + member) * NQ + qt;
+                    const float lse = p.row_lse[(unit + qt) * p.rowcap + lr];
+                    if (lse == -INFINITY) continue;
+                    const float part = p.sums[(at * kGran + gr % kGran) * p.rowcap + lr];
+                    if (part == 0.0f) continue;  // (m may then be anything)
+                    sum += part * exp2f(-p.sums_m[at * p.rowcap + lr] - lse);
+                }
+            }
         }
     }
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kThreads / 32; ++i) sum += part[i];
-        const float old = p.weights_in != nullptr ? p.weights_in[e] * p.decay : 0.0f;
-        p.weights_out[e] = old + sum;
-    }
+    if (lane == 0)
+        p.weights_out[e] = (p.weights_in != nullptr ? p.weights_in[e] * p.decay : 0.0f) + sum;
 }
 
-template <int HD>
-cudaError_t launch(const AttendParams& p, unsigned grid, cudaStream_t stream) {
-    const int smem = (kRows * HD + kTokens * (HD + 1) + kTokens * HD + kRows * kTokens + kTokens) * 4;
-    const cudaError_t e = cudaFuncSetAttribute(
-        attend_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(attend_kernel<HD>, dim3(grid), dim3(kThreads), smem, stream, p);
+// ------------------------------------------------------------------------------------- host
+
+// How a call is cut up; everything the workspace depends on.
+struct Plan {
+    int nq_tiles;    // row tiles per CTA: 1 or 2
+    int nodes_tile;  // nodes per row tile
+    int row_tiles;   // row tiles (or pairs) of the largest tree
+    int members, groups;
+    int rowcap;
+    int tile;
+    int64_t slots, tiles, units;
+    size_t header, seq_tiles, seq_items, part_o, part_ml, part_bad, row_lse, sums, sums_m, bytes;
+};
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total_blocks,
+               bool with_weights) {
+    Plan p;
+    const int g = d.num_q_heads / d.num_kv_heads;
+    p.nodes_tile = kRows / g;
+    p.tile = d.head_dim <= 128 ? 128 : 64;
+    p.nq_tiles = max_q > p.nodes_tile && d.head_dim < 256 ? 2 : 1;
+    const int span = p.nq_tiles * p.nodes_tile;
+    p.row_tiles = std::max(1, (max_q + span - 1) / span);
+    // Members of a group: row tiles in step.  The choice that leaves the fewest CTAs idle (in
+    // groups that do not fill the GPU, in a last batch that is not full), larger on a tie.
+    double best = -1.0;
+    p.members = 1;
+    for (int r = 1; r <= std::min(p.row_tiles, 19); ++r) {
+        if (p.row_tiles >= 4 && r < 4) continue;
+        const int batches = (p.row_tiles + r - 1) / r;
+        const double use = static_cast<double>(kCtas / r * r) / kCtas *
+                           (static_cast<double>(p.row_tiles) / (batches * r));
+        if (use >= best) {
+            best = use;
+            p.members = r;
+        }
+    }
+    p.groups = std::max(1, kCtas / p.members);
+    p.rowcap = std::min(kRows, g * std::min(max_q, p.nodes_tile));
+    const int64_t batches = (p.row_tiles + p.members - 1) / p.members;
+    const int64_t items = batches * d.num_kv_heads * num_seqs;
+    p.units = items * p.members * p.nq_tiles;
+    p.slots = (items + p.groups) * p.members * 2;
+    p.tiles = batches * d.num_kv_heads * (total_blocks * d.block_size / p.tile + num_seqs);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += up256(bytes);
+        return here;
+    };
+    p.header = take(16);
+    p.seq_tiles = take(static_cast<size_t>(num_seqs) * 8);
+    p.seq_items = take(static_cast<size_t>(num_seqs) * 4);
+    p.part_bad = take(static_cast<size_t>(p.slots) * 4);
+    p.part_ml = take(static_cast<size_t>(p.slots) * p.rowcap * 8);
+    p.part_o = take(static_cast<size_t>(p.slots) * p.rowcap * d.head_dim * 4);
+    p.row_lse = p.sums = p.sums_m = 0;
+    if (with_weights) {
+        const size_t lanes = static_cast<size_t>(p.tiles) * p.members * p.nq_tiles * p.rowcap;
+        p.row_lse = take(static_cast<size_t>(p.units) * p.rowcap * 4);
+        p.sums_m = take(lanes * 4);
+        p.sums = take(lanes * (p.tile / 16) * 4);
+    }
+    p.bytes = at;
+    return p;
+}
+
+bool encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const uint16_t* base,
+            int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<uint16_t*>(base), dims,
+               strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+std::mutex g_attr_mu;
+bool g_attr_set[64][8] = {};
+
+template <int HD, int NQ>
+hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap& mq,
+                      const CUtensorMap& mk, const CUtensorMap& mv, int device, int which,
+                      bool rows, cudaStream_t stream) {
+    using C = Cfg<HD, NQ>;
+    {
+        std::lock_guard<std::mutex> lk(g_attr_mu);
+        if (!g_attr_set[device & 63][which]) {
+            if (cudaFuncSetAttribute(attend_kernel<HD, NQ>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     C::kSmemBytes) != cudaSuccess)
+                return HSS_ERR_CUDA;
+            g_attr_set[device & 63][which] = true;
+        }
+    }
+    if (launch_pdl(attend_kernel<HD, NQ>, dim3(plan.groups * plan.members), dim3(kThreads),
+                   C::kSmemBytes, stream, mq, mk, mv, p) != cudaSuccess)
+        return HSS_ERR_CUDA;
+    if (rows) {
+        const unsigned grid = static_cast<unsigned>(plan.row_tiles) * p.nkv * p.num_seqs;
+        if (launch_pdl(join_kernel<HD, NQ>, dim3(grid), dim3(256), 0, stream, p,
+                       plan.row_tiles) != cudaSuccess)
+            return HSS_ERR_CUDA;
+    }
+    if (p.weights_out != nullptr &&
+        launch_pdl(weights_kernel<HD, NQ>, dim3(static_cast<unsigned>((p.total_blocks + 7) / 8)),
+                   dim3(256), 0, stream, p) != cudaSuccess)
+        return HSS_ERR_CUDA;
+    return HSS_OK;
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(const hss_dims& d, int32_t num_seqs, int32_t max_q,
                               int64_t total_blocks, bool with_weights) {
-    (void)total_blocks;
-    (void)with_weights;
-    return (static_cast<size_t>(num_seqs) * max_q * d.num_q_heads * 4 + 255) / 256 * 256;
+    return make_plan(d, num_seqs, max_q, total_blocks, with_weights).bytes;
 }
 
 hss_status launch_attend(const AttendArgs& r, cudaStream_t stream) {
     const hss_attend_args& a = *r.a;
     const DeviceInfo* dev = current_device_info();
     if (dev == nullptr) return HSS_ERR_CUDA;
+    const hss_dims& d = a.dims;
+    const bool weigh = r.weights_out != nullptr;
+    const Plan plan = make_plan(d, a.num_seqs, a.max_q, a.total_blocks, weigh);
+    auto enc = tensor_map_encoder();
+    if (enc == nullptr) return HSS_ERR_CUDA;
     AttendParams p;
-    p.Q = r.Q;
-    p.K = r.K;
     p.V = r.V;
     p.out = r.out;
-    p.lse = r.lse != nullptr ? r.lse : static_cast<float*>(a.workspace);
+    p.lse = r.lse;
     p.weights_in = r.weights_in;
     p.weights_out = r.weights_out;
     p.q_offsets = a.q_offsets;
@@ -236,35 +1139,77 @@ hss_status launch_attend(const AttendArgs& r, cudaStream_t stream) {
     p.table = a.block_table;
     p.seq_offsets = a.seq_offsets;
     p.ctx_len = a.ctx_len;
-    p.max_blocks = a.dims.max_blocks;
+    p.max_blocks = d.max_blocks;
     p.total_blocks = a.total_blocks;
     p.mask_words = a.mask_words;
     p.num_seqs = a.num_seqs;
     p.max_q = a.max_q;
-    p.nq = a.dims.num_q_heads;
-    p.nkv = a.dims.num_kv_heads;
+    p.nq = d.num_q_heads;
+    p.nkv = d.num_kv_heads;
     p.g = p.nq / p.nkv;
-    p.bs = a.dims.block_size;
-    p.scale = a.scale;
+    p.bs = d.block_size;
+    p.box = std::min(d.block_size & -d.block_size, plan.tile);
+    p.nodes_tile = plan.nodes_tile;
+    p.members = plan.members;
+    p.groups = plan.groups;
+    p.rowcap = plan.rowcap;
+    p.head_dim = d.head_dim;
+    p.c = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.44269504088896340736f;
+    p.pre = a.scale == 0.0f ? 0.0f : (a.scale < 0.0f ? -1.0f : 1.0f);
     p.decay = a.decay;
     p.dev_status = a.dev_status;
     p.lib_error = dev->error_word;
-    const int64_t tiles = (static_cast<int64_t>(a.max_q) * p.g + kRows - 1) / kRows;
-    const int64_t grid = tiles * p.nkv * a.num_seqs;
-    if (grid > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
-    if (a.total_q > 0) {
-        const unsigned n = static_cast<unsigned>(grid);
-        const cudaError_t e = a.dims.head_dim == 64    ? launch<64>(p, n, stream)
-                              : a.dims.head_dim == 128 ? launch<128>(p, n, stream)
-                              : a.dims.head_dim == 192 ? launch<192>(p, n, stream)
-                                                       : launch<256>(p, n, stream);
-        if (e != cudaSuccess) return HSS_ERR_CUDA;
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    p.header = reinterpret_cast<int64_t*>(ws + plan.header);
+    p.seq_tiles = reinterpret_cast<int64_t*>(ws + plan.seq_tiles);
+    p.seq_items = reinterpret_cast<int32_t*>(ws + plan.seq_items);
+    p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
+    p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
+    p.part_bad = reinterpret_cast<int32_t*>(ws + plan.part_bad);
+    p.row_lse = weigh ? reinterpret_cast<float*>(ws + plan.row_lse) : nullptr;
+    p.sums = weigh ? reinterpret_cast<float*>(ws + plan.sums) : nullptr;
+    p.sums_m = weigh ? reinterpret_cast<float*>(ws + plan.sums_m) : nullptr;
+    const bool rows = a.total_q > 0;
+    if (static_cast<int64_t>(plan.row_tiles) * p.nkv * p.num_seqs > 0x7FFFFFFF)
+        return HSS_ERR_INVALID_ARGUMENT;
+
+    // Without rows nothing is loaded, but the maps have to be well formed.
+    CUtensorMap mq, mk, mv;
+    const uint16_t* some = reinterpret_cast<const uint16_t*>(a.workspace);
+    const cuuint64_t hd = d.head_dim;
+    {
+        const cuuint64_t dims[3] = {hd, static_cast<cuuint64_t>(p.nq),
+                                    static_cast<cuuint64_t>(std::max<int64_t>(a.total_q, 1))};
+        const cuuint64_t strides[2] = {hd * 2, hd * 2 * p.nq};
+        const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.g),
+                                   static_cast<cuuint32_t>(p.nodes_tile)};
+        if (!encode(enc, &mq, rows ? r.Q : some, 3, dims, strides, box)) return HSS_ERR_CUDA;
     }
-    if (r.weights_out != nullptr &&
-        launch_pdl(weights_kernel, dim3(static_cast<unsigned>(a.total_blocks)), dim3(kThreads), 0,
-                   stream, p, a.dims.head_dim) != cudaSuccess)
-        return HSS_ERR_CUDA;
-    return HSS_OK;
+    {
+        const cuuint64_t dims[4] = {hd, static_cast<cuuint64_t>(p.nkv),
+                                    static_cast<cuuint64_t>(p.bs),
+                                    static_cast<cuuint64_t>(d.max_blocks)};
+        const cuuint64_t token = hd * 2 * p.nkv;
+        const cuuint64_t strides[3] = {hd * 2, token, token * p.bs};
+        const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(p.box), 1};
+        if (!encode(enc, &mk, rows ? r.K : some, 4, dims, strides, box) ||
+            !encode(enc, &mv, rows ? r.V : some, 4, dims, strides, box))
+            return HSS_ERR_CUDA;
+    }
+    const int dv = dev->device;
+    if (plan.nq_tiles == 2) {
+        switch (d.head_dim) {
+            case 64: return launch_all<64, 2>(p, plan, mq, mk, mv, dv, 0, rows, stream);
+            case 128: return launch_all<128, 2>(p, plan, mq, mk, mv, dv, 1, rows, stream);
+            default: return launch_all<192, 2>(p, plan, mq, mk, mv, dv, 2, rows, stream);
+        }
+    }
+    switch (d.head_dim) {
+        case 64: return launch_all<64, 1>(p, plan, mq, mk, mv, dv, 3, rows, stream);
+        case 128: return launch_all<128, 1>(p, plan, mq, mk, mv, dv, 4, rows, stream);
+        case 192: return launch_all<192, 1>(p, plan, mq, mk, mv, dv, 5, rows, stream);
+        default: return launch_all<256, 1>(p, plan, mq, mk, mv, dv, 6, rows, stream);
+    }
 }
 
 }  // namespace hss
