@@ -8,14 +8,15 @@
 // operand of the second product; K is its own K-major operand, V an MN-major one, both as TMA
 // leaves them.
 //
-// Roles of a CTA (10 warps, one CTA per SM):
-//   warp 0      looks up block ids, TMA: queries, then K and V tiles, two rings
-//   warp 1      TMEM allocation; one thread issues every product
-//   warps 2..9  two softmax groups of four warps.  With at most 128 rows the groups take a
-//               sequence's even and odd tiles, each with its own O, m and l (joined later, like
-//               any two pieces of a split sequence); with more rows they take two row tiles over
-//               the same K and V.  Either way one group's exponentials run under the other
-//               group's products.
+// Roles of a CTA (12 warps, one CTA per SM):
+//   warp 0       TMA of the queries and of K: looks up the block ids, one box per 16 or more tokens
+//   warp 1       TMA of V
+//   warps 2, 3   one thread each issues the products of one softmax group
+//   warps 4..11  two softmax groups of four warps.  With at most 128 rows the groups take a
+//                sequence's even and odd tiles, each with its own O, m and l (joined later, like
+//                any two pieces of a split sequence); with more rows they take two row tiles over
+//                the same K and V.  Either way one group's exponentials run under the other
+//                group's products.
 //
 // Split.  All (sequence, batch of row tiles, kv head, tile) units form one list, cut into equal
 // contiguous ranges: every SM gets the same number of tiles whatever the lengths are.  A range's
@@ -46,7 +47,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// Registers per thread: at launch, and after the loading and issuing warps have handed theirs to
+// the softmax warps, whose thread holds a row of scores.  128 * 88 + 256 * 208 = 384 * 168.
+constexpr int kRegsLaunch = 168, kRegsIssue = 88, kRegsSoftmax = 208;
 constexpr int kRows = 128;          // UMMA M
 constexpr int kMetaRing = 16;       // bad-id bits of the tiles in flight
 constexpr uint32_t kTmemCols = 512;
@@ -62,13 +66,18 @@ struct Cfg {
     static constexpr int kStageBytes = kTile * HD * 2;
     static constexpr int kQBytes = NQ * kRows * HD * 2;
     static constexpr int kBudget = 232448 - 1024 - 1024 - kQBytes;
-    static constexpr int kStages = kBudget / kStageBytes < 12 ? kBudget / kStageBytes : 12;
-    static constexpr int kStagesK = (kStages + 1) / 2;
-    static constexpr int kStagesV = kStages / 2;
-    static constexpr int kSmemBytes = 2048 + kQBytes + (kStagesK + kStagesV) * kStageBytes;
-    static_assert(kStagesV >= 2, "two tiles of V in flight");
+    // Two rings.  Groups on tiles of their own: one ring each, K and V in turn.  Otherwise one
+    // ring for K and one for V.  Whoever waits on a stage has then seen every earlier use of it
+    // complete, which a wait for a phase's parity takes for granted.
+    static constexpr bool kOwnTiles = NQ == 1 && kGroups == 2;
+    static constexpr int kMost = kBudget / kStageBytes < 12 ? kBudget / kStageBytes : 12;
+    static constexpr int kRing0 = kOwnTiles ? kMost / 2 : (kMost + 1) / 2;
+    static constexpr int kRing1 = kMost / 2;
+    static constexpr int kStages = kRing0 + kRing1;
+    static constexpr int kSmemBytes = 2048 + kQBytes + kStages * kStageBytes;
+    static_assert(kRing1 >= 2, "two operands in flight");
     static_assert(2 * kTile + kGroups * HD <= 512, "tensor memory");
-    static_assert(kStagesV + 3 <= kMetaRing, "tiles in flight");
+    static_assert(kRing0 + 2 <= kMetaRing, "tiles in flight");
 };
 
 struct AttendParams {
@@ -224,6 +233,87 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// A bounded wait whose waiting is cheap to leave: the clock and the abort flag are looked at only
+// after a run of failed tries.
+__device__ __forceinline__ bool wait_phase(uint64_t* b, uint32_t parity,
+                                           const volatile int* abort_flag) {
+    if (mbar_try_wait(b, parity)) return true;
+    uint64_t t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(b, parity)) return true;
+        if (*abort_flag) return false;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > kWaitLimitNs) return false;
+    }
+}
+
+// Where the K or V of a group's n-th tile (of all tiles, when the groups share them) goes.
+template <class C>
+__device__ __forceinline__ void place(bool values, int group, uint32_t n, int& stage,
+                                      uint32_t& parity) {
+    if constexpr (C::kOwnTiles) {
+        const uint32_t use = 2 * n + (values ? 1 : 0), round = use / C::kRing0;
+        stage = static_cast<int>(use - round * C::kRing0) + group * C::kRing0;
+        parity = round & 1;
+    } else if (!values) {
+        const uint32_t round = n / C::kRing0;
+        stage = static_cast<int>(n - round * C::kRing0);
+        parity = round & 1;
+    } else {
+        const uint32_t round = n / C::kRing1;
+        stage = static_cast<int>(n - round * C::kRing1) + C::kRing0;
+        parity = round & 1;
+    }
+}
+
+template <int REGS>
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// 32 columns of this thread's TMEM lane and their maximum (usable after the wait).
+__device__ __forceinline__ float tmem_ldred_values(uint32_t taddr, uint32_t* v) {
+    float m;
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+        "%32, [%33];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+          "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
+          "=r"(v[31]), "=f"(m)
+        : "r"(taddr));
+    return m;
+}
+
 // The wait for TMEM loads, with their uses held behind it.
 __device__ __forceinline__ void tmem_ld_wait_for(uint32_t* v) {
     tmem_ld_wait();
@@ -262,9 +352,9 @@ __device__ __forceinline__ uint32_t visible32(const AttendParams& p, const SeqIn
 }
 
 struct Barriers {
-    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+    uint64_t full[12], empty[12];
     uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], values;
-    uint32_t bad_ids[kMetaRing];  // per tile in flight: granules of 16 tokens with a bad id
+    uint32_t bad_ids[2][kMetaRing];  // [ring] per tile in flight: 16-token granules with a bad id
     int bad_value[2][2];          // [group][segment parity]: last segment with such a value
     int abort;
     uint32_t tmem;
@@ -280,34 +370,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap map_v, const AttendParams p) {
     using C = Cfg<HD, NQ>;
     constexpr int TILE = C::kTile, NG = C::kGroups;
-    constexpr int SK = C::kStagesK, SV = C::kStagesV;
     constexpr int kChunks = HD / 64;  // 128-byte columns of an operand row
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* sQ = smem;
-    uint8_t* sK = sQ + C::kQBytes;
-    uint8_t* sV = sK + SK * C::kStageBytes;
-    Barriers& bar = *reinterpret_cast<Barriers*>(sV + SV * C::kStageBytes);
+    uint8_t* sKV = sQ + C::kQBytes;
+    Barriers& bar = *reinterpret_cast<Barriers*>(sKV + C::kStages * C::kStageBytes);
     static_assert(sizeof(Barriers) <= 1024, "barrier block");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int span = NQ * p.nodes_tile;
 
-    if (warp == 1) {
+    if (warp == 2) {
         tmem_alloc(&bar.tmem, kTmemCols);
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < SK; ++i) {
-            mbar_init(&bar.k_full[i], 1);
-            mbar_init(&bar.k_empty[i], 1);
-        }
-        for (int i = 0; i < SV; ++i) {
-            mbar_init(&bar.v_full[i], 1);
-            mbar_init(&bar.v_empty[i], 1);
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.empty[i], NQ);
         }
         mbar_init(&bar.q_full, 1);
-        mbar_init(&bar.q_empty, 1);
+        mbar_init(&bar.q_empty, NG);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_full[i], 4);
@@ -412,192 +496,187 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int boxes = TILE / p.box;
 
     Walk<TILE> walk;
-    walk.begin(p, bar.start, span);
-    Segment g;
+    Segment g{};
+    // A role that gives up reports it and sends the others home.
+    auto give_up = [&]() {
+        if (lane == 0) raise_error(p.dev_status, p.lib_error, HSS_ERR_DEVICE_TIMEOUT);
+        *abort_flag = 1;
+    };
 
-    if (warp == 0) {
-        // ---------------------------------------------------------------- TMA producer
-        int64_t tile = 0;  // tiles issued by this CTA
-        int segs = 0;
-        bool ok = true;
-        const int my_box = lane % boxes, my_chunk = lane / boxes;
-        const bool loads = lane < boxes * kChunks;
-        // This lane's block id of tile t (its box), -1 past the sequence's tokens, -2 bad.
-        auto block_of = [&](const Segment& sg, int t) -> int {
-            const int pos = t * TILE + my_box * p.box;
-            if (!loads || pos >= sg.x.tokens) return -1;
-            const int id = __ldg(p.table + sg.x.e0 + pos / p.bs);
-            if (id < 0 || id >= p.max_blocks) {
-                raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
-                return -2;
-            }
-            return id;
-        };
-        auto load_tile = [&](const Segment& sg, const CUtensorMap* map, uint8_t* stage,
-                             uint64_t* full, int t, int id) {
-            if (lane == 0) mbar_arrive_expect_tx(full, C::kStageBytes);
-            __syncwarp();
-            if (loads) {
-                const int pos = t * TILE + my_box * p.box;
-                // an id outside the cache reads as zeros
-                tma_load_4d(stage + my_chunk * (TILE * 128) + my_box * (p.box * 128), map, full,
-                            my_chunk * 64, sg.h, pos % p.bs,
-                            id < 0 ? static_cast<int>(p.max_blocks) : id);
-            }
-            __syncwarp();
-        };
+    if (warp < 4) {
+        give_registers<kRegsIssue>();
+        walk.begin(p, bar.start, span);
         auto wait = [&](uint64_t* b, uint32_t parity) {
-            const bool got = mbar_wait(b, parity) && *abort_flag == 0;
-            return __all_sync(0xffffffffu, got) != 0;
+            return __all_sync(0xffffffffu, wait_phase(b, parity, abort_flag)) != 0;
         };
-        while (ok && walk.next(p, g)) {
-            if (g.n == 0) continue;
-            if (segs > 0 && !(ok = wait(&bar.q_empty, (segs - 1) & 1))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bar.q_full, NQ * kChunks * 128 * p.g * p.nodes_tile);
-                for (int q = 0; q < NQ; ++q)
-                    for (int ch = 0; ch < kChunks; ++ch)
-                        tma_load_3d(sQ + q * (kRows * HD * 2) + ch * (kRows * 128), &map_q,
-                                    &bar.q_full, ch * 64, g.h * p.g,
-                                    g.x.q0 + (g.rt * NQ + q) * p.nodes_tile);
-            }
-            __syncwarp();
-            ++segs;
-            // K runs one tile ahead of V, the order in which the products take them.
-            int id = block_of(g, g.ta), id_v = 0;
-            for (int i = 0; i <= g.n; ++i) {
-                if (i < g.n) {
-                    const int64_t n = tile + i;
-                    const int st = static_cast<int>(n % SK);
-                    const int ahead = i + 1 < g.n ? block_of(g, g.ta + i + 1) : -1;
-                    if (!(ok = wait(&bar.k_empty[st], static_cast<uint32_t>((n / SK) & 1) ^ 1u)))
-                        break;
-                    // bad ids of the tile, as granules of 16 tokens
-                    uint32_t bad = __ballot_sync(0xffffffffu, id == -2);
-                    if (bad != 0) {
-                        uint32_t bits = 0;
-                        for (int k = 0; k < TILE / 16; ++k)
-                            bits |= ((bad >> (16 * k / p.box)) & 1u) << k;
-                        bad = bits;
+        if (warp < 2) {
+            // ------------------------------------------------------------ TMA
+            // Own tiles: warp w brings K and V of group w's tiles.  Else warp 0 K and warp 1 V.
+            constexpr bool own = C::kOwnTiles;
+            const int first = own ? warp : 0, step = own ? 2 : 1;
+            const bool keys = own || warp == 0, values = own || warp == 1;
+            const bool loads = lane < boxes;  // a box per lane
+            uint32_t tile = 0, segs = 0;      // issued so far
+            bool ok = true;
+            // The block id under this lane's box of tile t, read ahead of its use (-1 past the
+            // sequence's tokens).
+            auto block_of = [&](int t) -> int {
+                const int pos = t * TILE + lane * p.box;
+                return loads && pos < g.x.tokens ? __ldg(p.table + g.x.e0 + pos / p.bs) : -1;
+            };
+            auto load = [&](bool v, int group_row) -> bool {
+                int st;
+                uint32_t par;
+                place<C>(v, first, tile, st, par);
+                if (!wait(&bar.empty[st], par ^ 1u)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(&bar.full[st], C::kStageBytes);
+                __syncwarp();
+                if (loads)
+                    tma_load_5d(sKV + st * C::kStageBytes + lane * p.box * (HD * 2),
+                                v ? &map_v : &map_k, &bar.full[st], 0, 0, 0, group_row, g.h);
+                __syncwarp();
+                return true;
+            };
+            while (ok && walk.next(p, g)) {
+                if (g.n == 0) continue;
+                if (warp == 0) {
+                    if (segs > 0 && !(ok = wait(&bar.q_empty, (segs - 1) & 1))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bar.q_full,
+                                              NQ * kChunks * 128 * p.g * p.nodes_tile);
+                        for (int q = 0; q < NQ; ++q)
+                            for (int ch = 0; ch < kChunks; ++ch)
+                                tma_load_3d(sQ + q * (kRows * HD * 2) + ch * (kRows * 128), &map_q,
+                                            &bar.q_full, ch * 64, g.h * p.g,
+                                            g.x.q0 + (g.rt * NQ + q) * p.nodes_tile);
                     }
-                    if (lane == 0) bar.bad_ids[n % kMetaRing] = bad;
-                    load_tile(g, &map_k, sK + st * C::kStageBytes, &bar.k_full[st], g.ta + i, id);
-                    const int keep = id;
+                    __syncwarp();
+                }
+                ++segs;
+                int id = first < g.n ? block_of(g.ta + first) : -1;
+                for (int i = first; i < g.n; i += step, ++tile) {
+                    const int ahead = i + step < g.n ? block_of(g.ta + i + step) : -1;
+                    const int pos = (g.ta + i) * TILE + lane * p.box;
+                    const bool good = id >= 0 && id < p.max_blocks;
+                    // groups of 8 tokens; past the cache's last one zeros are read
+                    const int group_row =
+                        static_cast<int>((good ? static_cast<int64_t>(id) * p.bs + pos % p.bs
+                                               : p.max_blocks * p.bs) / 8);
+                    if (keys) {
+                        // bad ids of the tile, as granules of 16 tokens
+                        const bool bad = loads && pos < g.x.tokens && !good;
+                        uint32_t bits = __ballot_sync(0xffffffffu, bad);
+                        if (bits != 0) {
+                            if (bad) raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
+                            uint32_t grains = 0;
+                            for (int k = 0; k < TILE / 16; ++k)
+                                grains |= ((bits >> (16 * k / p.box)) & 1u) << k;
+                            bits = grains;
+                        }
+                        // (its stage's barrier publishes it: written before the copies)
+                        if (lane == 0) bar.bad_ids[first][tile % kMetaRing] = bits;
+                        if (!(ok = load(false, group_row))) break;
+                    }
+                    if (values && !(ok = load(true, group_row))) break;
                     id = ahead;
-                    if (i == 0) {
-                        id_v = keep;
-                        continue;
-                    }
-                    const int64_t m = n - 1;
-                    const int sv = static_cast<int>(m % SV);
-                    if (!(ok = wait(&bar.v_empty[sv], static_cast<uint32_t>((m / SV) & 1) ^ 1u)))
-                        break;
-                    load_tile(g, &map_v, sV + sv * C::kStageBytes, &bar.v_full[sv], g.ta + i - 1,
-                              id_v);
-                    id_v = keep;
-                } else {
-                    const int64_t m = tile + i - 1;
-                    const int sv = static_cast<int>(m % SV);
-                    if (!(ok = wait(&bar.v_empty[sv], static_cast<uint32_t>((m / SV) & 1) ^ 1u)))
-                        break;
-                    load_tile(g, &map_v, sV + sv * C::kStageBytes, &bar.v_full[sv], g.ta + i - 1,
-                              id_v);
                 }
             }
-            tile += g.n;
-        }
-        if (!ok) {
-            if (lane == 0) raise_error(p.dev_status, p.lib_error, HSS_ERR_DEVICE_TIMEOUT);
-            *abort_flag = 1;
-            // Whatever copies are in flight end within this: each full barrier is given time to
-            // complete its current phase before the CTA may leave.
-            for (int i = 0; i < SK; ++i) {
-                (void)mbar_wait_for(&bar.k_full[i], 0, 1000000);
-                (void)mbar_wait_for(&bar.k_full[i], 1, 1000000);
+            if (!ok) give_up();
+            // Nobody leaves before the copies have landed and the products have released what
+            // they read: the last use of every stage (after a failure, when the count may be off,
+            // every stage gets time to finish the copy that it may be waiting for).
+            const int begin = own ? warp * C::kRing0 : (keys ? 0 : C::kRing0);
+            const uint32_t depth = keys ? C::kRing0 : C::kRing1;
+            const uint32_t uses = own ? 2 * tile : tile;
+            for (uint32_t i = 0; i < depth; ++i) {
+                if (!ok) {
+                    (void)mbar_wait_for(&bar.full[begin + i], 0, 1000000);
+                    (void)mbar_wait_for(&bar.full[begin + i], 1, 1000000);
+                } else if (uses > i) {
+                    const uint32_t par = ((uses - 1 - i) / depth) & 1;  // round of its last use
+                    (void)mbar_wait(&bar.full[begin + i], par);
+                    (void)mbar_wait(&bar.empty[begin + i], par);
+                }
             }
-            for (int i = 0; i < SV; ++i) {
-                (void)mbar_wait_for(&bar.v_full[i], 0, 1000000);
-                (void)mbar_wait_for(&bar.v_full[i], 1, 1000000);
+            if (warp == 0 && segs > 0) {
+                (void)mbar_wait_for(&bar.q_full, (segs - 1) & 1, ok ? kWaitLimitNs : 1000000);
+                if (ok) (void)mbar_wait(&bar.q_empty, (segs - 1) & 1);
             }
-            (void)mbar_wait_for(&bar.q_full, 0, 1000000);
-            (void)mbar_wait_for(&bar.q_full, 1, 1000000);
-        }
-    } else if (warp == 1) {
-        // ---------------------------------------------------------------- products
-        if (lane == 0) {
+        } else if (warp - 2 < NG && lane == 0) {
+            // ------------------------------------------------------------ products of group w
+            const int w = warp - 2;
+            constexpr int kBuffers = NG == 2 ? 1 : 2;  // score buffers of the group
             constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, TILE);
             constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, HD) | (1u << 16);  // V: MN-major
-            const uint64_t dq = smem_desc_kmajor(smem_u32(sQ), 128);
-            const uint64_t dk = smem_desc_kmajor(smem_u32(sK), 128);
-            const uint64_t dv = smem_desc_mnmajor(smem_u32(sV), TILE * 128);
-            int64_t tile = 0;
-            uint32_t segs = 0, np[2] = {0, 0};
+            const uint64_t dq = smem_desc_kmajor(smem_u32(sQ), 128) +
+                                (NQ == 2 ? w * (kRows * HD * 2 >> 4) : 0);
+            const uint64_t dk = smem_desc_128b(smem_u32(sKV), kChunks * 1024, 0);
+            const uint64_t dv = smem_desc_128b(smem_u32(sKV), kChunks * 1024, 1024);
+            const uint32_t d_o = tmem + 2 * TILE + w * HD;
+            uint32_t tile = 0, segs = 0, np[2] = {0, 0};
             bool ok = true;
             while (ok && walk.next(p, g)) {
                 if (g.n == 0) continue;
-                if (!(ok = mbar_wait(&bar.q_full, segs & 1) && *abort_flag == 0)) break;
+                if (!(ok = wait_phase(&bar.q_full, segs & 1, abort_flag))) break;
                 ++segs;
-                const int jobs = NQ * g.n;
-                auto score = [&](int i) -> bool {
-                    const int64_t n = tile + (NQ == 2 ? i >> 1 : i);
-                    const int st = static_cast<int>(n % SK), b = i & 1;
-                    if (!mbar_wait(&bar.k_full[st], static_cast<uint32_t>((n / SK) & 1)) ||
-                        *abort_flag)
-                        return false;
+                const int jobs = C::kOwnTiles ? (g.n - w + 1) / 2 : g.n;
+                if (jobs == 0) mbar_arrive(&bar.q_empty);
+                auto score = [&](int j) -> bool {
+                    int st;
+                    uint32_t par;
+                    place<C>(false, w, tile + j, st, par);
+                    const int b = NG == 2 ? w : j & 1;
+                    if (!wait_phase(&bar.full[st], par, abort_flag)) return false;
                     tc_fence_after_sync();
-                    const uint64_t a = dq + (NQ == 2 ? b * (kRows * HD * 2 >> 4) : 0);
-                    const uint64_t k = dk + static_cast<uint64_t>(st) * (C::kStageBytes >> 4);
+                    const uint64_t k = dk + static_cast<uint32_t>(st * (C::kStageBytes >> 4));
 #pragma unroll
                     for (int s = 0; s < HD / 16; ++s)
-                        umma_bf16(tmem + b * TILE, a + (s >> 2) * (kRows * 128 >> 4) + 2 * (s & 3),
-                                  k + (s >> 2) * (TILE * 128 >> 4) + 2 * (s & 3), idesc_s, s > 0);
+                        umma_bf16(tmem + b * TILE, dq + (s >> 2) * (kRows * 128 >> 4) + 2 * (s & 3),
+                                  k + (s >> 2) * (1024 >> 4) + 2 * (s & 3), idesc_s, s > 0);
                     umma_commit(&bar.s_full[b]);
-                    if (NQ == 1 || b == 1) umma_commit(&bar.k_empty[st]);
-                    if (i == jobs - 1) umma_commit(&bar.q_empty);
+                    umma_commit(&bar.empty[st]);
+                    if (j == jobs - 1) umma_commit(&bar.q_empty);
                     return true;
                 };
-                ok = score(0) && (jobs < 2 || score(1));
-                for (int i = 0; i < jobs && ok; ++i) {
-                    const int64_t n = tile + (NQ == 2 ? i >> 1 : i);
-                    const int st = static_cast<int>(n % SV), b = i & 1, w = NG == 2 ? b : 0;
-                    ok = mbar_wait(&bar.p_full[b], np[b] & 1) &&
-                         mbar_wait(&bar.v_full[st], static_cast<uint32_t>((n / SV) & 1)) &&
-                         *abort_flag == 0;
+                for (int j = 0; j < kBuffers && j < jobs && ok; ++j) ok = score(j);
+                for (int j = 0; j < jobs && ok; ++j) {
+                    int st;
+                    uint32_t par;
+                    place<C>(true, w, tile + j, st, par);
+                    const int b = NG == 2 ? w : j & 1;
+                    ok = wait_phase(&bar.full[st], par, abort_flag) &&
+                         wait_phase(&bar.p_full[b], np[b] & 1, abort_flag);
                     if (!ok) break;
                     ++np[b];
                     tc_fence_after_sync();
-                    const uint64_t v = dv + static_cast<uint64_t>(st) * (C::kStageBytes >> 4);
-                    const bool first = i < NG;
+                    const uint64_t v = dv + static_cast<uint32_t>(st * (C::kStageBytes >> 4));
 #pragma unroll
                     for (int s = 0; s < TILE / 16; ++s)
-                        umma_bf16_ts(tmem + 2 * TILE + w * HD, tmem + b * TILE + 8 * s,
-                                     v + s * (16 * 128 >> 4), idesc_o, !first || s > 0);
+                        umma_bf16_ts(d_o, tmem + b * TILE + 8 * s,
+                                     v + s * (2 * kChunks * 1024 >> 4), idesc_o, j > 0 || s > 0);
                     umma_commit(&bar.o_done[w]);
-                    if (NQ == 1 || b == 1) umma_commit(&bar.v_empty[st]);
-                    if (i + 2 < jobs) ok = score(i + 2);
+                    umma_commit(&bar.empty[st]);
+                    if (j + kBuffers < jobs) ok = score(j + kBuffers);
                 }
-                tile += g.n;
+                tile += jobs;
             }
-            if (!ok) {
-                raise_error(p.dev_status, p.lib_error, HSS_ERR_DEVICE_TIMEOUT);
-                *abort_flag = 1;
-            }
+            if (!ok) give_up();
         }
-        __syncwarp();
-    } else if (NG == 2 || warp < 6) {
+    } else {
+        take_registers<kRegsSoftmax>();
         // ---------------------------------------------------------------- softmax
-        const int w = (warp - 2) >> 2;
+        const int w = (warp - 4) >> 2;
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t o_cols = lanes + 2 * TILE + w * HD;
-        const int gt = ((warp - 2) & 3) * 32 + lane;  // thread of the group
-        int64_t tile = 0;
-        uint32_t segs = 0, ns[2] = {0, 0}, nv = 0, values = 0;
+        const int gt = quarter * 32 + lane;  // thread of the group
+        uint32_t tile = 0, segs = 0, ns[2] = {0, 0}, nv = 0, values = 0;
         bool ok = true;
+        walk.begin(p, bar.start, span);
+        if (w >= NG) walk.f = walk.f1;
         auto wait = [&](uint64_t* b, uint32_t parity) {
-            const bool got = mbar_wait(b, parity) && *abort_flag == 0;
-            return __all_sync(0xffffffffu, got) != 0;
+            return __all_sync(0xffffffffu, wait_phase(b, parity, abort_flag)) != 0;
         };
         while (ok && walk.next(p, g)) {
             const SeqInfo& x = g.x;
@@ -607,30 +686,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int node = first + row / p.g;
             float m = -INFINITY, l = 0.0f;
             int done = 0;
-            const int jobs = NQ * g.n;
-            for (int i = NG == 2 ? w : 0; i < jobs; i += NG) {
-                const int b = i & 1, ti = NQ == 2 ? i >> 1 : i;
-                const int64_t n = tile + ti;
+            const int64_t unit0 = (g.f * p.members + walk.member) * NQ + (NQ == 2 ? w : 0);
+            for (int ti = C::kOwnTiles ? w : 0; ti < g.n; ti += C::kOwnTiles ? 2 : 1) {
+                const int b = NG == 2 ? w : done & 1;
                 const int pos0 = (g.ta + ti) * TILE;
                 if (!(ok = wait(&bar.s_full[b], ns[b] & 1))) break;
                 ++ns[b];
                 tc_fence_after_sync();
-                const uint32_t bad = *(volatile uint32_t*)&bar.bad_ids[n % kMetaRing];
+                const uint32_t bad = *(volatile uint32_t*)
+                    &bar.bad_ids[C::kOwnTiles ? w : 0][(tile + done) % kMetaRing];
                 const bool special = pos0 + TILE > x.ctx || bad != 0 || p.pre != 1.0f;
                 if (pos0 + TILE > x.ctx) {
                     // Values past the end become zero; so do a node's non-finite elements.
-                    const int sv = static_cast<int>(n % SV);
-                    if (!(ok = wait(&bar.v_full[sv], static_cast<uint32_t>((n / SV) & 1)))) break;
-                    uint8_t* stage = sV + sv * C::kStageBytes;
+                    int sv;
+                    uint32_t par;
+                    place<C>(true, w, tile + done, sv, par);
+                    if (!(ok = wait(&bar.full[sv], par))) break;
+                    uint8_t* stage = sKV + sv * C::kStageBytes;
                     bool found = false;
                     constexpr int all = TILE * kChunks;
                     for (int k = gt + (NQ == 2 ? w * 128 : 0); k < all; k += NQ == 2 ? 256 : 128) {
                         const int r = k % TILE, ch = k / TILE;
                         if (pos0 + r < x.ctx) continue;
-#pragma unroll
+#pragma unroll 2
                         for (int e = 0; e < 8; ++e) {
                             uint4* at = reinterpret_cast<uint4*>(
-                                stage + ch * (TILE * 128) + swizzled_offset(r, 16 * e, 128));
+                                stage + ((r >> 3) * kChunks + ch) * 1024 +
+                                swizzled_offset(r & 7, 16 * e, 128));
                             if (pos0 + r >= x.tokens) {
                                 *at = make_uint4(0, 0, 0, 0);
                                 continue;
@@ -670,33 +752,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (warp_live) {
                     const uint32_t s_cols = lanes + b * TILE;
-                    uint32_t seen[TILE / 32];  // visibility, where it has to be looked at
-                    float top = -INFINITY;
-                    if (!special) {
-                        float part[TILE / 32];
+                    uint32_t v[TILE];
+                    float part[TILE / 32], top;
 #pragma unroll
-                        for (int k = 0; k < TILE / 32; ++k)
-                            part[k] = tmem_ldred_max<32>(s_cols + 32 * k);
-                        tmem_ld_wait();
+                    for (int k = 0; k < TILE / 32; ++k)
+                        part[k] = tmem_ldred_values(s_cols + 32 * k, v + 32 * k);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < TILE / 32; ++k) {
-                            order_after_wait(part[k]);
-                            top = fmaxf(top, part[k]);
-                        }
-                    } else {
+                    for (int k = 0; k < TILE / 32; ++k) order_after_wait(part[k]);
+#pragma unroll
+                    for (int k = 0; k < TILE; ++k) asm volatile("" : "+r"(v[k]));
+                    top = part[0];
+#pragma unroll
+                    for (int k = 1; k < TILE / 32; ++k) top = fmaxf(top, part[k]);
+                    if (special) {
+                        top = -INFINITY;
 #pragma unroll
                         for (int k = 0; k < TILE / 32; ++k) {
                             uint32_t bits = row < live ? visible32(p, x, node, pos0 + 32 * k) : 0u;
                             if ((bad >> (2 * k)) & 1) bits &= 0xFFFF0000u;
                             if ((bad >> (2 * k)) & 2) bits &= 0x0000FFFFu;
-                            seen[k] = bits;
-                            uint32_t v[32];
-                            tmem_ld_32x32b_x32(s_cols + 32 * k, v);
-                            tmem_ld_wait_for(v);
 #pragma unroll
-                            for (int d = 0; d < 32; ++d)
-                                if ((bits >> d) & 1)
-                                    top = fmaxf(top, __uint_as_float(v[d]) * p.pre);
+                            for (int d = 0; d < 32; ++d) {
+                                const float s = (bits >> d) & 1
+                                                    ? __uint_as_float(v[32 * k + d]) * p.pre
+                                                    : -INFINITY;
+                                v[32 * k + d] = __float_as_uint(s);
+                                top = fmaxf(top, s);
+                            }
                         }
                     }
                     top *= p.c;
@@ -723,42 +806,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float base = m == -INFINITY ? 0.0f : -m;
                     float* sums = nullptr;
                     if (p.sums != nullptr && row < p.rowcap) {
-                        const int64_t at =
-                            ((g.f + ti) * p.members + walk.member) * NQ + (NQ == 2 ? w : 0);
+                        const int64_t at = unit0 + static_cast<int64_t>(ti) * p.members * NQ;
                         sums = p.sums + at * (TILE / 16) * p.rowcap + row;
                         p.sums_m[at * p.rowcap + row] = base;
                     }
-                    // 32 scores at a time, the next 32 on their way meanwhile; their weights
-                    // take the place of scores that have been read.
-                    uint32_t v[2][32], packed[32];
-                    tmem_ld_32x32b_x32(s_cols, v[0]);
+                    const float2 c2 = make_float2(p.c, p.c), b2 = make_float2(base, base);
 #pragma unroll
-                    for (int k = 0; k < TILE / 32; ++k) {
-                        uint32_t* u = v[k & 1];
-                        tmem_ld_wait_for(u);
-                        if (k + 1 < TILE / 32)
-                            tmem_ld_32x32b_x32(s_cols + 32 * (k + 1), v[(k + 1) & 1]);
-                        if (special) {
+                    for (int k = 0; k < TILE; k += 64) {
+                        uint32_t packed[32];
 #pragma unroll
-                            for (int d = 0; d < 32; ++d)
-                                u[d] = (seen[k] >> d) & 1
-                                           ? __float_as_uint(__uint_as_float(u[d]) * p.pre)
-                                           : 0xFF800000u;
-                        }
+                        for (int q = 0; q < 4; ++q) {
+                            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            float sum = 0.0f;
-#pragma unroll
-                            for (int d = 16 * q; d < 16 * q + 16; d += 2) {
-                                const float e0 = ex2(fmaf(__uint_as_float(u[d]), p.c, base));
-                                const float e1 = ex2(fmaf(__uint_as_float(u[d + 1]), p.c, base));
-                                sum += e0 + e1;
-                                packed[(k & 1) * 16 + d / 2] = pack_bf16x2(e0, e1);
+                            for (int d = 0; d < 16; d += 2) {
+                                float2 e = make_float2(__uint_as_float(v[k + 16 * q + d]),
+                                                       __uint_as_float(v[k + 16 * q + d + 1]));
+                                e = fma2(e, c2, b2);
+                                e.x = ex2(e.x);
+                                e.y = ex2(e.y);
+                                sum = d == 0 ? e : add2(sum, e);
+                                packed[8 * q + d / 2] = pack_bf16x2(e.x, e.y);
                             }
-                            l += sum;
-                            if (sums != nullptr) sums[(2 * k + q) * p.rowcap] = sum;
+                            const float both = sum.x + sum.y;
+                            l += both;
+                            if (sums != nullptr) sums[(k / 16 + q) * p.rowcap] = both;
                         }
-                        if (k & 1) tmem_st_32x32b_x32(s_cols + 16 * (k - 1), packed);
+                        tmem_st_32x32b_x32(s_cols + k / 2, packed);
                     }
                     tmem_st_wait();
                 }
@@ -801,17 +874,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                        static_cast<int>(segs);
             }
             if (g.n > 0) ++segs;
-            tile += g.n;
+            tile += done;
         }
-        if (!ok) {
-            if (lane == 0) raise_error(p.dev_status, p.lib_error, HSS_ERR_DEVICE_TIMEOUT);
-            *abort_flag = 1;
-        }
+        if (!ok) give_up();
     }
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 2) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -1071,7 +1141,7 @@ Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total
 
 bool encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const uint16_t* base,
             int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<uint16_t*>(base), dims,
                strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1089,7 +1159,12 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
     {
         std::lock_guard<std::mutex> lk(g_attr_mu);
         if (!g_attr_set[device & 63][which]) {
-            if (cudaFuncSetAttribute(attend_kernel<HD, NQ>,
+            // The softmax warps wait for the registers that the others hand back: the kernel must
+            // have been launched with as many as the shares add up to.
+            cudaFuncAttributes attr;
+            if (cudaFuncGetAttributes(&attr, attend_kernel<HD, NQ>) != cudaSuccess ||
+                attr.numRegs < kRegsLaunch ||
+                cudaFuncSetAttribute(attend_kernel<HD, NQ>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      C::kSmemBytes) != cudaSuccess)
                 return HSS_ERR_CUDA;
@@ -1186,14 +1261,18 @@ hss_status launch_attend(const AttendArgs& r, cudaStream_t stream) {
         if (!encode(enc, &mq, rows ? r.Q : some, 3, dims, strides, box)) return HSS_ERR_CUDA;
     }
     {
-        const cuuint64_t dims[4] = {hd, static_cast<cuuint64_t>(p.nkv),
-                                    static_cast<cuuint64_t>(p.bs),
-                                    static_cast<cuuint64_t>(d.max_blocks)};
+        // 64 elements x 8 tokens x the head's 64-element columns x groups of 8 tokens x heads: a
+        // box of 16 or more tokens lands as 8-row atoms, a group's columns side by side, so that
+        // one copy brings whole rows and the atoms of an operand column stay evenly spaced.
         const cuuint64_t token = hd * 2 * p.nkv;
-        const cuuint64_t strides[3] = {hd * 2, token, token * p.bs};
-        const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(p.box), 1};
-        if (!encode(enc, &mk, rows ? r.K : some, 4, dims, strides, box) ||
-            !encode(enc, &mv, rows ? r.V : some, 4, dims, strides, box))
+        const cuuint64_t groups = static_cast<cuuint64_t>(d.max_blocks) * p.bs / 8;
+        if (groups > 0x7FFFFFFF) return HSS_ERR_UNSUPPORTED_SHAPE;
+        const cuuint64_t dims[5] = {64, 8, hd / 64, groups, static_cast<cuuint64_t>(p.nkv)};
+        const cuuint64_t strides[4] = {token, 128, token * 8, hd * 2};
+        const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(hd / 64),
+                                   static_cast<cuuint32_t>(p.box / 8), 1};
+        if (!encode(enc, &mk, rows ? r.K : some, 5, dims, strides, box) ||
+            !encode(enc, &mv, rows ? r.V : some, 5, dims, strides, box))
             return HSS_ERR_CUDA;
     }
     const int dv = dev->device;

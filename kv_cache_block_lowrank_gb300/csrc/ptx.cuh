@@ -155,12 +155,14 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
         : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
-                                            int32_t x, int32_t y, int32_t z, int32_t w) {
+__device__ __forceinline__ void tma_load_5d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t v,
+                                            int32_t w) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(v),
+        "r"(w)
         : "memory");
 }
 
@@ -361,14 +363,15 @@ __device__ __forceinline__ uint64_t smem_desc_kmajor(uint32_t saddr, uint32_t ro
     return d;
 }
 
-// The same for an MN-major operand with 128-byte swizzle: rows of 64 MN elements (128 bytes),
-// one row per K element, 8-row atoms 1024 bytes apart; the next 64 MN elements lie
-// `mn_stride` bytes on (the leading byte offset).
-__device__ __forceinline__ uint64_t smem_desc_mnmajor(uint32_t saddr, uint32_t mn_stride) {
+// The 128-byte swizzled layout with the 8-row atoms `atom_stride` bytes apart.  K-major: a row is
+// 64 K elements, and lead_stride is not used.  MN-major: a row is 64 MN elements, one row per K
+// element, and the next 64 MN elements lie lead_stride bytes on.
+__device__ __forceinline__ uint64_t smem_desc_128b(uint32_t saddr, uint32_t atom_stride,
+                                                   uint32_t lead_stride) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>((mn_stride & 0x3FFFFu) >> 4) << 16;
-    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>((lead_stride & 0x3FFFFu) >> 4) << 16;
+    d |= static_cast<uint64_t>((atom_stride & 0x3FFFFu) >> 4) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;
     return d;
