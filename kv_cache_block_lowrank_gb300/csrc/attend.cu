@@ -296,24 +296,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
-// 32 columns of this thread's TMEM lane and their maximum (usable after the wait).
-__device__ __forceinline__ float tmem_ldred_values(uint32_t taddr, uint32_t* v) {
-    float m;
-    asm volatile(
-        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
-        "%32, [%33];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
-          "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
-          "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
-          "=r"(v[31]), "=f"(m)
-        : "r"(taddr));
-    return m;
-}
-
 // The wait for TMEM loads, with their uses held behind it.
 __device__ __forceinline__ void tmem_ld_wait_for(uint32_t* v) {
     tmem_ld_wait();
@@ -353,7 +335,7 @@ __device__ __forceinline__ uint32_t visible32(const AttendParams& p, const SeqIn
 
 struct Barriers {
     uint64_t full[12], empty[12];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], values;
+    uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_done[2], values;
     uint32_t bad_ids[2][kMetaRing];  // [ring] per tile in flight: 16-token granules with a bad id
     int bad_value[2][2];          // [group][segment parity]: last segment with such a value
     int abort;
@@ -394,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bar.q_empty, NG);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.p_full[i][0], 4);
+            mbar_init(&bar.p_full[i][1], 4);
             mbar_init(&bar.o_done[i], 1);
             bar.bad_value[i][0] = bar.bad_value[i][1] = -1;
         }
@@ -606,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------------------ products of group w
             const int w = warp - 2;
             constexpr int kBuffers = NG == 2 ? 1 : 2;  // score buffers of the group
+            constexpr int kHalves = TILE / 64;
             constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, TILE);
             constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, HD) | (1u << 16);  // V: MN-major
             const uint64_t dq = smem_desc_kmajor(smem_u32(sQ), 128) +
@@ -621,42 +605,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++segs;
                 const int jobs = C::kOwnTiles ? (g.n - w + 1) / 2 : g.n;
                 if (jobs == 0) mbar_arrive(&bar.q_empty);
-                auto score = [&](int j) -> bool {
+                auto arrived = [&](bool v, int j) -> int {  // the stage, once its copy is there
                     int st;
                     uint32_t par;
-                    place<C>(false, w, tile + j, st, par);
-                    const int b = NG == 2 ? w : j & 1;
-                    if (!wait_phase(&bar.full[st], par, abort_flag)) return false;
-                    tc_fence_after_sync();
+                    place<C>(v, w, tile + j, st, par);
+                    if (!wait_phase(&bar.full[st], par, abort_flag)) ok = false;
+                    return st;
+                };
+                auto score = [&](int j, int st) {
                     const uint64_t k = dk + static_cast<uint32_t>(st * (C::kStageBytes >> 4));
+                    const uint32_t d_s = tmem + (NG == 2 ? w : j & 1) * TILE;
 #pragma unroll
                     for (int s = 0; s < HD / 16; ++s)
-                        umma_bf16(tmem + b * TILE, dq + (s >> 2) * (kRows * 128 >> 4) + 2 * (s & 3),
+                        umma_bf16(d_s, dq + (s >> 2) * (kRows * 128 >> 4) + 2 * (s & 3),
                                   k + (s >> 2) * (1024 >> 4) + 2 * (s & 3), idesc_s, s > 0);
-                    umma_commit(&bar.s_full[b]);
+                    umma_commit(&bar.s_full[NG == 2 ? w : j & 1]);
+                };
+                for (int j = 0; j < kBuffers && j < jobs && ok; ++j) {
+                    const int st = arrived(false, j);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    score(j, st);
                     umma_commit(&bar.empty[st]);
                     if (j == jobs - 1) umma_commit(&bar.q_empty);
-                    return true;
-                };
-                for (int j = 0; j < kBuffers && j < jobs && ok; ++j) ok = score(j);
+                }
                 for (int j = 0; j < jobs && ok; ++j) {
-                    int st;
-                    uint32_t par;
-                    place<C>(true, w, tile + j, st, par);
+                    // Everything but the weights is waited for first; nothing comes between the
+                    // weights and the next scores, which the group is waiting for, not even the
+                    // commits that only release stages.
                     const int b = NG == 2 ? w : j & 1;
-                    ok = wait_phase(&bar.full[st], par, abort_flag) &&
-                         wait_phase(&bar.p_full[b], np[b] & 1, abort_flag);
+                    const bool more = j + kBuffers < jobs;
+                    const int sv = arrived(true, j);
+                    const int sk = more && ok ? arrived(false, j + kBuffers) : 0;
+                    const uint64_t v = dv + static_cast<uint32_t>(sv * (C::kStageBytes >> 4));
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {
+                        ok = ok && wait_phase(&bar.p_full[b][h], np[b] & 1, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int s = 4 * h; s < 4 * h + 4; ++s)
+                            umma_bf16_ts(d_o, tmem + b * TILE + 8 * s,
+                                         v + s * (2 * kChunks * 1024 >> 4), idesc_o,
+                                         j > 0 || s > 0);
+                    }
                     if (!ok) break;
                     ++np[b];
-                    tc_fence_after_sync();
-                    const uint64_t v = dv + static_cast<uint32_t>(st * (C::kStageBytes >> 4));
-#pragma unroll
-                    for (int s = 0; s < TILE / 16; ++s)
-                        umma_bf16_ts(d_o, tmem + b * TILE + 8 * s,
-                                     v + s * (2 * kChunks * 1024 >> 4), idesc_o, j > 0 || s > 0);
-                    umma_commit(&bar.o_done[w]);
-                    umma_commit(&bar.empty[st]);
-                    if (j + kBuffers < jobs) ok = score(j + kBuffers);
+                    if (more) score(j + kBuffers, sk);
+                    // (two groups: the next scores' arrival says as much, but for the last job)
+                    if (NG == 1 || !more) umma_commit(&bar.o_done[w]);
+                    umma_commit(&bar.empty[sv]);
+                    if (more) umma_commit(&bar.empty[sk]);
+                    if (j + kBuffers == jobs - 1) umma_commit(&bar.q_empty);
                 }
                 tile += jobs;
             }
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t o_cols = lanes + 2 * TILE + w * HD;
         const int gt = quarter * 32 + lane;  // thread of the group
-        uint32_t tile = 0, segs = 0, ns[2] = {0, 0}, nv = 0, values = 0;
+        uint32_t tile = 0, segs = 0, ns[2] = {0, 0}, no = 0, values = 0;
         bool ok = true;
         walk.begin(p, bar.start, span);
         if (w >= NG) walk.f = walk.f1;
@@ -752,46 +752,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (warp_live) {
                     const uint32_t s_cols = lanes + b * TILE;
-                    uint32_t v[TILE];
-                    float part[TILE / 32], top;
+                    // Visibility of the tile's 32 tokens from 32 k on, where it has to be looked at.
+                    auto seen32 = [&](int k) -> uint32_t {
+                        uint32_t bits = row < live ? visible32(p, x, node, pos0 + 32 * k) : 0u;
+                        if ((bad >> (2 * k)) & 1) bits &= 0xFFFF0000u;
+                        if ((bad >> (2 * k)) & 2) bits &= 0x0000FFFFu;
+                        return bits;
+                    };
+                    float top = -INFINITY;
+                    if (!special) {
+                        float part[TILE / 32];
 #pragma unroll
-                    for (int k = 0; k < TILE / 32; ++k)
-                        part[k] = tmem_ldred_values(s_cols + 32 * k, v + 32 * k);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int k = 0; k < TILE / 32; ++k) order_after_wait(part[k]);
-#pragma unroll
-                    for (int k = 0; k < TILE; ++k) asm volatile("" : "+r"(v[k]));
-                    top = part[0];
-#pragma unroll
-                    for (int k = 1; k < TILE / 32; ++k) top = fmaxf(top, part[k]);
-                    if (special) {
-                        top = -INFINITY;
+                        for (int k = 0; k < TILE / 32; ++k)
+                            part[k] = tmem_ldred_max<32>(s_cols + 32 * k);
+                        tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < TILE / 32; ++k) {
-                            uint32_t bits = row < live ? visible32(p, x, node, pos0 + 32 * k) : 0u;
-                            if ((bad >> (2 * k)) & 1) bits &= 0xFFFF0000u;
-                            if ((bad >> (2 * k)) & 2) bits &= 0x0000FFFFu;
+                            order_after_wait(part[k]);
+                            top = fmaxf(top, part[k]);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < TILE / 32; ++k) {
+                            uint32_t u[32];
+                            tmem_ld_32x32b_x32(s_cols + 32 * k, u);
+                            const uint32_t bits = seen32(k);
+                            tmem_ld_wait_for(u);
 #pragma unroll
-                            for (int d = 0; d < 32; ++d) {
-                                const float s = (bits >> d) & 1
-                                                    ? __uint_as_float(v[32 * k + d]) * p.pre
-                                                    : -INFINITY;
-                                v[32 * k + d] = __float_as_uint(s);
-                                top = fmaxf(top, s);
-                            }
+                            for (int d = 0; d < 32; ++d)
+                                if ((bits >> d) & 1)
+                                    top = fmaxf(top, __uint_as_float(u[d]) * p.pre);
                         }
                     }
                     top *= p.c;
                     const bool grow = top > m + kLazy || m == -INFINITY;
                     const float m_new = grow ? fmaxf(top, m) : m;
                     if (__any_sync(0xffffffffu, grow && done > 0)) {
-                        if (!(ok = wait(&bar.o_done[w], (nv - 1) & 1))) break;
-                        tc_fence_after_sync();
+                        // The product before has to be done with O.  With two groups it was
+                        // issued before these scores were, and they are here.
+                        if (NG == 1) {
+                            if (!(ok = wait(&bar.o_done[w], (no - 1) & 1))) break;
+                            tc_fence_after_sync();
+                        }
                         const float shrink =
                             grow ? (m == -INFINITY ? 0.0f : ex2(m - m_new)) : 1.0f;
                         l *= shrink;
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < HD; k += 32) {
                             uint32_t o[32];
                             tmem_ld_32x32b_x32(o_cols + k, o);
@@ -804,42 +810,88 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     m = m_new;
                     const float base = m == -INFINITY ? 0.0f : -m;
-                    float* sums = nullptr;
-                    if (p.sums != nullptr && row < p.rowcap) {
-                        const int64_t at = unit0 + static_cast<int64_t>(ti) * p.members * NQ;
-                        sums = p.sums + at * (TILE / 16) * p.rowcap + row;
-                        p.sums_m[at * p.rowcap + row] = base;
-                    }
                     const float2 c2 = make_float2(p.c, p.c), b2 = make_float2(base, base);
+                    // The first 64 tokens' weights are stored: their product may begin.
+                    auto half_done = [&]() {
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.p_full[b][0]);
+                    };
+                    // The weights of 32 scores: packed to bf16, their sums over 16 tokens kept
+                    // (in registers: a branch here would keep the exponentials of different
+                    // grains from overlapping).
+                    float grain[TILE / 16];
+                    auto weigh = [&](const uint32_t* u, uint32_t* packed, int k) {
 #pragma unroll
-                    for (int k = 0; k < TILE; k += 64) {
-                        uint32_t packed[32];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
+                        for (int q = 0; q < 2; ++q) {
                             float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                             for (int d = 0; d < 16; d += 2) {
-                                float2 e = make_float2(__uint_as_float(v[k + 16 * q + d]),
-                                                       __uint_as_float(v[k + 16 * q + d + 1]));
+                                float2 e = make_float2(__uint_as_float(u[16 * q + d]),
+                                                       __uint_as_float(u[16 * q + d + 1]));
                                 e = fma2(e, c2, b2);
                                 e.x = ex2(e.x);
                                 e.y = ex2(e.y);
                                 sum = d == 0 ? e : add2(sum, e);
                                 packed[8 * q + d / 2] = pack_bf16x2(e.x, e.y);
                             }
-                            const float both = sum.x + sum.y;
-                            l += both;
-                            if (sums != nullptr) sums[(k / 16 + q) * p.rowcap] = both;
+                            grain[2 * k + q] = sum.x + sum.y;
                         }
-                        tmem_st_32x32b_x32(s_cols + k / 2, packed);
+                    };
+                    if (!special) {
+                        uint32_t v[2][32], packed[32];
+                        tmem_ld_32x32b_x32(s_cols, v[0]);
+#pragma unroll
+                        for (int k = 0; k < TILE / 32; ++k) {
+                            uint32_t* u = v[k & 1];
+                            tmem_ld_wait_for(u);
+                            if (k + 1 < TILE / 32)
+                                tmem_ld_32x32b_x32(s_cols + 32 * (k + 1), v[(k + 1) & 1]);
+                            weigh(u, packed + 16 * (k & 1), k);
+                            if (k & 1) tmem_st_32x32b_x32(s_cols + 16 * (k - 1), packed);
+                            if (TILE > 64 && k == 1) half_done();
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < TILE / 32; k += 2) {
+                            uint32_t packed[32];
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                uint32_t u[32];
+                                tmem_ld_32x32b_x32(s_cols + 32 * (k + q), u);
+                                const uint32_t bits = seen32(k + q);
+                                tmem_ld_wait_for(u);
+#pragma unroll
+                                for (int d = 0; d < 32; ++d)
+                                    u[d] = (bits >> d) & 1
+                                               ? __float_as_uint(__uint_as_float(u[d]) * p.pre)
+                                               : 0xFF800000u;
+                                weigh(u, packed + 16 * q, k + q);
+                            }
+                            tmem_st_32x32b_x32(s_cols + 16 * k, packed);
+                            if (TILE > 64 && k == 0) half_done();
+                        }
                     }
                     tmem_st_wait();
+#pragma unroll
+                    for (int k = 0; k < TILE / 16; ++k) l += grain[k];
+                    if (p.sums != nullptr && row < p.rowcap) {
+                        const int64_t at = unit0 + static_cast<int64_t>(ti) * p.members * NQ;
+                        float* sums = p.sums + at * (TILE / 16) * p.rowcap + row;
+                        p.sums_m[at * p.rowcap + row] = base;
+#pragma unroll
+                        for (int k = 0; k < TILE / 16; ++k) sums[k * p.rowcap] = grain[k];
+                    }
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.p_full[b]);
+                if (lane == 0) {
+                    if (TILE > 64 && !warp_live) mbar_arrive(&bar.p_full[b][0]);
+                    mbar_arrive(&bar.p_full[b][TILE / 64 - 1]);
+                }
                 ++done;
-                ++nv;
+                if (NG == 1) ++no;
             }
             if (!ok) break;
             // What this piece of the sequence came to.
@@ -850,8 +902,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (done > 0) {
                     // (one group: the last product's scores may have been issued before the
                     // product before it, so that one is waited for too)
-                    if (NG == 1 && done > 1 && !(ok = wait(&bar.o_done[w], nv & 1))) break;
-                    if (!(ok = wait(&bar.o_done[w], (nv - 1) & 1))) break;
+                    if (NG == 1 && done > 1 && !(ok = wait(&bar.o_done[w], no & 1))) break;
+                    if (!(ok = wait(&bar.o_done[w], (NG == 1 ? no - 1 : no) & 1))) break;
                     tc_fence_after_sync();
                     float* to = p.part_o + (slot * p.rowcap + row) * HD;
 #pragma unroll
@@ -874,6 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                        static_cast<int>(segs);
             }
             if (g.n > 0) ++segs;
+            if (NG == 2 && done > 0) ++no;
             tile += done;
         }
         if (!ok) give_up();
