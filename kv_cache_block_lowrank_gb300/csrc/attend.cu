@@ -48,21 +48,23 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 namespace {
 
 constexpr int kThreads = 384;
-// Registers per thread: at launch, and after the loading and issuing warps have handed theirs to
-// the softmax warps, whose thread holds a row of scores.  128 * 88 + 256 * 208 = 384 * 168.
-constexpr int kRegsLaunch = 168, kRegsIssue = 88, kRegsSoftmax = 208;
 constexpr int kRows = 128;          // UMMA M
 constexpr int kMetaRing = 16;       // bad-id bits of the tiles in flight
 constexpr uint32_t kTmemCols = 512;
 constexpr int kCtas = 152;          // GB300's SMs; the workspace does not depend on the device
 constexpr float kLazy = 8.0f;       // the maximum may lag by 2^8 before O is rescaled
 
-// Tokens per tile, softmax groups, ring depths: S takes 2 TILE columns of TMEM and every
-// group's O HD, 512 in all, and the rings what is left of 227 KB.
+// A tile of K or V is what one ring stage holds; a job is the 64 tokens that a softmax group
+// takes at a time.  TMEM: the score buffers of every group, then every group's O, 512 columns.
+// Two score buffers let a group start on its next scores while the product with its last weights
+// and the scores after that are on their way; for head_dim 192 there is room for one.
 template <int HD, int NQ>
 struct Cfg {
     static constexpr int kTile = HD <= 128 ? 128 : 64;
+    static constexpr int kJobs = kTile / 64;
     static constexpr int kGroups = HD == 256 ? 1 : 2;
+    static constexpr int kBuffers = HD == 192 ? 1 : 2;
+    static constexpr int kOCols = kGroups * kBuffers * 64;  // where O begins
     static constexpr int kStageBytes = kTile * HD * 2;
     static constexpr int kQBytes = NQ * kRows * HD * 2;
     static constexpr int kBudget = 232448 - 1024 - 1024 - kQBytes;
@@ -76,7 +78,7 @@ struct Cfg {
     static constexpr int kStages = kRing0 + kRing1;
     static constexpr int kSmemBytes = 2048 + kQBytes + kStages * kStageBytes;
     static_assert(kRing1 >= 2, "two operands in flight");
-    static_assert(2 * kTile + kGroups * HD <= 512, "tensor memory");
+    static_assert(kOCols + kGroups * HD <= 512, "tensor memory");
     static_assert(kRing0 + 2 <= kMetaRing, "tiles in flight");
 };
 
@@ -114,7 +116,7 @@ struct AttendParams {
     int32_t* part_bad;   // [slot] a node's value was not finite
     float* row_lse;      // [unit row tile][row], log2
     float* sums;         // [tile][member][q tile][16-token granule][row]
-    float* sums_m;       // [tile][member][q tile][row]
+    float* sums_m;       // [tile][member][q tile][job][row]
 };
 
 struct SeqInfo {
@@ -269,15 +271,6 @@ __device__ __forceinline__ void place(bool values, int group, uint32_t n, int& s
     }
 }
 
-template <int REGS>
-__device__ __forceinline__ void give_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-template <int REGS>
-__device__ __forceinline__ void take_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -296,11 +289,32 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
-// The wait for TMEM loads, with their uses held behind it.
-__device__ __forceinline__ void tmem_ld_wait_for(uint32_t* v) {
-    tmem_ld_wait();
+// 32 columns of this thread's TMEM lane and their maximum (usable after the wait).
+__device__ __forceinline__ float tmem_ldred_values(uint32_t taddr, uint32_t* v) {
+    float m;
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+        "%32, [%33];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+          "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]),
+          "=r"(v[31]), "=f"(m)
+        : "r"(taddr));
+    return m;
+}
+
+// The wait for TMEM loads, with the uses of what they brought held behind it.
+__device__ __forceinline__ void tmem_hold(uint32_t* v) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i])::"memory");
+}
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t* v) {
+    tmem_ld_wait();
+    tmem_hold(v);
 }
 
 // 64 visibility bits of a row for nodes 64 w ..
@@ -335,7 +349,7 @@ __device__ __forceinline__ uint32_t visible32(const AttendParams& p, const SeqIn
 
 struct Barriers {
     uint64_t full[12], empty[12];
-    uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_done[2], values;
+    uint64_t q_full, q_empty, s_full[4], p_full[4], o_done[4], values;
     uint32_t bad_ids[2][kMetaRing];  // [ring] per tile in flight: 16-token granules with a bad id
     int bad_value[2][2];          // [group][segment parity]: last segment with such a value
     int abort;
@@ -352,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap map_v, const AttendParams p) {
     using C = Cfg<HD, NQ>;
     constexpr int TILE = C::kTile, NG = C::kGroups;
+    constexpr int kJobs = C::kJobs, kBuffers = C::kBuffers;
     constexpr int kChunks = HD / 64;  // 128-byte columns of an operand row
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -374,13 +389,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&bar.q_full, 1);
         mbar_init(&bar.q_empty, NG);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i][0], 4);
-            mbar_init(&bar.p_full[i][1], 4);
+            mbar_init(&bar.p_full[i], 4);
             mbar_init(&bar.o_done[i], 1);
-            bar.bad_value[i][0] = bar.bad_value[i][1] = -1;
         }
+        for (int i = 0; i < 2; ++i) bar.bad_value[i][0] = bar.bad_value[i][1] = -1;
         mbar_init(&bar.values, 8);
         bar.abort = 0;
         fence_mbarrier_init();
@@ -487,7 +501,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp < 4) {
-        give_registers<kRegsIssue>();
         walk.begin(p, bar.start, span);
         auto wait = [&](uint64_t* b, uint32_t parity) {
             return __all_sync(0xffffffffu, wait_phase(b, parity, abort_flag)) != 0;
@@ -588,95 +601,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp - 2 < NG && lane == 0) {
             // ------------------------------------------------------------ products of group w
             const int w = warp - 2;
-            constexpr int kBuffers = NG == 2 ? 1 : 2;  // score buffers of the group
-            constexpr int kHalves = TILE / 64;
-            constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, TILE);
+            constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, 64);
             constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, HD) | (1u << 16);  // V: MN-major
+            constexpr uint32_t kJobBytes = 64 * HD * 2;  // a job's part of a stage
             const uint64_t dq = smem_desc_kmajor(smem_u32(sQ), 128) +
                                 (NQ == 2 ? w * (kRows * HD * 2 >> 4) : 0);
             const uint64_t dk = smem_desc_128b(smem_u32(sKV), kChunks * 1024, 0);
             const uint64_t dv = smem_desc_128b(smem_u32(sKV), kChunks * 1024, 1024);
-            const uint32_t d_o = tmem + 2 * TILE + w * HD;
+            const uint32_t d_s = tmem + w * (kBuffers * 64);
+            const uint32_t d_o = tmem + C::kOCols + w * HD;
             uint32_t tile = 0, segs = 0, np[2] = {0, 0};
             bool ok = true;
             while (ok && walk.next(p, g)) {
                 if (g.n == 0) continue;
                 if (!(ok = wait_phase(&bar.q_full, segs & 1, abort_flag))) break;
                 ++segs;
-                const int jobs = C::kOwnTiles ? (g.n - w + 1) / 2 : g.n;
+                const int tiles = C::kOwnTiles ? (g.n - w + 1) / 2 : g.n;
+                const int jobs = tiles * kJobs;
                 if (jobs == 0) mbar_arrive(&bar.q_empty);
-                auto arrived = [&](bool v, int j) -> int {  // the stage, once its copy is there
-                    int st;
+                int sk = 0, sv = 0;  // the stages of the tile that each product is on
+                auto stage_of = [&](bool v, int j, int& st) {
                     uint32_t par;
-                    place<C>(v, w, tile + j, st, par);
-                    if (!wait_phase(&bar.full[st], par, abort_flag)) ok = false;
-                    return st;
+                    place<C>(v, w, tile + j / kJobs, st, par);
+                    if (j % kJobs == 0) ok = ok && wait_phase(&bar.full[st], par, abort_flag);
                 };
-                auto score = [&](int j, int st) {
-                    const uint64_t k = dk + static_cast<uint32_t>(st * (C::kStageBytes >> 4));
-                    const uint32_t d_s = tmem + (NG == 2 ? w : j & 1) * TILE;
+                auto score = [&](int j) {
+                    const int b = kBuffers == 2 ? j & 1 : 0;
+                    const uint64_t k =
+                        dk + static_cast<uint32_t>((sk * C::kStageBytes +
+                                                    (j % kJobs) * kJobBytes) >> 4);
 #pragma unroll
                     for (int s = 0; s < HD / 16; ++s)
-                        umma_bf16(d_s, dq + (s >> 2) * (kRows * 128 >> 4) + 2 * (s & 3),
+                        umma_bf16(d_s + 64 * b, dq + (s >> 2) * (kRows * 128 >> 4) + 2 * (s & 3),
                                   k + (s >> 2) * (1024 >> 4) + 2 * (s & 3), idesc_s, s > 0);
-                    umma_commit(&bar.s_full[NG == 2 ? w : j & 1]);
+                    umma_commit(&bar.s_full[w * kBuffers + b]);
+                };
+                auto scored = [&](int j) {  // releases behind the scores
+                    if (j % kJobs == kJobs - 1) umma_commit(&bar.empty[sk]);
+                    if (j == jobs - 1) umma_commit(&bar.q_empty);
                 };
                 for (int j = 0; j < kBuffers && j < jobs && ok; ++j) {
-                    const int st = arrived(false, j);
+                    stage_of(false, j, sk);
                     if (!ok) break;
                     tc_fence_after_sync();
-                    score(j, st);
-                    umma_commit(&bar.empty[st]);
-                    if (j == jobs - 1) umma_commit(&bar.q_empty);
+                    score(j);
+                    scored(j);
                 }
                 for (int j = 0; j < jobs && ok; ++j) {
                     // Everything but the weights is waited for first; nothing comes between the
-                    // weights and the next scores, which the group is waiting for, not even the
-                    // commits that only release stages.
-                    const int b = NG == 2 ? w : j & 1;
+                    // weights and the scores that go into their buffer, which the group will
+                    // wait for, not even the commits that only release stages.
+                    const int b = kBuffers == 2 ? j & 1 : 0;
                     const bool more = j + kBuffers < jobs;
-                    const int sv = arrived(true, j);
-                    const int sk = more && ok ? arrived(false, j + kBuffers) : 0;
-                    const uint64_t v = dv + static_cast<uint32_t>(sv * (C::kStageBytes >> 4));
-#pragma unroll
-                    for (int h = 0; h < kHalves; ++h) {
-                        ok = ok && wait_phase(&bar.p_full[b][h], np[b] & 1, abort_flag);
-                        if (!ok) break;
-                        tc_fence_after_sync();
-#pragma unroll
-                        for (int s = 4 * h; s < 4 * h + 4; ++s)
-                            umma_bf16_ts(d_o, tmem + b * TILE + 8 * s,
-                                         v + s * (2 * kChunks * 1024 >> 4), idesc_o,
-                                         j > 0 || s > 0);
-                    }
+                    stage_of(true, j, sv);
+                    if (more) stage_of(false, j + kBuffers, sk);
+                    ok = ok && wait_phase(&bar.p_full[w * kBuffers + b], np[b] & 1, abort_flag);
                     if (!ok) break;
                     ++np[b];
-                    if (more) score(j + kBuffers, sk);
-                    // (two groups: the next scores' arrival says as much, but for the last job)
-                    if (NG == 1 || !more) umma_commit(&bar.o_done[w]);
-                    umma_commit(&bar.empty[sv]);
-                    if (more) umma_commit(&bar.empty[sk]);
-                    if (j + kBuffers == jobs - 1) umma_commit(&bar.q_empty);
+                    tc_fence_after_sync();
+                    const uint64_t v =
+                        dv + static_cast<uint32_t>((sv * C::kStageBytes +
+                                                    (j % kJobs) * kJobBytes) >> 4);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        umma_bf16_ts(d_o, d_s + 64 * b + 8 * s, v + s * (2 * kChunks * 1024 >> 4),
+                                     idesc_o, j > 0 || s > 0);
+                    if (more) score(j + kBuffers);
+                    umma_commit(&bar.o_done[w * kBuffers + b]);
+                    if (j % kJobs == kJobs - 1) umma_commit(&bar.empty[sv]);
+                    if (more) scored(j + kBuffers);
                 }
-                tile += jobs;
+                tile += tiles;
             }
             if (!ok) give_up();
         }
     } else {
-        take_registers<kRegsSoftmax>();
         // ---------------------------------------------------------------- softmax
         const int w = (warp - 4) >> 2;
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        const uint32_t o_cols = lanes + 2 * TILE + w * HD;
+        const uint32_t o_cols = lanes + C::kOCols + w * HD;
         const int gt = quarter * 32 + lane;  // thread of the group
-        uint32_t tile = 0, segs = 0, ns[2] = {0, 0}, no = 0, values = 0;
+        uint32_t tile = 0, segs = 0, ns[2] = {0, 0}, given[2] = {0, 0}, values = 0;
         bool ok = true;
         walk.begin(p, bar.start, span);
         if (w >= NG) walk.f = walk.f1;
         auto wait = [&](uint64_t* b, uint32_t parity) {
             return __all_sync(0xffffffffu, wait_phase(b, parity, abort_flag)) != 0;
+        };
+        // Waits until the product with buffer b's last weights is done.  A parity names a phase
+        // only if the phase before it has completed and the one after has not.  The one after
+        // takes weights that this warp has not given; the one before was issued two jobs ago,
+        // before scores that this warp has seen.  Hence a barrier for each buffer.
+        auto product_done = [&](int b) -> bool {
+            const bool got = wait(&bar.o_done[w * kBuffers + b], (given[b] - 1) & 1);
+            tc_fence_after_sync();
+            return got;
         };
         while (ok && walk.next(p, g)) {
             const SeqInfo& x = g.x;
@@ -685,33 +706,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool warp_live = quarter * 32 < live;
             const int node = first + row / p.g;
             float m = -INFINITY, l = 0.0f;
-            int done = 0;
+            const int tiles = C::kOwnTiles ? (g.n - w + 1) / 2 : g.n;
+            const int jobs = tiles * kJobs;
             const int64_t unit0 = (g.f * p.members + walk.member) * NQ + (NQ == 2 ? w : 0);
-            for (int ti = C::kOwnTiles ? w : 0; ti < g.n; ti += C::kOwnTiles ? 2 : 1) {
-                const int b = NG == 2 ? w : done & 1;
-                const int pos0 = (g.ta + ti) * TILE;
-                if (!(ok = wait(&bar.s_full[b], ns[b] & 1))) break;
+            for (int j = 0; j < jobs; ++j) {
+                const int b = kBuffers == 2 ? j & 1 : 0, half = j % kJobs;
+                const int ti = C::kOwnTiles ? w + 2 * (j / kJobs) : j / kJobs;
+                const int pos0 = (g.ta + ti) * TILE + 64 * half;
+                if (!(ok = wait(&bar.s_full[w * kBuffers + b], ns[b] & 1))) break;
                 ++ns[b];
                 tc_fence_after_sync();
-                const uint32_t bad = *(volatile uint32_t*)
-                    &bar.bad_ids[C::kOwnTiles ? w : 0][(tile + done) % kMetaRing];
-                const bool special = pos0 + TILE > x.ctx || bad != 0 || p.pre != 1.0f;
-                if (pos0 + TILE > x.ctx) {
+                const uint32_t bad =
+                    *(volatile uint32_t*)&bar.bad_ids[C::kOwnTiles ? w : 0]
+                                                     [(tile + j / kJobs) % kMetaRing] >> (4 * half);
+                const bool special = pos0 + 64 > x.ctx || (bad & 15) != 0 || p.pre != 1.0f;
+                if (pos0 + 64 > x.ctx) {
                     // Values past the end become zero; so do a node's non-finite elements.
                     int sv;
                     uint32_t par;
-                    place<C>(true, w, tile + done, sv, par);
+                    place<C>(true, w, tile + j / kJobs, sv, par);
                     if (!(ok = wait(&bar.full[sv], par))) break;
-                    uint8_t* stage = sKV + sv * C::kStageBytes;
+                    uint8_t* part = sKV + sv * C::kStageBytes + half * (64 * HD * 2);
                     bool found = false;
-                    constexpr int all = TILE * kChunks;
-                    for (int k = gt + (NQ == 2 ? w * 128 : 0); k < all; k += NQ == 2 ? 256 : 128) {
-                        const int r = k % TILE, ch = k / TILE;
+                    for (int k = gt + (NQ == 2 ? w * 128 : 0); k < 64 * kChunks;
+                         k += NQ == 2 ? 256 : 128) {
+                        const int r = k % 64, ch = k / 64;
                         if (pos0 + r < x.ctx) continue;
 #pragma unroll 2
                         for (int e = 0; e < 8; ++e) {
                             uint4* at = reinterpret_cast<uint4*>(
-                                stage + ((r >> 3) * kChunks + ch) * 1024 +
+                                part + ((r >> 3) * kChunks + ch) * 1024 +
                                 swizzled_offset(r & 7, 16 * e, 128));
                             if (pos0 + r >= x.tokens) {
                                 *at = make_uint4(0, 0, 0, 0);
@@ -751,49 +775,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (warp_live) {
-                    const uint32_t s_cols = lanes + b * TILE;
-                    // Visibility of the tile's 32 tokens from 32 k on, where it has to be looked at.
-                    auto seen32 = [&](int k) -> uint32_t {
-                        uint32_t bits = row < live ? visible32(p, x, node, pos0 + 32 * k) : 0u;
-                        if ((bad >> (2 * k)) & 1) bits &= 0xFFFF0000u;
-                        if ((bad >> (2 * k)) & 2) bits &= 0x0000FFFFu;
-                        return bits;
-                    };
-                    float top = -INFINITY;
-                    if (!special) {
-                        float part[TILE / 32];
+                    const uint32_t s_cols = lanes + (w * kBuffers + b) * 64;
+                    // The job's scores and their maximum in one read.
+                    uint32_t v[64];
+                    const float top0 = tmem_ldred_values(s_cols, v);
+                    float top = tmem_ldred_values(s_cols + 32, v + 32);
+                    tmem_ld_wait_for(v);
+                    tmem_hold(v + 32);
+                    float t0 = top0;
+                    order_after_wait(t0);
+                    order_after_wait(top);
+                    top = fmaxf(top, t0);
+                    if (special) {
+                        // What the row does not see goes to -inf.
+                        top = -INFINITY;
 #pragma unroll
-                        for (int k = 0; k < TILE / 32; ++k)
-                            part[k] = tmem_ldred_max<32>(s_cols + 32 * k);
-                        tmem_ld_wait();
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t bits = row < live ? visible32(p, x, node, pos0 + 32 * k) : 0u;
+                            if ((bad >> (2 * k)) & 1) bits &= 0xFFFF0000u;
+                            if ((bad >> (2 * k)) & 2) bits &= 0x0000FFFFu;
 #pragma unroll
-                        for (int k = 0; k < TILE / 32; ++k) {
-                            order_after_wait(part[k]);
-                            top = fmaxf(top, part[k]);
-                        }
-                    } else {
-#pragma unroll 1
-                        for (int k = 0; k < TILE / 32; ++k) {
-                            uint32_t u[32];
-                            tmem_ld_32x32b_x32(s_cols + 32 * k, u);
-                            const uint32_t bits = seen32(k);
-                            tmem_ld_wait_for(u);
-#pragma unroll
-                            for (int d = 0; d < 32; ++d)
-                                if ((bits >> d) & 1)
-                                    top = fmaxf(top, __uint_as_float(u[d]) * p.pre);
+                            for (int d = 0; d < 32; ++d) {
+                                const float s = (bits >> d) & 1
+                                                    ? __uint_as_float(v[32 * k + d]) * p.pre
+                                                    : -INFINITY;
+                                v[32 * k + d] = __float_as_uint(s);
+                                top = fmaxf(top, s);
+                            }
                         }
                     }
                     top *= p.c;
                     const bool grow = top > m + kLazy || m == -INFINITY;
                     const float m_new = grow ? fmaxf(top, m) : m;
-                    if (__any_sync(0xffffffffu, grow && done > 0)) {
-                        // The product before has to be done with O.  With two groups it was
-                        // issued before these scores were, and they are here.
-                        if (NG == 1) {
-                            if (!(ok = wait(&bar.o_done[w], (no - 1) & 1))) break;
-                            tc_fence_after_sync();
-                        }
+                    if (__any_sync(0xffffffffu, grow && j > 0)) {
+                        // The product before has to be done with O.
+                        if (!(ok = product_done(kBuffers == 2 ? b ^ 1 : 0))) break;
                         const float shrink =
                             grow ? (m == -INFINITY ? 0.0f : ex2(m - m_new)) : 1.0f;
                         l *= shrink;
@@ -811,87 +827,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m = m_new;
                     const float base = m == -INFINITY ? 0.0f : -m;
                     const float2 c2 = make_float2(p.c, p.c), b2 = make_float2(base, base);
-                    // The first 64 tokens' weights are stored: their product may begin.
-                    auto half_done = [&]() {
-                        tmem_st_wait();
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.p_full[b][0]);
-                    };
-                    // The weights of 32 scores: packed to bf16, their sums over 16 tokens kept
-                    // (in registers: a branch here would keep the exponentials of different
-                    // grains from overlapping).
-                    float grain[TILE / 16];
-                    auto weigh = [&](const uint32_t* u, uint32_t* packed, int k) {
+                    // The weights, packed to bf16, and their sums over 16 tokens (which stay in
+                    // registers until the end: a branch in between would keep the exponentials
+                    // of different granules from overlapping).
+                    float grain[4];
+                    uint32_t packed[32];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            float2 sum = make_float2(0.0f, 0.0f);
+                    for (int q = 0; q < 4; ++q) {
+                        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                            for (int d = 0; d < 16; d += 2) {
-                                float2 e = make_float2(__uint_as_float(u[16 * q + d]),
-                                                       __uint_as_float(u[16 * q + d + 1]));
-                                e = fma2(e, c2, b2);
-                                e.x = ex2(e.x);
-                                e.y = ex2(e.y);
-                                sum = d == 0 ? e : add2(sum, e);
-                                packed[8 * q + d / 2] = pack_bf16x2(e.x, e.y);
-                            }
-                            grain[2 * k + q] = sum.x + sum.y;
+                        for (int d = 0; d < 16; d += 2) {
+                            float2 e = make_float2(__uint_as_float(v[16 * q + d]),
+                                                   __uint_as_float(v[16 * q + d + 1]));
+                            e = fma2(e, c2, b2);
+                            e.x = ex2(e.x);
+                            e.y = ex2(e.y);
+                            sum = d == 0 ? e : add2(sum, e);
+                            packed[8 * q + d / 2] = pack_bf16x2(e.x, e.y);
                         }
-                    };
-                    if (!special) {
-                        uint32_t v[2][32], packed[32];
-                        tmem_ld_32x32b_x32(s_cols, v[0]);
-#pragma unroll
-                        for (int k = 0; k < TILE / 32; ++k) {
-                            uint32_t* u = v[k & 1];
-                            tmem_ld_wait_for(u);
-                            if (k + 1 < TILE / 32)
-                                tmem_ld_32x32b_x32(s_cols + 32 * (k + 1), v[(k + 1) & 1]);
-                            weigh(u, packed + 16 * (k & 1), k);
-                            if (k & 1) tmem_st_32x32b_x32(s_cols + 16 * (k - 1), packed);
-                            if (TILE > 64 && k == 1) half_done();
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < TILE / 32; k += 2) {
-                            uint32_t packed[32];
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                uint32_t u[32];
-                                tmem_ld_32x32b_x32(s_cols + 32 * (k + q), u);
-                                const uint32_t bits = seen32(k + q);
-                                tmem_ld_wait_for(u);
-#pragma unroll
-                                for (int d = 0; d < 32; ++d)
-                                    u[d] = (bits >> d) & 1
-                                               ? __float_as_uint(__uint_as_float(u[d]) * p.pre)
-                                               : 0xFF800000u;
-                                weigh(u, packed + 16 * q, k + q);
-                            }
-                            tmem_st_32x32b_x32(s_cols + 16 * k, packed);
-                            if (TILE > 64 && k == 0) half_done();
-                        }
+                        grain[q] = sum.x + sum.y;
                     }
+                    tmem_st_32x32b_x32(s_cols, packed);
                     tmem_st_wait();
-#pragma unroll
-                    for (int k = 0; k < TILE / 16; ++k) l += grain[k];
+                    l += (grain[0] + grain[1]) + (grain[2] + grain[3]);
                     if (p.sums != nullptr && row < p.rowcap) {
-                        const int64_t at = unit0 + static_cast<int64_t>(ti) * p.members * NQ;
-                        float* sums = p.sums + at * (TILE / 16) * p.rowcap + row;
+                        const int64_t at =
+                            (unit0 + static_cast<int64_t>(ti) * p.members * NQ) * kJobs + half;
+                        float* sums = p.sums + at * 4 * p.rowcap + row;
                         p.sums_m[at * p.rowcap + row] = base;
 #pragma unroll
-                        for (int k = 0; k < TILE / 16; ++k) sums[k * p.rowcap] = grain[k];
+                        for (int k = 0; k < 4; ++k) sums[k * p.rowcap] = grain[k];
                     }
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) {
-                    if (TILE > 64 && !warp_live) mbar_arrive(&bar.p_full[b][0]);
-                    mbar_arrive(&bar.p_full[b][TILE / 64 - 1]);
-                }
-                ++done;
-                if (NG == 1) ++no;
+                if (lane == 0) mbar_arrive(&bar.p_full[w * kBuffers + b]);
+                ++given[b];
             }
             if (!ok) break;
             // What this piece of the sequence came to.
@@ -899,12 +870,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t slot =
                     (static_cast<int64_t>(g.item + blockIdx.x / p.members) * p.members +
                      walk.member) * 2 + w;
-                if (done > 0) {
-                    // (one group: the last product's scores may have been issued before the
-                    // product before it, so that one is waited for too)
-                    if (NG == 1 && done > 1 && !(ok = wait(&bar.o_done[w], no & 1))) break;
-                    if (!(ok = wait(&bar.o_done[w], (NG == 1 ? no - 1 : no) & 1))) break;
-                    tc_fence_after_sync();
+                if (jobs > 0) {
+                    if (!(ok = product_done(0)) || (jobs > 1 && kBuffers == 2 &&
+                                                    !(ok = product_done(1))))
+                        break;
                     float* to = p.part_o + (slot * p.rowcap + row) * HD;
 #pragma unroll
                     for (int k = 0; k < HD; k += 32) {
@@ -922,12 +891,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (row < live) p.part_ml[slot * p.rowcap + row] = make_float2(m, l);
                 if (row == 0)
-                    p.part_bad[slot] = done > 0 && *(volatile int*)&bar.bad_value[w][segs & 1] ==
+                    p.part_bad[slot] = jobs > 0 && *(volatile int*)&bar.bad_value[w][segs & 1] ==
                                                        static_cast<int>(segs);
             }
             if (g.n > 0) ++segs;
-            if (NG == 2 && done > 0) ++no;
-            tile += done;
+            tile += tiles;
         }
         if (!ok) give_up();
     }
@@ -1070,7 +1038,7 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row
 template <int HD, int NQ>
 __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p) {
     using C = Cfg<HD, NQ>;
-    constexpr int TILE = C::kTile, kGran = TILE / 16;
+    constexpr int TILE = C::kTile, kGran = TILE / 16, kJobs = C::kJobs;
     const int span = NQ * p.nodes_tile;
     const int lane = threadIdx.x & 31;
     grid_dependency_wait();
@@ -1112,7 +1080,8 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p) {
                     if (lse == -INFINITY) continue;
                     const float part = p.sums[(at * kGran + gr % kGran) * p.rowcap + lr];
                     if (part == 0.0f) continue;  // (m may then be anything)
-                    sum += part * exp2f(-p.sums_m[at * p.rowcap + lr] - lse);
+                    sum += part *
+                           exp2f(-p.sums_m[(at * kJobs + gr % kGran / 4) * p.rowcap + lr] - lse);
                 }
             }
         }
@@ -1185,7 +1154,7 @@ Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total
     if (with_weights) {
         const size_t lanes = static_cast<size_t>(p.tiles) * p.members * p.nq_tiles * p.rowcap;
         p.row_lse = take(static_cast<size_t>(p.units) * p.rowcap * 4);
-        p.sums_m = take(lanes * 4);
+        p.sums_m = take(lanes * (p.tile / 64) * 4);
         p.sums = take(lanes * (p.tile / 16) * 4);
     }
     p.bytes = at;
@@ -1212,12 +1181,7 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
     {
         std::lock_guard<std::mutex> lk(g_attr_mu);
         if (!g_attr_set[device & 63][which]) {
-            // The softmax warps wait for the registers that the others hand back: the kernel must
-            // have been launched with as many as the shares add up to.
-            cudaFuncAttributes attr;
-            if (cudaFuncGetAttributes(&attr, attend_kernel<HD, NQ>) != cudaSuccess ||
-                attr.numRegs < kRegsLaunch ||
-                cudaFuncSetAttribute(attend_kernel<HD, NQ>,
+            if (cudaFuncSetAttribute(attend_kernel<HD, NQ>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      C::kSmemBytes) != cudaSuccess)
                 return HSS_ERR_CUDA;
