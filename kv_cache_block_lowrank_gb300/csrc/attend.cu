@@ -924,112 +924,168 @@ __device__ __forceinline__ void item_range(const AttendParams& p, const SeqInfo&
     f += static_cast<int64_t>(h) * n;
 }
 
-// Joins the pieces of every row: one warp per row at a time, a CTA per (sequence, row tile,
-// head).
-template <int HD, int NQ>
-__global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row_tiles) {
+// Joins the pieces of the rows.  A CTA takes 8 / WPR rows of one (sequence, row tile, head), WPR
+// warps to a row: with few rows the pieces of a row (a long sequence is cut into as many as there
+// are CTAs to share it) are spread over warps, so that their loads are in flight together; with
+// many rows a warp takes a row by itself.
+template <int HD, int NQ, int WPR>
+__global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row_tiles,
+                                                   int row_parts) {
     using C = Cfg<HD, NQ>;
     constexpr int TILE = C::kTile;
     constexpr int kEach = HD / 32;  // elements of a row per lane, in pairs
+    constexpr int kAtOnce = 32 / kEach;
+    constexpr int kPieceWidth = NQ == 1 ? C::kGroups : 1;  // pieces of a row per CTA group
+    __shared__ float sh_acc[WPR > 1 ? 8 : 1][HD];
+    __shared__ float sh_l[8], sh_top[8];
     const int span = NQ * p.nodes_tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = blockIdx.x % row_parts;
+    const int unit = blockIdx.x / row_parts;
+    const int rt = unit % row_tiles;
+    const int h = unit / row_tiles % p.nkv;
+    const int s = unit / row_tiles / p.nkv;
+    const int sub = warp % WPR;
+    const int r = part * (8 / WPR) + warp / WPR;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int rt = blockIdx.x % row_tiles;
-    const int h = blockIdx.x / row_tiles % p.nkv;
-    const int s = blockIdx.x / row_tiles / p.nkv;
     const SeqInfo x = load_seq(p, s);
-    const int rows = min(max(x.nodes - rt * span, 0), span) * p.g;
-    if (rows == 0) return;
+    const int64_t seq0 = p.seq_tiles[s], per = p.header[1];
     const int b = rt / p.members, member = rt % p.members;
+    const int64_t item = p.seq_items[s] + b * p.nkv + h;
+    const int rows = min(max(x.nodes - rt * span, 0), span) * p.g;
+    const bool mine = r < rows;
+    if (WPR == 1 && !mine) return;  // (with several warps a row, the CTA meets below)
     int64_t f;
     int n;
-    item_range<TILE>(p, x, span, p.seq_tiles[s], b, h, f, n);
-    const int64_t per = p.header[1];
-    const int64_t item = p.seq_items[s] + b * p.nkv + h;
+    item_range<TILE>(p, x, span, seq0, b, h, f, n);
     const int64_t g0 = n > 0 ? f / per : 0, g1 = n > 0 ? (f + n - 1) / per : -1;
-    const int pieces = static_cast<int>(g1 - g0 + 1) * (NQ == 1 ? C::kGroups : 1);
-    for (int r = warp; r < rows; r += 8) {
-        const int node = rt * span + r / p.g, head = h * p.g + r % p.g;
-        const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
-        const int lr = r - qt * p.nodes_tile * p.g;
-        // piece k of the row -> slot
-        auto slot_of = [&](int k) -> int64_t {
-            const int grp = NQ == 1 && C::kGroups == 2 ? k >> 1 : k;
-            const int w = NQ == 2 ? qt : (C::kGroups == 2 ? k & 1 : 0);
-            return ((item + g0 + grp) * p.members + member) * 2 + w;
-        };
-        float top = -INFINITY;
-        int bad = 0;
-        for (int k = lane; k < pieces; k += 32) {
-            const int64_t sl = slot_of(k);
-            const float2 ml = p.part_ml[sl * p.rowcap + lr];
-            if (ml.y != 0.0f) top = fmaxf(top, ml.x);
-            bad |= p.part_bad[sl];
+    const int pieces = mine ? static_cast<int>(g1 - g0 + 1) * kPieceWidth : 0;
+    const int node = rt * span + r / p.g, head = h * p.g + r % p.g;
+    const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
+    const int lr = r - qt * p.nodes_tile * p.g;
+    // piece k of the row -> slot
+    auto slot_of = [&](int k) -> int64_t {
+        const int grp = k / kPieceWidth;
+        const int w = NQ == 2 ? qt : k % kPieceWidth;
+        return ((item + g0 + grp) * p.members + member) * 2 + w;
+    };
+    float top = -INFINITY;
+    int bad = 0;
+    for (int k = sub + WPR * lane; k < pieces; k += 32 * WPR) {
+        const int64_t sl = slot_of(k);
+        const float2 ml = p.part_ml[sl * p.rowcap + lr];
+        if (ml.y != 0.0f) top = fmaxf(top, ml.x);
+        bad |= p.part_bad[sl];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    bad = __any_sync(0xffffffffu, bad);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float l = 0.0f, acc[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) acc[i] = 0.0f;
+    for (int k0 = sub; k0 < pieces; k0 += 32 * WPR) {
+        float wt = 0.0f;
+        if (k0 + WPR * lane < pieces) {
+            const float2 ml = p.part_ml[slot_of(k0 + WPR * lane) * p.rowcap + lr];
+            wt = ml.y != 0.0f ? exp2f(ml.x - base) : 0.0f;
+            l += ml.y != 0.0f ? wt * ml.y : 0.0f;
         }
+        const int here = min(32, (pieces - k0 + WPR - 1) / WPR);
+        for (int k = 0; k < here; k += kAtOnce) {
+            float2 v[kAtOnce][kEach / 2];
+            float wk[kAtOnce];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        bad = __any_sync(0xffffffffu, bad);
-        const float base = top == -INFINITY ? 0.0f : top;
-        float l = 0.0f, acc[kEach];
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) acc[i] = 0.0f;
-        for (int k0 = 0; k0 < pieces; k0 += 32) {
-            float wt = 0.0f;
-            if (k0 + lane < pieces) {
-                const float2 ml = p.part_ml[slot_of(k0 + lane) * p.rowcap + lr];
-                wt = ml.y != 0.0f ? exp2f(ml.x - base) : 0.0f;
-                l += ml.y != 0.0f ? wt * ml.y : 0.0f;
-            }
-            const int here = min(32, pieces - k0);
-#pragma unroll 4
-            for (int k = 0; k < here; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, wt, k);
-                if (wk == 0.0f) continue;
+            for (int q = 0; q < kAtOnce; ++q) {
+                wk[q] = __shfl_sync(0xffffffffu, wt, (k + q) & 31);
+                if (k + q >= here) wk[q] = 0.0f;
+                // (a piece without weight may hold anything)
                 const float2* o = reinterpret_cast<const float2*>(
-                    p.part_o + (slot_of(k0 + k) * p.rowcap + lr) * HD);
+                    p.part_o + (slot_of(k0 + WPR * (k + q)) * p.rowcap + lr) * HD);
+#pragma unroll
+                for (int i = 0; i < kEach / 2; ++i)
+                    v[q][i] = wk[q] != 0.0f ? o[lane + 32 * i] : make_float2(0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q)
 #pragma unroll
                 for (int i = 0; i < kEach / 2; ++i) {
-                    const float2 v = o[lane + 32 * i];
-                    acc[2 * i] += wk * v.x;
-                    acc[2 * i + 1] += wk * v.y;
+                    acc[2 * i] += wk[q] * v[q][i].x;
+                    acc[2 * i + 1] += wk[q] * v[q][i].y;
                 }
-            }
         }
+    }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (bad) {
-            // Non-finite values of the nodes this row sees.
-            for (int j = 0; j < x.nodes; ++j) {
-                if (x.ctx + j >= x.tokens) break;
-                if (!((node_word(p, x, node, j >> 6) >> (j & 63)) & 1)) continue;
-                const int pos = x.ctx + j;
-                const int64_t id = p.table[x.e0 + pos / p.bs];
-                if (id < 0 || id >= p.max_blocks) continue;
-                const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                    p.V + ((id * p.bs + pos % p.bs) * p.nkv + h) * HD);
-#pragma unroll
-                for (int i = 0; i < kEach / 2; ++i) {
-                    const uint32_t u = v[lane + 32 * i];
-                    const float lo = __uint_as_float(u << 16);
-                    const float hi = __uint_as_float(u & 0xFFFF0000u);
-                    if (!isfinite(lo)) acc[2 * i] += lo;
-                    if (!isfinite(hi)) acc[2 * i + 1] += hi;
-                }
-            }
-        }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int64_t at = (static_cast<int64_t>(x.q0) + node) * p.nq + head;
-        uint32_t* to = reinterpret_cast<uint32_t*>(p.out + at * HD);
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float m = base;
+    if constexpr (WPR > 1) {
+        // The row's first warp adds up what the others have.
 #pragma unroll
         for (int i = 0; i < kEach / 2; ++i)
-            to[lane + 32 * i] = l == 0.0f ? 0u : pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+            *reinterpret_cast<float2*>(&sh_acc[warp][2 * (lane + 32 * i)]) =
+                make_float2(acc[2 * i], acc[2 * i + 1]);
         if (lane == 0) {
-            const float lse2 = l == 0.0f ? -INFINITY : base + log2f(l);
-            if (p.lse != nullptr) p.lse[at] = lse2 * 0.693147180559945309f;
-            if (p.sums != nullptr)
-                p.row_lse[((item * p.members + member) * NQ + qt) * p.rowcap + lr] = lse2;
+            sh_l[warp] = l;
+            sh_top[warp] = top;
         }
+        bad = __syncthreads_or(bad);
+        if (sub != 0 || !mine) return;
+        float all = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < WPR; ++k)
+            if (sh_l[warp + k] != 0.0f) all = fmaxf(all, sh_top[warp + k]);
+        m = all == -INFINITY ? 0.0f : all;
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) acc[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < WPR; ++k) {
+            const float lk = sh_l[warp + k];
+            if (lk == 0.0f) continue;
+            const float t = sh_top[warp + k];
+            const float wk = exp2f((t == -INFINITY ? 0.0f : t) - m);
+            l += wk * lk;
+#pragma unroll
+            for (int i = 0; i < kEach / 2; ++i) {
+                const float2 v =
+                    *reinterpret_cast<const float2*>(&sh_acc[warp + k][2 * (lane + 32 * i)]);
+                acc[2 * i] += wk * v.x;
+                acc[2 * i + 1] += wk * v.y;
+            }
+        }
+    }
+    if (bad) {
+        // Non-finite values of the nodes this row sees.
+        for (int j = 0; j < x.nodes; ++j) {
+            if (x.ctx + j >= x.tokens) break;
+            if (!((node_word(p, x, node, j >> 6) >> (j & 63)) & 1)) continue;
+            const int pos = x.ctx + j;
+            const int64_t id = p.table[x.e0 + pos / p.bs];
+            if (id < 0 || id >= p.max_blocks) continue;
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                p.V + ((id * p.bs + pos % p.bs) * p.nkv + h) * HD);
+#pragma unroll
+            for (int i = 0; i < kEach / 2; ++i) {
+                const uint32_t u = v[lane + 32 * i];
+                const float lo = __uint_as_float(u << 16);
+                const float hi = __uint_as_float(u & 0xFFFF0000u);
+                if (!isfinite(lo)) acc[2 * i] += lo;
+                if (!isfinite(hi)) acc[2 * i + 1] += hi;
+            }
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t at = (static_cast<int64_t>(x.q0) + node) * p.nq + head;
+    uint32_t* to = reinterpret_cast<uint32_t*>(p.out + at * HD);
+#pragma unroll
+    for (int i = 0; i < kEach / 2; ++i)
+        to[lane + 32 * i] = l == 0.0f ? 0u : pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    if (lane == 0) {
+        const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+        if (p.lse != nullptr) p.lse[at] = lse2 * 0.693147180559945309f;
+        if (p.sums != nullptr)
+            p.row_lse[((item * p.members + member) * NQ + qt) * p.rowcap + lr] = lse2;
     }
 }
 
@@ -1059,30 +1115,31 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p) {
     if (pos0 < x.tokens) {
         const int left = static_cast<int>(min(static_cast<int64_t>(p.bs), x.tokens - pos0));
         const int gr0 = static_cast<int>(pos0 / 16), grains = (left + 15) / 16;
-        for (int h = 0; h < p.nkv; ++h) {
-            for (int rt = 0; rt < rts; ++rt) {
-                const int b = rt / p.members, member = rt % p.members;
-                int64_t f;
-                int n;
-                item_range<TILE>(p, x, span, seq0, b, h, f, n);
-                const int mine = tiles_upto<TILE>(p, x, min(x.nodes, (rt + 1) * span));
-                const int rows = min(x.nodes - rt * span, span) * p.g;
-                const int64_t unit = (static_cast<int64_t>(item0 + b * p.nkv + h) * p.members +
-                                      member) * NQ;
-                for (int i = lane; i < rows * grains; i += 32) {
-                    const int r = i % rows, gr = gr0 + i / rows;
-                    const int t = gr / kGran;
-                    if (t >= mine) continue;
-                    const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
-                    const int lr = r - qt * p.nodes_tile * p.g;
-                    const int64_t at = ((f + t) * p.members + member) * NQ + qt;
-                    const float lse = p.row_lse[(unit + qt) * p.rowcap + lr];
-                    if (lse == -INFINITY) continue;
-                    const float part = p.sums[(at * kGran + gr % kGran) * p.rowcap + lr];
-                    if (part == 0.0f) continue;  // (m may then be anything)
-                    sum += part *
-                           exp2f(-p.sums_m[(at * kJobs + gr % kGran / 4) * p.rowcap + lr] - lse);
-                }
+        for (int rt = 0; rt < rts; ++rt) {
+            // the (head, granule, row) triples of the row tile, over the lanes
+            const int bt = rt / p.members, member = rt % p.members;
+            const int mine = tiles_upto<TILE>(p, x, min(x.nodes, (rt + 1) * span));
+            const int rows = min(x.nodes - rt * span, span) * p.g;
+            const int each = rows * grains;
+            int64_t f0;
+            int n;
+            item_range<TILE>(p, x, span, seq0, bt, 0, f0, n);
+            for (int i = lane; i < each * p.nkv; i += 32) {
+                const int h = i / each, in = i - h * each;
+                const int gr = gr0 + in / rows, r = in % rows;
+                const int t = gr / kGran;
+                if (t >= mine) continue;
+                const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
+                const int lr = r - qt * p.nodes_tile * p.g;
+                const int64_t at =
+                    ((f0 + static_cast<int64_t>(h) * n + t) * p.members + member) * NQ + qt;
+                const int64_t row =
+                    (static_cast<int64_t>(item0 + bt * p.nkv + h) * p.members + member) * NQ + qt;
+                const float lse = p.row_lse[row * p.rowcap + lr];
+                const float m = p.sums_m[(at * kJobs + gr % kGran / 4) * p.rowcap + lr];
+                const float part = p.sums[(at * kGran + gr % kGran) * p.rowcap + lr];
+                if (lse == -INFINITY || part == 0.0f) continue;  // (m may then be anything)
+                sum += part * exp2f(-m - lse);
             }
         }
     }
@@ -1192,9 +1249,16 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
                    C::kSmemBytes, stream, mq, mk, mv, p) != cudaSuccess)
         return HSS_ERR_CUDA;
     if (rows) {
-        const unsigned grid = static_cast<unsigned>(plan.row_tiles) * p.nkv * p.num_seqs;
-        if (launch_pdl(join_kernel<HD, NQ>, dim3(grid), dim3(256), 0, stream, p,
-                       plan.row_tiles) != cudaSuccess)
+        // Warps to a row: 8 while a CTA per row leaves SMs free (a lone sequence's 32 rows of 38
+        // pieces), else one.
+        const int unit_rows = std::min(p.max_q, NQ * plan.nodes_tile) * p.g;
+        const int64_t units = static_cast<int64_t>(plan.row_tiles) * p.nkv * p.num_seqs;
+        const bool few = units * unit_rows <= 2 * kCtas;
+        const int parts = few ? unit_rows : (unit_rows + 7) / 8;
+        if (units * parts > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
+        auto join = few ? join_kernel<HD, NQ, 8> : join_kernel<HD, NQ, 1>;
+        if (launch_pdl(join, dim3(static_cast<unsigned>(units * parts)), dim3(256), 0, stream, p,
+                       plan.row_tiles, parts) != cudaSuccess)
             return HSS_ERR_CUDA;
     }
     if (p.weights_out != nullptr &&
@@ -1262,8 +1326,6 @@ hss_status launch_attend(const AttendArgs& r, cudaStream_t stream) {
     p.sums = weigh ? reinterpret_cast<float*>(ws + plan.sums) : nullptr;
     p.sums_m = weigh ? reinterpret_cast<float*>(ws + plan.sums_m) : nullptr;
     const bool rows = a.total_q > 0;
-    if (static_cast<int64_t>(plan.row_tiles) * p.nkv * p.num_seqs > 0x7FFFFFFF)
-        return HSS_ERR_INVALID_ARGUMENT;
 
     // Without rows nothing is loaded, but the maps have to be well formed.
     CUtensorMap mq, mk, mv;
