@@ -108,8 +108,8 @@ struct AttendParams {
     int32_t* dev_status;
     int32_t* lib_error;
     // workspace
-    int64_t* header;     // [0] tiles in all, [1] tiles per group
-    int64_t* seq_tiles;  // [num_seqs] tiles before a sequence
+    int32_t* header;     // [0] tiles in all, [1] tiles per group
+    int32_t* seq_tiles;  // [num_seqs] tiles before a sequence
     int32_t* seq_items;  // [num_seqs] (batch, head) items before a sequence
     float* part_o;       // [slot][row][head_dim]
     float2* part_ml;     // [slot][row] (m, l)
@@ -152,18 +152,17 @@ __device__ __forceinline__ int batch_tiles(const AttendParams& p, const SeqInfo&
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 template <int TILE>
-__device__ __forceinline__ int64_t seq_tiles(const AttendParams& p, const SeqInfo& x, int span,
-                                             int nb) {
+__device__ __forceinline__ int seq_tiles(const AttendParams& p, const SeqInfo& x, int span,
+                                         int nb) {
     if (p.mask != nullptr || nb == 1)
-        return static_cast<int64_t>(nb) * p.nkv * (nb > 0 ? batch_tiles<TILE>(p, x, span, 0) : 0);
-    int64_t w = 0;
+        return nb * p.nkv * (nb > 0 ? batch_tiles<TILE>(p, x, span, 0) : 0);
+    int w = 0;
     for (int b = 0; b < nb; ++b) w += batch_tiles<TILE>(p, x, span, b);
     return w * p.nkv;
 }
 
 struct Start {
-    int s, b, h, t, item0;
-    int64_t total, per;
+    int s, b, h, t, item0, total, per;
 };
 
 // One piece of this CTA's range: tiles [ta, ta + n) of (sequence, head) for row tile rt.
@@ -171,14 +170,13 @@ struct Segment {
     SeqInfo x;
     int h, rt, ta, n, item;
     bool rows;  // the row tile exists
-    int64_t f;  // list index of tile ta
+    int f;      // list index of tile ta
 };
 
 template <int TILE>
 struct Walk {
     SeqInfo x;
-    int s, b, h, t, nb, rts, item0, member, span;
-    int64_t f, f1;
+    int s, b, h, t, nb, rts, item0, member, span, f, f1;
 
     __device__ __forceinline__ void enter(const AttendParams& p) {
         x = load_seq(p, s);
@@ -202,7 +200,7 @@ struct Walk {
         while (f < f1) {
             const int n = nb > 0 ? batch_tiles<TILE>(p, x, span, b) : 0;
             if (t < n) {
-                const int take = static_cast<int>(min(static_cast<int64_t>(n - t), f1 - f));
+                const int take = min(n - t, f1 - f);
                 g.x = x;
                 g.h = h;
                 g.rt = b * p.members + member;
@@ -355,7 +353,7 @@ struct Barriers {
     int abort;
     uint32_t tmem;
     Start start;
-    int64_t scan[kThreads / 32];
+    int scan[kThreads / 32];
     int scan_items[kThreads / 32];
 };
 
@@ -410,10 +408,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int each = ceil_div(p.num_seqs, kThreads);
         const int s0 = min(static_cast<int>(threadIdx.x) * each, p.num_seqs);
         const int s1 = min(s0 + each, p.num_seqs);
-        int64_t tiles = 0;
+        int tiles = 0;
         int items = 0;
+        SeqInfo x;  // (with one sequence a thread, still there for the second look)
         for (int s = s0; s < s1; ++s) {
-            const SeqInfo x = load_seq(p, s);
+            x = load_seq(p, s);
             const int nb = ceil_div(ceil_div(x.nodes, span), p.members);
             tiles += seq_tiles<TILE>(p, x, span, nb);
             items += nb * p.nkv;
@@ -424,11 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
             }
         }
-        int64_t before = tiles;
+        int before = tiles;
         int items_before = items;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, before, m);
+            const int o = __shfl_up_sync(0xffffffffu, before, m);
             const int q = __shfl_up_sync(0xffffffffu, items_before, m);
             if (lane >= m) {
                 before += o;
@@ -444,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         before -= tiles;
         items_before -= items;
-        int64_t total = 0;
+        int total = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) {
                 before += bar.scan[w];
@@ -452,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             total += bar.scan[w];
         }
-        const int64_t per = (total + p.groups - 1) / p.groups;
+        const int per = ceil_div(total, p.groups);
         if (threadIdx.x == 0) {
             bar.start.total = total;
             bar.start.per = per;
@@ -461,26 +460,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p.header[1] = per;
             }
         }
-        const int64_t f0 = blockIdx.x / p.members * per;
+        const int f0 = static_cast<int>(blockIdx.x) / p.members * per;
         for (int s = s0; s < s1; ++s) {
-            const SeqInfo x = load_seq(p, s);
+            if (each > 1) x = load_seq(p, s);
             const int nb = ceil_div(ceil_div(x.nodes, span), p.members);
-            const int64_t n = seq_tiles<TILE>(p, x, span, nb);
+            const int n = seq_tiles<TILE>(p, x, span, nb);
             if (blockIdx.x == 0) {
                 p.seq_tiles[s] = before;
                 p.seq_items[s] = items_before;
             }
             if (before <= f0 && f0 < before + n) {
-                int64_t o = f0 - before;
+                int o = f0 - before;
                 int b = 0, bt = batch_tiles<TILE>(p, x, span, 0);
-                while (o >= static_cast<int64_t>(bt) * p.nkv) {
-                    o -= static_cast<int64_t>(bt) * p.nkv;
+                while (o >= bt * p.nkv) {
+                    o -= bt * p.nkv;
                     bt = batch_tiles<TILE>(p, x, span, ++b);
                 }
                 bar.start.s = s;
                 bar.start.b = b;
-                bar.start.h = static_cast<int>(o / bt);
-                bar.start.t = static_cast<int>(o % bt);
+                bar.start.h = o / bt;
+                bar.start.t = o % bt;
                 bar.start.item0 = items_before;
             }
             before += n;
@@ -708,7 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.0f;
             const int tiles = C::kOwnTiles ? (g.n - w + 1) / 2 : g.n;
             const int jobs = tiles * kJobs;
-            const int64_t unit0 = (g.f * p.members + walk.member) * NQ + (NQ == 2 ? w : 0);
+            const int64_t unit0 =
+                (static_cast<int64_t>(g.f) * p.members + walk.member) * NQ + (NQ == 2 ? w : 0);
             for (int j = 0; j < jobs; ++j) {
                 const int b = kBuffers == 2 ? j & 1 : 0, half = j % kJobs;
                 const int ti = C::kOwnTiles ? w + 2 * (j / kJobs) : j / kJobs;
@@ -911,17 +911,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The list position of (batch, head) of a sequence and its length in tiles.
 template <int TILE>
 __device__ __forceinline__ void item_range(const AttendParams& p, const SeqInfo& x, int span,
-                                           int64_t seq0, int b, int h, int64_t& f, int& n) {
+                                           int seq0, int b, int h, int& f, int& n) {
     f = seq0;
-    if (p.mask != nullptr) {
-        n = batch_tiles<TILE>(p, x, span, b);
-        f += static_cast<int64_t>(b) * p.nkv * n;
-    } else {
-        for (int k = 0; k < b; ++k)
-            f += static_cast<int64_t>(p.nkv) * batch_tiles<TILE>(p, x, span, k);
-        n = batch_tiles<TILE>(p, x, span, b);
-    }
-    f += static_cast<int64_t>(h) * n;
+    n = batch_tiles<TILE>(p, x, span, b);
+    if (p.mask != nullptr)
+        f += b * p.nkv * n;
+    else
+        for (int k = 0; k < b; ++k) f += p.nkv * batch_tiles<TILE>(p, x, span, k);
+    f += h * n;
 }
 
 // Joins the pieces of the rows.  A CTA takes 8 / WPR rows of one (sequence, row tile, head), WPR
@@ -929,8 +926,8 @@ __device__ __forceinline__ void item_range(const AttendParams& p, const SeqInfo&
 // are CTAs to share it) are spread over warps, so that their loads are in flight together; with
 // many rows a warp takes a row by itself.
 template <int HD, int NQ, int WPR>
-__global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row_tiles,
-                                                   int row_parts) {
+__device__ __forceinline__ void join_rows(const AttendParams& p, int block, int row_tiles,
+                                          int row_parts) {
     using C = Cfg<HD, NQ>;
     constexpr int TILE = C::kTile;
     constexpr int kEach = HD / 32;  // elements of a row per lane, in pairs
@@ -940,27 +937,24 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row
     __shared__ float sh_l[8], sh_top[8];
     const int span = NQ * p.nodes_tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int part = blockIdx.x % row_parts;
-    const int unit = blockIdx.x / row_parts;
+    const int part = block % row_parts;
+    const int unit = block / row_parts;
     const int rt = unit % row_tiles;
     const int h = unit / row_tiles % p.nkv;
     const int s = unit / row_tiles / p.nkv;
     const int sub = warp % WPR;
     const int r = part * (8 / WPR) + warp / WPR;
-    grid_dependency_wait();
-    grid_launch_dependents();
     const SeqInfo x = load_seq(p, s);
-    const int64_t seq0 = p.seq_tiles[s], per = p.header[1];
+    const int seq0 = p.seq_tiles[s], per = p.header[1];
     const int b = rt / p.members, member = rt % p.members;
     const int64_t item = p.seq_items[s] + b * p.nkv + h;
     const int rows = min(max(x.nodes - rt * span, 0), span) * p.g;
     const bool mine = r < rows;
     if (WPR == 1 && !mine) return;  // (with several warps a row, the CTA meets below)
-    int64_t f;
-    int n;
+    int f, n;
     item_range<TILE>(p, x, span, seq0, b, h, f, n);
-    const int64_t g0 = n > 0 ? f / per : 0, g1 = n > 0 ? (f + n - 1) / per : -1;
-    const int pieces = mine ? static_cast<int>(g1 - g0 + 1) * kPieceWidth : 0;
+    const int g0 = n > 0 ? f / per : 0, g1 = n > 0 ? (f + n - 1) / per : -1;
+    const int pieces = mine ? (g1 - g0 + 1) * kPieceWidth : 0;
     const int node = rt * span + r / p.g, head = h * p.g + r % p.g;
     const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
     const int lr = r - qt * p.nodes_tile * p.g;
@@ -970,21 +964,33 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row
         const int w = NQ == 2 ? qt : k % kPieceWidth;
         return ((item + g0 + grp) * p.members + member) * 2 + w;
     };
-    float top = -INFINITY;
+    float top = -INFINITY, l = 0.0f, acc[kEach];
     int bad = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) acc[i] = 0.0f;
     for (int k = sub + WPR * lane; k < pieces; k += 32 * WPR) {
         const int64_t sl = slot_of(k);
         const float2 ml = p.part_ml[sl * p.rowcap + lr];
         if (ml.y != 0.0f) top = fmaxf(top, ml.x);
         bad |= p.part_bad[sl];
     }
+    // The first pieces' O is on its way before their weights are known.
+    float2 v[kAtOnce][kEach / 2];
+    auto fetch = [&](int k0, int here) {
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+            if (q >= here) break;
+            const float2* o = reinterpret_cast<const float2*>(
+                p.part_o + (slot_of(k0 + WPR * q) * p.rowcap + lr) * HD);
+#pragma unroll
+            for (int i = 0; i < kEach / 2; ++i) v[q][i] = o[lane + 32 * i];
+        }
+    };
+    fetch(sub, (pieces - sub + WPR - 1) / WPR);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     bad = __any_sync(0xffffffffu, bad);
     const float base = top == -INFINITY ? 0.0f : top;
-    float l = 0.0f, acc[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) acc[i] = 0.0f;
     for (int k0 = sub; k0 < pieces; k0 += 32 * WPR) {
         float wt = 0.0f;
         if (k0 + WPR * lane < pieces) {
@@ -994,26 +1000,17 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row
         }
         const int here = min(32, (pieces - k0 + WPR - 1) / WPR);
         for (int k = 0; k < here; k += kAtOnce) {
-            float2 v[kAtOnce][kEach / 2];
-            float wk[kAtOnce];
+            if (k0 != sub || k != 0) fetch(k0 + WPR * k, here - k);
 #pragma unroll
             for (int q = 0; q < kAtOnce; ++q) {
-                wk[q] = __shfl_sync(0xffffffffu, wt, (k + q) & 31);
-                if (k + q >= here) wk[q] = 0.0f;
-                // (a piece without weight may hold anything)
-                const float2* o = reinterpret_cast<const float2*>(
-                    p.part_o + (slot_of(k0 + WPR * (k + q)) * p.rowcap + lr) * HD);
-#pragma unroll
-                for (int i = 0; i < kEach / 2; ++i)
-                    v[q][i] = wk[q] != 0.0f ? o[lane + 32 * i] : make_float2(0.0f, 0.0f);
-            }
-#pragma unroll
-            for (int q = 0; q < kAtOnce; ++q)
+                const float wk = __shfl_sync(0xffffffffu, wt, (k + q) & 31);
+                if (k + q >= here || wk == 0.0f) continue;  // without weight O may be anything
 #pragma unroll
                 for (int i = 0; i < kEach / 2; ++i) {
-                    acc[2 * i] += wk[q] * v[q][i].x;
-                    acc[2 * i + 1] += wk[q] * v[q][i].y;
+                    acc[2 * i] += wk * v[q][i].x;
+                    acc[2 * i + 1] += wk * v[q][i].y;
                 }
+            }
         }
     }
 #pragma unroll
@@ -1089,64 +1086,165 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row
     }
 }
 
-// One warp per table entry: the sums of its granules over heads, row tiles and rows, each scaled
-// by its row's exp2(m - lse).
-template <int HD, int NQ>
-__global__ void __launch_bounds__(256) weights_kernel(const AttendParams p) {
+template <int HD, int NQ, int WPR>
+__global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row_tiles,
+                                                   int row_parts) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    join_rows<HD, NQ, WPR>(p, blockIdx.x, row_tiles, row_parts);
+}
+
+// The weights of kEntries table entries from e on of a sequence, by one warp: the sums of their
+// granules over heads, row tiles and rows (over the lanes), each scaled by its row's exp2(m -
+// lse).  `row_lse(h, rt, qt, lr)` gives the log2 lse of a row.  Several entries at once, because
+// what an entry costs is the way of its loads.
+constexpr int kEntries = 4;
+
+template <int HD, int NQ, typename Lse>
+__device__ __forceinline__ void entry_weights(const AttendParams& p, const SeqInfo& x, int seq0,
+                                              int64_t e, Lse&& row_lse) {
     using C = Cfg<HD, NQ>;
     constexpr int TILE = C::kTile, kGran = TILE / 16, kJobs = C::kJobs;
     const int span = NQ * p.nodes_tile;
     const int lane = threadIdx.x & 31;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int64_t e = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (e >= p.total_blocks) return;
-    int lo = 0, hi = p.num_seqs;  // last s with seq_offsets[s] <= e
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (__ldg(p.seq_offsets + mid) <= e) lo = mid; else hi = mid;
-    }
-    const SeqInfo x = load_seq(p, lo);
     const int rts = ceil_div(x.nodes, span);
-    const int64_t seq0 = p.seq_tiles[lo];
-    const int item0 = p.seq_items[lo];
-    const int64_t pos0 = (e - x.e0) * p.bs;
-    float sum = 0.0f;
-    if (pos0 < x.tokens) {
-        const int left = static_cast<int>(min(static_cast<int64_t>(p.bs), x.tokens - pos0));
-        const int gr0 = static_cast<int>(pos0 / 16), grains = (left + 15) / 16;
-        for (int rt = 0; rt < rts; ++rt) {
-            // the (head, granule, row) triples of the row tile, over the lanes
-            const int bt = rt / p.members, member = rt % p.members;
-            const int mine = tiles_upto<TILE>(p, x, min(x.nodes, (rt + 1) * span));
-            const int rows = min(x.nodes - rt * span, span) * p.g;
-            const int each = rows * grains;
-            int64_t f0;
-            int n;
-            item_range<TILE>(p, x, span, seq0, bt, 0, f0, n);
-            for (int i = lane; i < each * p.nkv; i += 32) {
-                const int h = i / each, in = i - h * each;
-                const int gr = gr0 + in / rows, r = in % rows;
-                const int t = gr / kGran;
-                if (t >= mine) continue;
-                const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
-                const int lr = r - qt * p.nodes_tile * p.g;
-                const int64_t at =
-                    ((f0 + static_cast<int64_t>(h) * n + t) * p.members + member) * NQ + qt;
-                const int64_t row =
-                    (static_cast<int64_t>(item0 + bt * p.nkv + h) * p.members + member) * NQ + qt;
-                const float lse = p.row_lse[row * p.rowcap + lr];
-                const float m = p.sums_m[(at * kJobs + gr % kGran / 4) * p.rowcap + lr];
-                const float part = p.sums[(at * kGran + gr % kGran) * p.rowcap + lr];
-                if (lse == -INFINITY || part == 0.0f) continue;  // (m may then be anything)
-                sum += part * exp2f(-m - lse);
+    const int grains = p.bs / 16;
+    const int64_t gr0 = (e - x.e0) * grains;  // first granule of the first entry
+    const int last = (x.tokens + 15) / 16;    // granules that hold tokens
+    float sum[kEntries];
+#pragma unroll
+    for (int q = 0; q < kEntries; ++q) sum[q] = 0.0f;
+    for (int rt = 0; rt < rts; ++rt) {
+        const int bt = rt / p.members, member = rt % p.members;
+        const int seen = min(last, tiles_upto<TILE>(p, x, min(x.nodes, (rt + 1) * span)) * kGran);
+        const int rows = min(x.nodes - rt * span, span) * p.g;
+        int f0, n;
+        item_range<TILE>(p, x, span, seq0, bt, 0, f0, n);
+        for (int i = lane; i < rows * p.nkv; i += 32) {
+            const int h = i / rows, r = i - h * rows;
+            const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
+            const int lr = r - qt * p.nodes_tile * p.g;
+            const float lse = row_lse(h, rt, qt, lr);
+            for (int k = 0; k < grains; ++k) {
+                float m[kEntries], part[kEntries];
+#pragma unroll
+                for (int q = 0; q < kEntries; ++q) {
+                    const int64_t gr = gr0 + q * grains + k;
+                    part[q] = 0.0f;
+                    if (gr >= seen) continue;
+                    const int t = static_cast<int>(gr) / kGran, in = static_cast<int>(gr) % kGran;
+                    const int64_t at =
+                        (static_cast<int64_t>(f0 + h * n + t) * p.members + member) * NQ + qt;
+                    m[q] = p.sums_m[(at * kJobs + in / 4) * p.rowcap + lr];
+                    part[q] = p.sums[(at * kGran + in) * p.rowcap + lr];
+                }
+#pragma unroll
+                for (int q = 0; q < kEntries; ++q)  // (without weight m may be anything)
+                    if (part[q] != 0.0f && lse != -INFINITY) sum[q] += part[q] * exp2f(-m[q] - lse);
             }
         }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0)
-        p.weights_out[e] = (p.weights_in != nullptr ? p.weights_in[e] * p.decay : 0.0f) + sum;
+    for (int q = 0; q < kEntries; ++q) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], o);
+        if (lane == q && e + q < x.end)
+            p.weights_out[e + q] =
+                (p.weights_in != nullptr ? p.weights_in[e + q] * p.decay : 0.0f) + sum[q];
+    }
+}
+
+// The weights after the join, which has left every row's lse; a CTA takes a share of one
+// sequence's entries.
+template <int HD, int NQ>
+__global__ void __launch_bounds__(256) weights_kernel(const AttendParams p, int shares) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int s = blockIdx.x / shares, share = blockIdx.x % shares;
+    const SeqInfo x = load_seq(p, s);
+    const int item0 = p.seq_items[s], seq0 = p.seq_tiles[s];
+    const int warp = threadIdx.x >> 5;
+    for (int64_t e = x.e0 + (share * 8 + warp) * kEntries; e < x.end; e += shares * 8 * kEntries)
+        entry_weights<HD, NQ>(p, x, seq0, e, [&](int h, int rt, int qt, int lr) {
+            const int64_t row =
+                (static_cast<int64_t>(item0 + rt / p.members * p.nkv + h) * p.members +
+                 rt % p.members) * NQ + qt;
+            return p.row_lse[row * p.rowcap + lr];
+        });
+}
+
+// Join and weights in one launch, for one row tile (NQ 1, one member): the first CTAs join, the
+// others each take a share of one sequence's entries and work the rows' lse out for themselves
+// from the pieces' m and l, which for a few rows is quicker than waiting for the join.
+constexpr int kFewRows = 512;  // rows of a sequence, nodes times query heads
+
+template <int HD, int WPR>
+__global__ void __launch_bounds__(256) finish_kernel(const AttendParams p, int row_parts,
+                                                     int join_ctas, int shares) {
+    using C = Cfg<HD, 1>;
+    __shared__ float sh_lse[kFewRows];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (static_cast<int>(blockIdx.x) < join_ctas) {
+        join_rows<HD, 1, WPR>(p, blockIdx.x, 1, row_parts);
+        return;
+    }
+    const int s = (blockIdx.x - join_ctas) / shares, share = (blockIdx.x - join_ctas) % shares;
+    const int warp = threadIdx.x >> 5;
+    const SeqInfo x = load_seq(p, s);
+    const int seq0 = p.seq_tiles[s], per = p.header[1];
+    const int item0 = p.seq_items[s];
+    const int rows = x.nodes * p.g;  // of a head
+    const int entries = x.end - x.e0;
+    if (share * 8 * kEntries >= entries) return;
+    const int n = tiles_upto<C::kTile>(p, x, x.nodes);
+    // lse of row i = (head, row): as many lanes to a row as keep the CTA busy
+    const int all = rows * p.nkv;
+    const int lanes = all <= 8 ? 32 : all <= 16 ? 16 : all <= 32 ? 8 : all <= 64 ? 4 : 1;
+    const int per_pass = 256 / lanes;
+    for (int i0 = 0; i0 < all; i0 += per_pass) {
+        const int i = i0 + static_cast<int>(threadIdx.x) / lanes, at = threadIdx.x % lanes;
+        float top = -INFINITY, l = 0.0f;
+        if (i < all && n > 0) {
+            const int h = i / rows, lr = i % rows;
+            const int f = seq0 + h * n;
+            const int g0 = f / per, g1 = (f + n - 1) / per;
+            const int pieces = (g1 - g0 + 1) * C::kGroups;
+            for (int k0 = at; k0 < pieces; k0 += 8 * lanes) {
+                float2 ml[8];
+                float m = top;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int k = k0 + q * lanes;
+                    ml[q] = make_float2(-INFINITY, 0.0f);
+                    if (k >= pieces) continue;
+                    const int64_t slot =
+                        static_cast<int64_t>(item0 + h + g0 + k / C::kGroups) * 2 + k % C::kGroups;
+                    ml[q] = p.part_ml[slot * p.rowcap + lr];
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (ml[q].y != 0.0f) m = fmaxf(m, ml[q].x);
+                l = l != 0.0f ? l * exp2f(top - m) : 0.0f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (ml[q].y != 0.0f) l += ml[q].y * exp2f(ml[q].x - m);
+                top = m;
+            }
+        }
+        for (int o = 1; o < lanes; o <<= 1) {
+            const float ot = __shfl_xor_sync(0xffffffffu, top, o);
+            const float ol = __shfl_xor_sync(0xffffffffu, l, o);
+            const float m = fmaxf(top, ot);
+            l = (l != 0.0f ? l * exp2f(top - m) : 0.0f) + (ol != 0.0f ? ol * exp2f(ot - m) : 0.0f);
+            top = m;
+        }
+        if (i < all && at == 0) sh_lse[i] = l == 0.0f ? -INFINITY : top + log2f(l);
+    }
+    __syncthreads();
+    for (int64_t e = x.e0 + (share * 8 + warp) * kEntries; e < x.end; e += shares * 8 * kEntries)
+        entry_weights<HD, 1>(p, x, seq0, e,
+                             [&](int h, int, int, int lr) { return sh_lse[h * rows + lr]; });
 }
 
 // ------------------------------------------------------------------------------------- host
@@ -1201,8 +1299,8 @@ Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total
         at += up256(bytes);
         return here;
     };
-    p.header = take(16);
-    p.seq_tiles = take(static_cast<size_t>(num_seqs) * 8);
+    p.header = take(8);
+    p.seq_tiles = take(static_cast<size_t>(num_seqs) * 4);
     p.seq_items = take(static_cast<size_t>(num_seqs) * 4);
     p.part_bad = take(static_cast<size_t>(p.slots) * 4);
     p.part_ml = take(static_cast<size_t>(p.slots) * p.rowcap * 8);
@@ -1248,22 +1346,42 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
     if (launch_pdl(attend_kernel<HD, NQ>, dim3(plan.groups * plan.members), dim3(kThreads),
                    C::kSmemBytes, stream, mq, mk, mv, p) != cudaSuccess)
         return HSS_ERR_CUDA;
+    // Warps to a row: 8 while a CTA per row leaves SMs free (a lone sequence's 32 rows of 38
+    // pieces), else one.
+    const int unit_rows = std::min(p.max_q, NQ * plan.nodes_tile) * p.g;
+    const int64_t units = static_cast<int64_t>(plan.row_tiles) * p.nkv * p.num_seqs;
+    const bool few = units * unit_rows <= 2 * kCtas;
+    const int parts = few ? unit_rows : (unit_rows + 7) / 8;
+    const int64_t join_ctas = units * parts;
+    // CTAs to a sequence's entries: an even share of all entries in one pass, if the sequences
+    // are alike, within what the GPU holds at once.
+    const int64_t per_cta = 8 * kEntries;
+    const int64_t even = (p.total_blocks / std::max(p.num_seqs, 1) + per_cta) / per_cta;
+    const int64_t most = std::max<int64_t>(1, 8 * kCtas / std::max(p.num_seqs, 1));
+    const int shares = static_cast<int>(std::min(even, most));
+    if constexpr (NQ == 1) {
+        // One launch for both, while the rows' lse fit in shared memory.
+        if (rows && p.weights_out != nullptr && plan.row_tiles == 1 && p.num_seqs > 0 &&
+            static_cast<int64_t>(p.max_q) * p.nq <= kFewRows) {
+            const int64_t grid = join_ctas + static_cast<int64_t>(p.num_seqs) * shares;
+            if (grid > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
+            auto finish = few ? finish_kernel<HD, 8> : finish_kernel<HD, 1>;
+            if (launch_pdl(finish, dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, p,
+                           parts, static_cast<int>(join_ctas), shares) != cudaSuccess)
+                return HSS_ERR_CUDA;
+            return HSS_OK;
+        }
+    }
     if (rows) {
-        // Warps to a row: 8 while a CTA per row leaves SMs free (a lone sequence's 32 rows of 38
-        // pieces), else one.
-        const int unit_rows = std::min(p.max_q, NQ * plan.nodes_tile) * p.g;
-        const int64_t units = static_cast<int64_t>(plan.row_tiles) * p.nkv * p.num_seqs;
-        const bool few = units * unit_rows <= 2 * kCtas;
-        const int parts = few ? unit_rows : (unit_rows + 7) / 8;
-        if (units * parts > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
+        if (join_ctas > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
         auto join = few ? join_kernel<HD, NQ, 8> : join_kernel<HD, NQ, 1>;
-        if (launch_pdl(join, dim3(static_cast<unsigned>(units * parts)), dim3(256), 0, stream, p,
+        if (launch_pdl(join, dim3(static_cast<unsigned>(join_ctas)), dim3(256), 0, stream, p,
                        plan.row_tiles, parts) != cudaSuccess)
             return HSS_ERR_CUDA;
     }
     if (p.weights_out != nullptr &&
-        launch_pdl(weights_kernel<HD, NQ>, dim3(static_cast<unsigned>((p.total_blocks + 7) / 8)),
-                   dim3(256), 0, stream, p) != cudaSuccess)
+        launch_pdl(weights_kernel<HD, NQ>, dim3(static_cast<unsigned>(p.num_seqs * shares)),
+                   dim3(256), 0, stream, p, shares) != cudaSuccess)
         return HSS_ERR_CUDA;
     return HSS_OK;
 }
@@ -1282,6 +1400,7 @@ hss_status launch_attend(const AttendArgs& r, cudaStream_t stream) {
     const hss_dims& d = a.dims;
     const bool weigh = r.weights_out != nullptr;
     const Plan plan = make_plan(d, a.num_seqs, a.max_q, a.total_blocks, weigh);
+    if (plan.tiles > (1 << 30) || plan.slots > (1 << 30)) return HSS_ERR_INVALID_ARGUMENT;
     auto enc = tensor_map_encoder();
     if (enc == nullptr) return HSS_ERR_CUDA;
     AttendParams p;
@@ -1316,8 +1435,8 @@ hss_status launch_attend(const AttendArgs& r, cudaStream_t stream) {
     p.dev_status = a.dev_status;
     p.lib_error = dev->error_word;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    p.header = reinterpret_cast<int64_t*>(ws + plan.header);
-    p.seq_tiles = reinterpret_cast<int64_t*>(ws + plan.seq_tiles);
+    p.header = reinterpret_cast<int32_t*>(ws + plan.header);
+    p.seq_tiles = reinterpret_cast<int32_t*>(ws + plan.seq_tiles);
     p.seq_items = reinterpret_cast<int32_t*>(ws + plan.seq_items);
     p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
     p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
