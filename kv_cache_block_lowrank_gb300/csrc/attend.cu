@@ -139,10 +139,12 @@ __device__ __forceinline__ SeqInfo load_seq(const AttendParams& p, int s) {
 
 // Row tiles of a sequence are `span` nodes each (NQ tiles of 128 rows); `members` of them form a
 // batch.  A chain's rows see nothing past themselves, so its earlier batches have fewer tiles.
+__device__ __forceinline__ int tokens_upto(const AttendParams& p, const SeqInfo& x, int nodes) {
+    return max(p.mask == nullptr ? min(x.tokens - x.ctx, nodes) + x.ctx : x.tokens, 0);
+}
 template <int TILE>
 __device__ __forceinline__ int tiles_upto(const AttendParams& p, const SeqInfo& x, int nodes) {
-    const int seen = p.mask == nullptr ? min(x.tokens - x.ctx, nodes) + x.ctx : x.tokens;
-    return (max(min(seen, x.tokens), 0) + TILE - 1) / TILE;
+    return (tokens_upto(p, x, nodes) + TILE - 1) / TILE;
 }
 template <int TILE>
 __device__ __forceinline__ int batch_tiles(const AttendParams& p, const SeqInfo& x, int span,
@@ -169,6 +171,7 @@ struct Start {
 struct Segment {
     SeqInfo x;
     int h, rt, ta, n, item;
+    int seen;   // tokens that some row of the row tile may see
     bool rows;  // the row tile exists
     int f;      // list index of tile ta
 };
@@ -206,7 +209,8 @@ struct Walk {
                 g.rt = b * p.members + member;
                 g.rows = g.rt < rts;
                 g.ta = t;
-                const int mine = g.rows ? tiles_upto<TILE>(p, x, min(x.nodes, (g.rt + 1) * span)) : 0;
+                g.seen = g.rows ? tokens_upto(p, x, min(x.nodes, (g.rt + 1) * span)) : 0;
+                const int mine = (g.seen + TILE - 1) / TILE;
                 g.n = max(0, min(t + take, mine) - t);
                 g.item = item0 + b * p.nkv + h;
                 g.f = f;
@@ -226,6 +230,15 @@ struct Walk {
         return false;
     }
 };
+
+// A group's jobs in a piece: two per tile, but for a last half tile that nobody sees.
+template <class C>
+__device__ __forceinline__ int jobs_of(const Segment& g, int group, int& tiles) {
+    tiles = C::kOwnTiles ? (g.n - group + 1) / 2 : g.n;
+    if (tiles == 0) return 0;
+    const int last = g.ta + (C::kOwnTiles ? group + 2 * (tiles - 1) : tiles - 1);
+    return tiles * C::kJobs - (C::kJobs == 2 && last * C::kTile + 64 >= g.seen ? 1 : 0);
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -326,19 +339,22 @@ __device__ __forceinline__ uint64_t node_word(const AttendParams& p, const SeqIn
     return __ldg(p.mask + (static_cast<int64_t>(x.q0) + node) * p.mask_words + w);
 }
 
-// Visibility of the 32 tokens from position p0 on for a row.
+// Visibility of the 32 tokens from position p0 on for a row, whose first two words are given.
 __device__ __forceinline__ uint32_t visible32(const AttendParams& p, const SeqInfo& x, int node,
-                                              int p0) {
+                                              int p0, uint64_t word0, uint64_t word1) {
+    auto word = [&](int w) {
+        return w == 0 ? word0 : (w == 1 ? word1 : node_word(p, x, node, w));
+    };
     uint32_t bits;
     const int j0 = p0 - x.ctx;
     if (j0 <= -32) {
         bits = 0xFFFFFFFFu;
     } else if (j0 < 0) {
-        bits = (static_cast<uint32_t>(node_word(p, x, node, 0)) << -j0) | ((1u << -j0) - 1);
+        bits = (static_cast<uint32_t>(word0) << -j0) | ((1u << -j0) - 1);
     } else {
         const int w = j0 >> 6, sh = j0 & 63;
-        uint64_t v = node_word(p, x, node, w) >> sh;
-        if (sh > 32) v |= node_word(p, x, node, w + 1) << (64 - sh);
+        uint64_t v = word(w) >> sh;
+        if (sh > 32 && 64 * (w + 1) < x.nodes) v |= word(w + 1) << (64 - sh);
         bits = static_cast<uint32_t>(v);
     }
     const int left = x.tokens - p0;
@@ -609,14 +625,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t dv = smem_desc_128b(smem_u32(sKV), kChunks * 1024, 1024);
             const uint32_t d_s = tmem + w * (kBuffers * 64);
             const uint32_t d_o = tmem + C::kOCols + w * HD;
-            uint32_t tile = 0, segs = 0, np[2] = {0, 0};
+            uint32_t tile = 0, segs = 0, taken = 0;  // taken: bit b, parity of buffer b's next weights
             bool ok = true;
             while (ok && walk.next(p, g)) {
                 if (g.n == 0) continue;
                 if (!(ok = wait_phase(&bar.q_full, segs & 1, abort_flag))) break;
                 ++segs;
-                const int tiles = C::kOwnTiles ? (g.n - w + 1) / 2 : g.n;
-                const int jobs = tiles * kJobs;
+                int tiles;
+                const int jobs = jobs_of<C>(g, w, tiles);
                 if (jobs == 0) mbar_arrive(&bar.q_empty);
                 int sk = 0, sv = 0;  // the stages of the tile that each product is on
                 auto stage_of = [&](bool v, int j, int& st) {
@@ -636,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     umma_commit(&bar.s_full[w * kBuffers + b]);
                 };
                 auto scored = [&](int j) {  // releases behind the scores
-                    if (j % kJobs == kJobs - 1) umma_commit(&bar.empty[sk]);
+                    if (j % kJobs == kJobs - 1 || j == jobs - 1) umma_commit(&bar.empty[sk]);
                     if (j == jobs - 1) umma_commit(&bar.q_empty);
                 };
                 for (int j = 0; j < kBuffers && j < jobs && ok; ++j) {
@@ -654,9 +670,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool more = j + kBuffers < jobs;
                     stage_of(true, j, sv);
                     if (more) stage_of(false, j + kBuffers, sk);
-                    ok = ok && wait_phase(&bar.p_full[w * kBuffers + b], np[b] & 1, abort_flag);
+                    ok = ok && wait_phase(&bar.p_full[w * kBuffers + b], (taken >> b) & 1, abort_flag);
                     if (!ok) break;
-                    ++np[b];
+                    taken ^= 1u << b;
                     tc_fence_after_sync();
                     const uint64_t v =
                         dv + static_cast<uint32_t>((sv * C::kStageBytes +
@@ -667,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      idesc_o, j > 0 || s > 0);
                     if (more) score(j + kBuffers);
                     umma_commit(&bar.o_done[w * kBuffers + b]);
-                    if (j % kJobs == kJobs - 1) umma_commit(&bar.empty[sv]);
+                    if (j % kJobs == kJobs - 1 || j == jobs - 1) umma_commit(&bar.empty[sv]);
                     if (more) scored(j + kBuffers);
                 }
                 tile += tiles;
@@ -682,7 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t o_cols = lanes + C::kOCols + w * HD;
         const int gt = quarter * 32 + lane;  // thread of the group
-        uint32_t tile = 0, segs = 0, ns[2] = {0, 0}, given[2] = {0, 0}, values = 0;
+        uint32_t tile = 0, segs = 0, values = 0;
+        uint32_t next = 0, given = 0;  // bit b: parity of buffer b's next scores, next weights
         bool ok = true;
         walk.begin(p, bar.start, span);
         if (w >= NG) walk.f = walk.f1;
@@ -694,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // takes weights that this warp has not given; the one before was issued two jobs ago,
         // before scores that this warp has seen.  Hence a barrier for each buffer.
         auto product_done = [&](int b) -> bool {
-            const bool got = wait(&bar.o_done[w * kBuffers + b], (given[b] - 1) & 1);
+            const bool got = wait(&bar.o_done[w * kBuffers + b], ((given >> b) & 1) ^ 1u);
             tc_fence_after_sync();
             return got;
         };
@@ -705,16 +722,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool warp_live = quarter * 32 < live;
             const int node = first + row / p.g;
             float m = -INFINITY, l = 0.0f;
-            const int tiles = C::kOwnTiles ? (g.n - w + 1) / 2 : g.n;
-            const int jobs = tiles * kJobs;
+            int tiles;
+            const int jobs = jobs_of<C>(g, w, tiles);
+            // The row's first two mask words, on their way before they are needed.
+            uint64_t word0 = 0, word1 = 0;
+            if (row < live && (g.ta + g.n) * TILE > x.ctx) {
+                word0 = node_word(p, x, node, 0);
+                if (x.nodes > 64) word1 = node_word(p, x, node, 1);
+            }
             const int64_t unit0 =
                 (static_cast<int64_t>(g.f) * p.members + walk.member) * NQ + (NQ == 2 ? w : 0);
             for (int j = 0; j < jobs; ++j) {
                 const int b = kBuffers == 2 ? j & 1 : 0, half = j % kJobs;
                 const int ti = C::kOwnTiles ? w + 2 * (j / kJobs) : j / kJobs;
                 const int pos0 = (g.ta + ti) * TILE + 64 * half;
-                if (!(ok = wait(&bar.s_full[w * kBuffers + b], ns[b] & 1))) break;
-                ++ns[b];
+                if (!(ok = wait(&bar.s_full[w * kBuffers + b], (next >> b) & 1))) break;
+                next ^= 1u << b;
                 tc_fence_after_sync();
                 const uint32_t bad =
                     *(volatile uint32_t*)&bar.bad_ids[C::kOwnTiles ? w : 0]
@@ -732,33 +755,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                          k += NQ == 2 ? 256 : 128) {
                         const int r = k % 64, ch = k / 64;
                         if (pos0 + r < x.ctx) continue;
-#pragma unroll 2
+                        uint8_t* at = part + ((r >> 3) * kChunks + ch) * 1024;
+                        if (pos0 + r >= x.tokens) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<uint4*>(at + swizzled_offset(r & 7, 16 * e, 128)) =
+                                    make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        uint4 q[8];
+                        uint32_t most = 0;  // the largest exponent field, twice in a word
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            q[e] = *reinterpret_cast<const uint4*>(
+                                at + swizzled_offset(r & 7, 16 * e, 128));
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            most = __vmaxu2(__vmaxu2(most, __vmaxu2(q[e].x & 0x7FFF7FFFu,
+                                                                    q[e].y & 0x7FFF7FFFu)),
+                                            __vmaxu2(q[e].z & 0x7FFF7FFFu, q[e].w & 0x7FFF7FFFu));
+                        if (max(most & 0xFFFFu, most >> 16) < 0x7F80u) continue;
+                        found = true;
+#pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            uint4* at = reinterpret_cast<uint4*>(
-                                part + ((r >> 3) * kChunks + ch) * 1024 +
-                                swizzled_offset(r & 7, 16 * e, 128));
-                            if (pos0 + r >= x.tokens) {
-                                *at = make_uint4(0, 0, 0, 0);
-                                continue;
-                            }
-                            uint4 v = *at;
-                            uint32_t* u = &v.x;
-                            bool hit = false;
+                            uint32_t* u = &q[e].x;
 #pragma unroll
                             for (int d = 0; d < 4; ++d) {
-                                if ((u[d] & 0x7F80u) == 0x7F80u) {
-                                    u[d] &= 0xFFFF0000u;
-                                    hit = true;
-                                }
-                                if ((u[d] & 0x7F800000u) == 0x7F800000u) {
-                                    u[d] &= 0x0000FFFFu;
-                                    hit = true;
-                                }
+                                if ((u[d] & 0x7F80u) == 0x7F80u) u[d] &= 0xFFFF0000u;
+                                if ((u[d] & 0x7F800000u) == 0x7F800000u) u[d] &= 0x0000FFFFu;
                             }
-                            if (hit) {
-                                *at = v;
-                                found = true;
-                            }
+                            *reinterpret_cast<uint4*>(at + swizzled_offset(r & 7, 16 * e, 128)) =
+                                q[e];
                         }
                     }
                     if (found) {
@@ -791,7 +818,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         top = -INFINITY;
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            uint32_t bits = row < live ? visible32(p, x, node, pos0 + 32 * k) : 0u;
+                            uint32_t bits = row < live ? visible32(p, x, node, pos0 + 32 * k, word0, word1)
+                                                  : 0u;
                             if ((bad >> (2 * k)) & 1) bits &= 0xFFFF0000u;
                             if ((bad >> (2 * k)) & 2) bits &= 0x0000FFFFu;
 #pragma unroll
@@ -862,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[w * kBuffers + b]);
-                ++given[b];
+                given ^= 1u << b;
             }
             if (!ok) break;
             // What this piece of the sequence came to.
@@ -1110,13 +1138,13 @@ __device__ __forceinline__ void entry_weights(const AttendParams& p, const SeqIn
     const int rts = ceil_div(x.nodes, span);
     const int grains = p.bs / 16;
     const int64_t gr0 = (e - x.e0) * grains;  // first granule of the first entry
-    const int last = (x.tokens + 15) / 16;    // granules that hold tokens
     float sum[kEntries];
 #pragma unroll
     for (int q = 0; q < kEntries; ++q) sum[q] = 0.0f;
     for (int rt = 0; rt < rts; ++rt) {
         const int bt = rt / p.members, member = rt % p.members;
-        const int seen = min(last, tiles_upto<TILE>(p, x, min(x.nodes, (rt + 1) * span)) * kGran);
+        // granules that the row tile looked at
+        const int seen = (tokens_upto(p, x, min(x.nodes, (rt + 1) * span)) + 15) / 16;
         const int rows = min(x.nodes - rt * span, span) * p.g;
         int f0, n;
         item_range<TILE>(p, x, span, seq0, bt, 0, f0, n);
