@@ -389,7 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sKV = sQ + C::kQBytes;
     Barriers& bar = *reinterpret_cast<Barriers*>(sKV + C::kStages * C::kStageBytes);
     static_assert(sizeof(Barriers) <= 1024, "barrier block");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (a shuffle, so that the compiler knows the roles' branches to be the whole warp's)
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
     const int span = NQ * p.nodes_tile;
 
     if (warp == 2) {
@@ -613,47 +615,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                 (void)mbar_wait_for(&bar.q_full, (segs - 1) & 1, ok ? kWaitLimitNs : 1000000);
                 if (ok) (void)mbar_wait(&bar.q_empty, (segs - 1) & 1);
             }
-        } else if (warp - 2 < NG && lane == 0) {
+        } else if (warp - 2 < NG) {
             // ------------------------------------------------------------ products of group w
             const int w = warp - 2;
             constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, 64);
             constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, HD) | (1u << 16);  // V: MN-major
             constexpr uint32_t kJobBytes = 64 * HD * 2;  // a job's part of a stage
+            const uint32_t leader = elect_one();
+            // Descriptors: the high words do not change, the low ones by (offset >> 4) only.
             const uint64_t dq = smem_desc_kmajor(smem_u32(sQ), 128) +
                                 (NQ == 2 ? w * (kRows * HD * 2 >> 4) : 0);
             const uint64_t dk = smem_desc_128b(smem_u32(sKV), kChunks * 1024, 0);
             const uint64_t dv = smem_desc_128b(smem_u32(sKV), kChunks * 1024, 1024);
+            const uint32_t q_lo = static_cast<uint32_t>(dq), q_hi = static_cast<uint32_t>(dq >> 32);
+            const uint32_t k_lo = static_cast<uint32_t>(dk), k_hi = static_cast<uint32_t>(dk >> 32);
+            const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
             const uint32_t d_s = tmem + w * (kBuffers * 64);
             const uint32_t d_o = tmem + C::kOCols + w * HD;
             uint32_t tile = 0, segs = 0, taken = 0;  // taken: bit b, parity of buffer b's next weights
             bool ok = true;
             while (ok && walk.next(p, g)) {
                 if (g.n == 0) continue;
-                if (!(ok = wait_phase(&bar.q_full, segs & 1, abort_flag))) break;
+                if (!(ok = wait(&bar.q_full, segs & 1))) break;
                 ++segs;
                 int tiles;
-                const int jobs = jobs_of<C>(g, w, tiles);
-                if (jobs == 0) mbar_arrive(&bar.q_empty);
+                const int jobs = __shfl_sync(0xffffffffu, jobs_of<C>(g, w, tiles), 0);
+                if (jobs == 0 && leader) mbar_arrive(&bar.q_empty);
+                __syncwarp();
                 int sk = 0, sv = 0;  // the stages of the tile that each product is on
                 auto stage_of = [&](bool v, int j, int& st) {
+                    if (j % kJobs != 0) return;
                     uint32_t par;
                     place<C>(v, w, tile + j / kJobs, st, par);
-                    if (j % kJobs == 0) ok = ok && wait_phase(&bar.full[st], par, abort_flag);
+                    st = __shfl_sync(0xffffffffu, st, 0);
+                    ok = ok && wait(&bar.full[st], par);
                 };
                 auto score = [&](int j) {
                     const int b = kBuffers == 2 ? j & 1 : 0;
-                    const uint64_t k =
-                        dk + static_cast<uint32_t>((sk * C::kStageBytes +
-                                                    (j % kJobs) * kJobBytes) >> 4);
+                    const uint32_t k =
+                        k_lo + ((sk * C::kStageBytes + (j % kJobs) * kJobBytes) >> 4);
 #pragma unroll
                     for (int s = 0; s < HD / 16; ++s)
-                        umma_bf16(d_s + 64 * b, dq + (s >> 2) * (kRows * 128 >> 4) + 2 * (s & 3),
-                                  k + (s >> 2) * (1024 >> 4) + 2 * (s & 3), idesc_s, s > 0);
-                    umma_commit(&bar.s_full[w * kBuffers + b]);
+                        umma_bf16_warp(leader, d_s + 64 * b,
+                                       q_lo + (s >> 2) * (kRows * 128 >> 4) + 2 * (s & 3), q_hi,
+                                       k + (s >> 2) * (1024 >> 4) + 2 * (s & 3), k_hi, idesc_s,
+                                       s > 0);
+                    umma_commit_warp(leader, &bar.s_full[w * kBuffers + b]);
                 };
                 auto scored = [&](int j) {  // releases behind the scores
-                    if (j % kJobs == kJobs - 1 || j == jobs - 1) umma_commit(&bar.empty[sk]);
-                    if (j == jobs - 1) umma_commit(&bar.q_empty);
+                    if (j % kJobs == kJobs - 1 || j == jobs - 1)
+                        umma_commit_warp(leader, &bar.empty[sk]);
+                    if (j == jobs - 1) umma_commit_warp(leader, &bar.q_empty);
                 };
                 for (int j = 0; j < kBuffers && j < jobs && ok; ++j) {
                     stage_of(false, j, sk);
@@ -670,20 +682,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool more = j + kBuffers < jobs;
                     stage_of(true, j, sv);
                     if (more) stage_of(false, j + kBuffers, sk);
-                    ok = ok && wait_phase(&bar.p_full[w * kBuffers + b], (taken >> b) & 1, abort_flag);
+                    ok = ok && wait(&bar.p_full[w * kBuffers + b], (taken >> b) & 1);
                     if (!ok) break;
                     taken ^= 1u << b;
                     tc_fence_after_sync();
-                    const uint64_t v =
-                        dv + static_cast<uint32_t>((sv * C::kStageBytes +
-                                                    (j % kJobs) * kJobBytes) >> 4);
+                    const uint32_t v =
+                        v_lo + ((sv * C::kStageBytes + (j % kJobs) * kJobBytes) >> 4);
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        umma_bf16_ts(d_o, d_s + 64 * b + 8 * s, v + s * (2 * kChunks * 1024 >> 4),
-                                     idesc_o, j > 0 || s > 0);
+                        umma_bf16_ts_warp(leader, d_o, d_s + 64 * b + 8 * s,
+                                          v + s * (2 * kChunks * 1024 >> 4), v_hi, idesc_o,
+                                          j > 0 || s > 0);
                     if (more) score(j + kBuffers);
-                    umma_commit(&bar.o_done[w * kBuffers + b]);
-                    if (j % kJobs == kJobs - 1 || j == jobs - 1) umma_commit(&bar.empty[sv]);
+                    umma_commit_warp(leader, &bar.o_done[w * kBuffers + b]);
+                    if (j % kJobs == kJobs - 1 || j == jobs - 1)
+                        umma_commit_warp(leader, &bar.empty[sv]);
                     if (more) scored(j + kBuffers);
                 }
                 tile += tiles;
