@@ -694,7 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           v + s * (2 * kChunks * 1024 >> 4), v_hi, idesc_o,
                                           j > 0 || s > 0);
                     if (more) score(j + kBuffers);
-                    umma_commit_warp(leader, &bar.o_done[w * kBuffers + b]);
+                    // (before the last jobs, the scores just issued will say as much)
+                    if (!more) umma_commit_warp(leader, &bar.o_done[w * kBuffers + b]);
                     if (j % kJobs == kJobs - 1 || j == jobs - 1)
                         umma_commit_warp(leader, &bar.empty[sv]);
                     if (more) scored(j + kBuffers);
@@ -712,21 +713,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t o_cols = lanes + C::kOCols + w * HD;
         const int gt = quarter * 32 + lane;  // thread of the group
         uint32_t tile = 0, segs = 0, values = 0;
-        uint32_t next = 0, given = 0;  // bit b: parity of buffer b's next scores, next weights
+        uint32_t next = 0, ends = 0;  // bit b: parity of buffer b's next scores, next end of a piece
         bool ok = true;
         walk.begin(p, bar.start, span);
         if (w >= NG) walk.f = walk.f1;
         auto wait = [&](uint64_t* b, uint32_t parity) {
             return __all_sync(0xffffffffu, wait_phase(b, parity, abort_flag)) != 0;
-        };
-        // Waits until the product with buffer b's last weights is done.  A parity names a phase
-        // only if the phase before it has completed and the one after has not.  The one after
-        // takes weights that this warp has not given; the one before was issued two jobs ago,
-        // before scores that this warp has seen.  Hence a barrier for each buffer.
-        auto product_done = [&](int b) -> bool {
-            const bool got = wait(&bar.o_done[w * kBuffers + b], ((given >> b) & 1) ^ 1u);
-            tc_fence_after_sync();
-            return got;
         };
         while (ok && walk.next(p, g)) {
             const SeqInfo& x = g.x;
@@ -849,8 +841,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool grow = top > m + kLazy || m == -INFINITY;
                     const float m_new = grow ? fmaxf(top, m) : m;
                     if (__any_sync(0xffffffffu, grow && j > 0)) {
-                        // The product before has to be done with O.
-                        if (!(ok = product_done(kBuffers == 2 ? b ^ 1 : 0))) break;
+                        // The product before has to be done with O.  What was issued after it
+                        // tells: with one buffer these scores, with two the next ones.  (A parity
+                        // names a phase only if the one before it has completed and the one after
+                        // has not: this warp has seen the scores before, and those after wait for
+                        // weights that it has not given.)
+                        if (kBuffers == 2) {
+                            const int o = b ^ 1;
+                            ok = j + 1 < jobs ? wait(&bar.s_full[w * 2 + o], (next >> o) & 1)
+                                              : wait(&bar.o_done[w * 2 + o], (ends >> o) & 1);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                        }
                         const float shrink =
                             grow ? (m == -INFINITY ? 0.0f : ex2(m - m_new)) : 1.0f;
                         l *= shrink;
@@ -903,7 +905,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[w * kBuffers + b]);
-                given ^= 1u << b;
             }
             if (!ok) break;
             // What this piece of the sequence came to.
@@ -912,9 +913,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     (static_cast<int64_t>(g.item + blockIdx.x / p.members) * p.members +
                      walk.member) * 2 + w;
                 if (jobs > 0) {
-                    if (!(ok = product_done(0)) || (jobs > 1 && kBuffers == 2 &&
-                                                    !(ok = product_done(1))))
-                        break;
+                    const int b = kBuffers == 2 ? (jobs - 1) & 1 : 0;  // the last product
+                    if (!(ok = wait(&bar.o_done[w * kBuffers + b], (ends >> b) & 1))) break;
+                    tc_fence_after_sync();
                     float* to = p.part_o + (slot * p.rowcap + row) * HD;
 #pragma unroll
                     for (int k = 0; k < HD; k += 32) {
@@ -936,6 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                        static_cast<int>(segs);
             }
             if (g.n > 0) ++segs;
+            ends ^= jobs > 1 && kBuffers == 2 ? 3u : (jobs > 0 ? 1u : 0u);
             tile += tiles;
         }
         if (!ok) give_up();
