@@ -177,7 +177,7 @@ def _stream(stream) -> Optional[int]:
         # torch.cuda.current_stream().cuda_stream without building a Stream object.
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is not None:
-            return raw(torch.cuda.current_device())
+            return raw(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

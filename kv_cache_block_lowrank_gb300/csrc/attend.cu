@@ -964,10 +964,52 @@ __device__ __forceinline__ void item_range(const AttendParams& p, const SeqInfo&
     f += h * n;
 }
 
-// Joins the pieces of the rows.  A CTA takes 8 / WPR rows of one (sequence, row tile, head), WPR
-// warps to a row: with few rows the pieces of a row (a long sequence is cut into as many as there
-// are CTAs to share it) are spread over warps, so that their loads are in flight together; with
-// many rows a warp takes a row by itself.
+// Adds the non-finite values of the nodes a row sees.
+template <int HD>
+__device__ __forceinline__ void add_bad_values(const AttendParams& p, const SeqInfo& x, int node, int h,
+                                            float* acc) {
+    const int lane = threadIdx.x & 31;
+    for (int j = 0; j < x.nodes; ++j) {
+        if (x.ctx + j >= x.tokens) break;
+        if (!((node_word(p, x, node, j >> 6) >> (j & 63)) & 1)) continue;
+        const int pos = x.ctx + j;
+        const int64_t id = p.table[x.e0 + pos / p.bs];
+        if (id < 0 || id >= p.max_blocks) continue;
+        const uint32_t* v = reinterpret_cast<const uint32_t*>(
+            p.V + ((id * p.bs + pos % p.bs) * p.nkv + h) * HD);
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i) {
+            const uint32_t u = v[lane + 32 * i];
+            const float lo = __uint_as_float(u << 16);
+            const float hi = __uint_as_float(u & 0xFFFF0000u);
+            if (!isfinite(lo)) acc[2 * i] += lo;
+            if (!isfinite(hi)) acc[2 * i + 1] += hi;
+        }
+    }
+}
+
+// A joined row: out, lse, and for the weights its log2 lse.
+template <int HD>
+__device__ __forceinline__ void write_row(const AttendParams& p, const SeqInfo& x, int node,
+                                          int head, float m, float l, const float* acc,
+                                          int64_t lse_at) {
+    const int lane = threadIdx.x & 31;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t at = (static_cast<int64_t>(x.q0) + node) * p.nq + head;
+    uint32_t* to = reinterpret_cast<uint32_t*>(p.out + at * HD);
+#pragma unroll
+    for (int i = 0; i < HD / 64; ++i)
+        to[lane + 32 * i] = l == 0.0f ? 0u : pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    if (lane == 0) {
+        const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+        if (p.lse != nullptr) p.lse[at] = lse2 * 0.693147180559945309f;
+        if (p.sums != nullptr) p.row_lse[lse_at] = lse2;
+    }
+}
+
+// Joins the pieces of the rows.  Few rows: a CTA takes 8 / WPR rows of one (sequence, row tile,
+// head), WPR warps to a row, so that the pieces of a row (a long sequence is cut into as many as
+// there are CTAs to share it) are on their way together.
 template <int HD, int NQ, int WPR>
 __device__ __forceinline__ void join_rows(const AttendParams& p, int block, int row_tiles,
                                           int row_parts) {
@@ -993,12 +1035,11 @@ __device__ __forceinline__ void join_rows(const AttendParams& p, int block, int 
     const int64_t item = p.seq_items[s] + b * p.nkv + h;
     const int rows = min(max(x.nodes - rt * span, 0), span) * p.g;
     const bool mine = r < rows;
-    if (WPR == 1 && !mine) return;  // (with several warps a row, the CTA meets below)
     int f, n;
     item_range<TILE>(p, x, span, seq0, b, h, f, n);
     const int g0 = n > 0 ? f / per : 0, g1 = n > 0 ? (f + n - 1) / per : -1;
     const int pieces = mine ? (g1 - g0 + 1) * kPieceWidth : 0;
-    const int node = rt * span + r / p.g, head = h * p.g + r % p.g;
+    const int node = rt * span + r / p.g;
     const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
     const int lr = r - qt * p.nodes_tile * p.g;
     // piece k of the row -> slot
@@ -1095,37 +1136,103 @@ __device__ __forceinline__ void join_rows(const AttendParams& p, int block, int 
             }
         }
     }
-    if (bad) {
-        // Non-finite values of the nodes this row sees.
-        for (int j = 0; j < x.nodes; ++j) {
-            if (x.ctx + j >= x.tokens) break;
-            if (!((node_word(p, x, node, j >> 6) >> (j & 63)) & 1)) continue;
-            const int pos = x.ctx + j;
-            const int64_t id = p.table[x.e0 + pos / p.bs];
-            if (id < 0 || id >= p.max_blocks) continue;
-            const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                p.V + ((id * p.bs + pos % p.bs) * p.nkv + h) * HD);
+    if (bad) add_bad_values<HD>(p, x, node, h, acc);
+    write_row<HD>(p, x, node, h * p.g + r % p.g, m, l, acc,
+                  ((item * p.members + member) * NQ + qt) * p.rowcap + lr);
+}
+
+// Many rows: a warp takes four rows of one (sequence, row tile, head) at a time, eight lanes a row
+// for its pieces' m and l, so that the loads of several rows are in flight together.
+template <int HD, int NQ>
+__device__ __forceinline__ void join_many(const AttendParams& p, int block, int row_tiles,
+                                          int row_parts) {
+    using C = Cfg<HD, NQ>;
+    constexpr int TILE = C::kTile;
+    constexpr int kEach = HD / 32;
+    constexpr int kPieceWidth = NQ == 1 ? C::kGroups : 1;
+    const int span = NQ * p.nodes_tile;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = block % row_parts, unit = block / row_parts;
+    const int rt = unit % row_tiles, h = unit / row_tiles % p.nkv, s = unit / row_tiles / p.nkv;
+    const int r0 = part * 32 + warp * 4;
+    const SeqInfo x = load_seq(p, s);
+    const int seq0 = p.seq_tiles[s], per = p.header[1];
+    const int b = rt / p.members, member = rt % p.members;
+    const int64_t item = p.seq_items[s] + b * p.nkv + h;
+    const int rows = min(max(x.nodes - rt * span, 0), span) * p.g;
+    if (r0 >= rows) return;
+    int f, n;
+    item_range<TILE>(p, x, span, seq0, b, h, f, n);
+    const int g0 = n > 0 ? f / per : 0, g1 = n > 0 ? (f + n - 1) / per : -1;
+    const int pieces = (g1 - g0 + 1) * kPieceWidth;
+    auto place_of = [&](int r, int k) -> int64_t {  // row r's piece k, in rows of the workspace
+        const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
+        const int w = NQ == 2 ? qt : k % kPieceWidth;
+        return (((item + g0 + k / kPieceWidth) * p.members + member) * 2 + w) * p.rowcap +
+               (r - qt * p.nodes_tile * p.g);
+    };
+    // m of the row: lane 8 q + i looks at pieces i, i + 8, ... of row r0 + q
+    const int my_row = min(r0 + lane / 8, rows - 1);
+    float top = -INFINITY, l = 0.0f;
+    int bad = 0;
+    for (int k = lane % 8; k < pieces; k += 8) {
+        const int64_t at = place_of(my_row, k);
+        const float2 ml = p.part_ml[at];
+        bad |= p.part_bad[at / p.rowcap];
+        if (ml.y != 0.0f) top = fmaxf(top, ml.x);
+    }
 #pragma unroll
-            for (int i = 0; i < kEach / 2; ++i) {
-                const uint32_t u = v[lane + 32 * i];
-                const float lo = __uint_as_float(u << 16);
-                const float hi = __uint_as_float(u & 0xFFFF0000u);
-                if (!isfinite(lo)) acc[2 * i] += lo;
-                if (!isfinite(hi)) acc[2 * i + 1] += hi;
+    for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float acc[4][kEach];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) acc[q][i] = 0.0f;
+    for (int k0 = 0; k0 < pieces; k0 += 8) {
+        float wt = 0.0f;
+        if (k0 + lane % 8 < pieces) {
+            const float2 ml = p.part_ml[place_of(my_row, k0 + lane % 8)];
+            wt = ml.y != 0.0f ? exp2f(ml.x - base) : 0.0f;
+            l += ml.y != 0.0f ? wt * ml.y : 0.0f;
+        }
+        const int here = min(8, pieces - k0);
+        for (int k = 0; k < here; ++k) {
+            float2 v[4][kEach / 2];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2* o = reinterpret_cast<const float2*>(
+                    p.part_o + place_of(min(r0 + q, rows - 1), k0 + k) * HD);
+#pragma unroll
+                for (int i = 0; i < kEach / 2; ++i) v[q][i] = __ldcg(o + lane + 32 * i);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float wk = __shfl_sync(0xffffffffu, wt, 8 * q + k);
+                if (wk == 0.0f) continue;  // without weight O may be anything
+#pragma unroll
+                for (int i = 0; i < kEach / 2; ++i) {
+                    acc[q][2 * i] += wk * v[q][i].x;
+                    acc[q][2 * i + 1] += wk * v[q][i].y;
+                }
             }
         }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t at = (static_cast<int64_t>(x.q0) + node) * p.nq + head;
-    uint32_t* to = reinterpret_cast<uint32_t*>(p.out + at * HD);
 #pragma unroll
-    for (int i = 0; i < kEach / 2; ++i)
-        to[lane + 32 * i] = l == 0.0f ? 0u : pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    if (lane == 0) {
-        const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
-        if (p.lse != nullptr) p.lse[at] = lse2 * 0.693147180559945309f;
-        if (p.sums != nullptr)
-            p.row_lse[((item * p.members + member) * NQ + qt) * p.rowcap + lr] = lse2;
+    for (int o = 1; o < 8; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const bool any_bad = __any_sync(0xffffffffu, bad) != 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int r = r0 + q;
+        const float lq = __shfl_sync(0xffffffffu, l, 8 * q);
+        const float mq = __shfl_sync(0xffffffffu, base, 8 * q);
+        if (r >= rows) break;
+        const int node = rt * span + r / p.g;
+        const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
+        if (any_bad) add_bad_values<HD>(p, x, node, h, acc[q]);
+        write_row<HD>(p, x, node, h * p.g + r % p.g, mq, lq, acc[q],
+                      ((item * p.members + member) * NQ + qt) * p.rowcap + r -
+                          qt * p.nodes_tile * p.g);
     }
 }
 
@@ -1134,7 +1241,10 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row
                                                    int row_parts) {
     grid_dependency_wait();
     grid_launch_dependents();
-    join_rows<HD, NQ, WPR>(p, blockIdx.x, row_tiles, row_parts);
+    if constexpr (WPR > 1)
+        join_rows<HD, NQ, WPR>(p, blockIdx.x, row_tiles, row_parts);
+    else
+        join_many<HD, NQ>(p, blockIdx.x, row_tiles, row_parts);
 }
 
 // The weights of kEntries table entries from e on of a sequence, by one warp: the sums of their
@@ -1229,7 +1339,10 @@ __global__ void __launch_bounds__(256) finish_kernel(const AttendParams p, int r
     grid_dependency_wait();
     grid_launch_dependents();
     if (static_cast<int>(blockIdx.x) < join_ctas) {
-        join_rows<HD, 1, WPR>(p, blockIdx.x, 1, row_parts);
+        if constexpr (WPR > 1)
+            join_rows<HD, 1, WPR>(p, blockIdx.x, 1, row_parts);
+        else
+            join_many<HD, 1>(p, blockIdx.x, 1, row_parts);
         return;
     }
     const int s = (blockIdx.x - join_ctas) / shares, share = (blockIdx.x - join_ctas) % shares;
@@ -1389,12 +1502,12 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
     if (launch_pdl(attend_kernel<HD, NQ>, dim3(plan.groups * plan.members), dim3(kThreads),
                    C::kSmemBytes, stream, mq, mk, mv, p) != cudaSuccess)
         return HSS_ERR_CUDA;
-    // Warps to a row: 8 while a CTA per row leaves SMs free (a lone sequence's 32 rows of 38
-    // pieces), else one.
+    // A CTA to a row while that leaves SMs free (a lone sequence's 32 rows of 38 pieces), else a
+    // warp to four.
     const int unit_rows = std::min(p.max_q, NQ * plan.nodes_tile) * p.g;
     const int64_t units = static_cast<int64_t>(plan.row_tiles) * p.nkv * p.num_seqs;
     const bool few = units * unit_rows <= 2 * kCtas;
-    const int parts = few ? unit_rows : (unit_rows + 7) / 8;
+    const int parts = few ? unit_rows : (unit_rows + 31) / 32;
     const int64_t join_ctas = units * parts;
     // CTAs to a sequence's entries: an even share of all entries in one pass, if the sequences
     // are alike, within what the GPU holds at once.
