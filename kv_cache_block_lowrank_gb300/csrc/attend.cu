@@ -1247,54 +1247,44 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row
         join_many<HD, NQ>(p, blockIdx.x, row_tiles, row_parts);
 }
 
-// The weights of kEntries table entries from e on of a sequence, by one warp: the sums of their
-// granules over heads, row tiles and rows (over the lanes), each scaled by its row's exp2(m -
-// lse).  `row_lse(h, rt, qt, lr)` gives the log2 lse of a row.  Several entries at once, because
-// what an entry costs is the way of its loads.
+// Few rows: the weights of kEntries table entries from e on of a sequence, by one warp: the sums
+// of their granules over heads and rows (over the lanes), each scaled by its row's exp2(m - lse),
+// with row r of head h's log2 lse at lse[h * rows + r].  Several entries at once, because what an
+// entry costs is the way of its loads.
 constexpr int kEntries = 4;
 
-template <int HD, int NQ, typename Lse>
+template <int HD>
 __device__ __forceinline__ void entry_weights(const AttendParams& p, const SeqInfo& x, int seq0,
-                                              int64_t e, Lse&& row_lse) {
-    using C = Cfg<HD, NQ>;
+                                              int64_t e, const float* lse_of) {
+    using C = Cfg<HD, 1>;
     constexpr int TILE = C::kTile, kGran = TILE / 16, kJobs = C::kJobs;
-    const int span = NQ * p.nodes_tile;
     const int lane = threadIdx.x & 31;
-    const int rts = ceil_div(x.nodes, span);
     const int grains = p.bs / 16;
     const int64_t gr0 = (e - x.e0) * grains;  // first granule of the first entry
     float sum[kEntries];
 #pragma unroll
     for (int q = 0; q < kEntries; ++q) sum[q] = 0.0f;
-    for (int rt = 0; rt < rts; ++rt) {
-        const int bt = rt / p.members, member = rt % p.members;
-        // granules that the row tile looked at
-        const int seen = (tokens_upto(p, x, min(x.nodes, (rt + 1) * span)) + 15) / 16;
-        const int rows = min(x.nodes - rt * span, span) * p.g;
-        int f0, n;
-        item_range<TILE>(p, x, span, seq0, bt, 0, f0, n);
-        for (int i = lane; i < rows * p.nkv; i += 32) {
-            const int h = i / rows, r = i - h * rows;
-            const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
-            const int lr = r - qt * p.nodes_tile * p.g;
-            const float lse = row_lse(h, rt, qt, lr);
-            for (int k = 0; k < grains; ++k) {
-                float m[kEntries], part[kEntries];
+    const int seen = ceil_div(tokens_upto(p, x, x.nodes), 16);
+    const int rows = x.nodes * p.g;
+    const int n = tiles_upto<TILE>(p, x, x.nodes);
+    for (int i = lane; i < rows * p.nkv; i += 32) {
+        const int h = i / rows, r = i - h * rows;
+        const float lse = lse_of[i];
+        for (int k = 0; k < grains; ++k) {
+            float m[kEntries], part[kEntries];
 #pragma unroll
-                for (int q = 0; q < kEntries; ++q) {
-                    const int64_t gr = gr0 + q * grains + k;
-                    part[q] = 0.0f;
-                    if (gr >= seen) continue;
-                    const int t = static_cast<int>(gr) / kGran, in = static_cast<int>(gr) % kGran;
-                    const int64_t at =
-                        (static_cast<int64_t>(f0 + h * n + t) * p.members + member) * NQ + qt;
-                    m[q] = p.sums_m[(at * kJobs + in / 4) * p.rowcap + lr];
-                    part[q] = p.sums[(at * kGran + in) * p.rowcap + lr];
-                }
-#pragma unroll
-                for (int q = 0; q < kEntries; ++q)  // (without weight m may be anything)
-                    if (part[q] != 0.0f && lse != -INFINITY) sum[q] += part[q] * exp2f(-m[q] - lse);
+            for (int q = 0; q < kEntries; ++q) {
+                const int64_t gr = gr0 + q * grains + k;
+                part[q] = 0.0f;
+                if (gr >= seen) continue;
+                const int t = static_cast<int>(gr) / kGran, in = static_cast<int>(gr) % kGran;
+                const int64_t at = seq0 + h * n + t;
+                m[q] = p.sums_m[(at * kJobs + in / 4) * p.rowcap + r];
+                part[q] = p.sums[(at * kGran + in) * p.rowcap + r];
             }
+#pragma unroll
+            for (int q = 0; q < kEntries; ++q)  // (without weight m may be anything)
+                if (part[q] != 0.0f && lse != -INFINITY) sum[q] += part[q] * exp2f(-m[q] - lse);
         }
     }
 #pragma unroll
@@ -1307,29 +1297,111 @@ __device__ __forceinline__ void entry_weights(const AttendParams& p, const SeqIn
     }
 }
 
-// The weights after the join, which has left every row's lse; a CTA takes a share of one
-// sequence's entries.
+// Many rows: first, every job's four granule sums over its row tile's rows, once the join has left
+// the rows' lse.  A CTA takes a share of the jobs of one (sequence, head, row tile), a warp per
+// job, its lanes on the rows (whose lse stay in registers), so that everything is read in whole
+// lines.  The totals take the place of the first row's sums.
+template <int HD, int NQ>
+__global__ void __launch_bounds__(256) grains_kernel(const AttendParams p, int row_tiles,
+                                                     int shares) {
+    using C = Cfg<HD, NQ>;
+    constexpr int TILE = C::kTile, kJobs = C::kJobs;
+    const int span = NQ * p.nodes_tile;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int share = blockIdx.x % shares, unit = blockIdx.x / shares;
+    const int qt = unit % NQ, rt = unit / NQ % row_tiles;
+    const int h = unit / NQ / row_tiles % p.nkv, s = unit / NQ / row_tiles / p.nkv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const SeqInfo x = load_seq(p, s);
+    const int first = (rt * NQ + qt) * p.nodes_tile;
+    const int rows = min(max(x.nodes - first, 0), p.nodes_tile) * p.g;
+    if (rows == 0) return;
+    const int b = rt / p.members, member = rt % p.members;
+    int f, n;
+    item_range<TILE>(p, x, span, p.seq_tiles[s], b, h, f, n);
+    const int jobs = ceil_div(tokens_upto(p, x, min(x.nodes, (rt + 1) * span)), 64);
+    const int64_t lse_at =
+        ((static_cast<int64_t>(p.seq_items[s] + b * p.nkv + h) * p.members + member) * NQ + qt) *
+        p.rowcap;
+    float lse[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int r = lane + 32 * q;
+        lse[q] = r < rows ? p.row_lse[lse_at + r] : -INFINITY;
+    }
+    for (int j = share * 8 + warp; j < jobs; j += shares * 8) {
+        const int64_t at = ((static_cast<int64_t>(f + j / kJobs) * p.members + member) * NQ + qt) *
+                               kJobs + j % kJobs;
+        float* sums = p.sums + at * 4 * p.rowcap;
+        float m[4], part[4][4], total[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int r = lane + 32 * q;
+            m[q] = r < rows ? p.sums_m[at * p.rowcap + r] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) part[q][k] = r < rows ? sums[k * p.rowcap + r] : 0.0f;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float scale = exp2f(-m[q] - lse[q]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // (without weight m may be anything)
+                if (part[q][k] != 0.0f && lse[q] != -INFINITY) total[k] += part[q][k] * scale;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                total[k] += __shfl_xor_sync(0xffffffffu, total[k], o);
+        __syncwarp();
+        if (lane < 4) sums[lane * p.rowcap] = lane == 0   ? total[0]
+                                              : lane == 1 ? total[1]
+                                              : lane == 2 ? total[2]
+                                                          : total[3];
+    }
+}
+
+// Then an entry's weight is the sum of its granules' totals over heads and row tiles: a warp per
+// entry, its lanes on the (granule, head, row tile) triples.
 template <int HD, int NQ>
 __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p, int shares) {
+    using C = Cfg<HD, NQ>;
+    constexpr int TILE = C::kTile, kGran = TILE / 16;
+    const int span = NQ * p.nodes_tile;
     grid_dependency_wait();
     grid_launch_dependents();
     const int s = blockIdx.x / shares, share = blockIdx.x % shares;
     const SeqInfo x = load_seq(p, s);
-    const int item0 = p.seq_items[s], seq0 = p.seq_tiles[s];
-    const int warp = threadIdx.x >> 5;
-    for (int64_t e = x.e0 + (share * 8 + warp) * kEntries; e < x.end; e += shares * 8 * kEntries)
-        entry_weights<HD, NQ>(p, x, seq0, e, [&](int h, int rt, int qt, int lr) {
-            const int64_t row =
-                (static_cast<int64_t>(item0 + rt / p.members * p.nkv + h) * p.members +
-                 rt % p.members) * NQ + qt;
-            return p.row_lse[row * p.rowcap + lr];
-        });
+    const int seq0 = p.seq_tiles[s];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rts = ceil_div(x.nodes, span), grains = p.bs / 16;
+    const int tiles = ceil_div(x.nodes, p.nodes_tile);  // row tiles with rows in use
+    for (int64_t e = x.e0 + share * 8 + warp; e < x.end; e += shares * 8) {
+        float sum = 0.0f;
+        for (int i = lane; i < grains * p.nkv * rts * NQ; i += 32) {
+            const int qt = i % NQ, rt = i / NQ % rts, h = i / NQ / rts % p.nkv;
+            const int64_t gr = (e - x.e0) * grains + i / NQ / rts / p.nkv;
+            const int seen = ceil_div(tokens_upto(p, x, min(x.nodes, (rt + 1) * span)), 16);
+            if (gr >= seen || rt * NQ + qt >= tiles) continue;
+            int f, n;
+            item_range<TILE>(p, x, span, seq0, rt / p.members, h, f, n);
+            const int t = static_cast<int>(gr) / kGran, in = static_cast<int>(gr) % kGran;
+            const int64_t at =
+                (static_cast<int64_t>(f + t) * p.members + rt % p.members) * NQ + qt;
+            sum += p.sums[(at * kGran + in) * p.rowcap];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0)
+            p.weights_out[e] = (p.weights_in != nullptr ? p.weights_in[e] * p.decay : 0.0f) + sum;
+    }
 }
 
 // Join and weights in one launch, for one row tile (NQ 1, one member): the first CTAs join, the
 // others each take a share of one sequence's entries and work the rows' lse out for themselves
 // from the pieces' m and l, which for a few rows is quicker than waiting for the join.
-constexpr int kFewRows = 512;  // rows of a sequence, nodes times query heads
+constexpr int kFewRows = 256;  // rows of a sequence, nodes times query heads
 
 template <int HD, int WPR>
 __global__ void __launch_bounds__(256) finish_kernel(const AttendParams p, int row_parts,
@@ -1399,8 +1471,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const AttendParams p, int r
     }
     __syncthreads();
     for (int64_t e = x.e0 + (share * 8 + warp) * kEntries; e < x.end; e += shares * 8 * kEntries)
-        entry_weights<HD, 1>(p, x, seq0, e,
-                             [&](int h, int, int, int lr) { return sh_lse[h * rows + lr]; });
+        entry_weights<HD>(p, x, seq0, e, sh_lse);
 }
 
 // ------------------------------------------------------------------------------------- host
@@ -1511,14 +1582,18 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
     const int64_t join_ctas = units * parts;
     // CTAs to a sequence's entries: an even share of all entries in one pass, if the sequences
     // are alike, within what the GPU holds at once.
-    const int64_t per_cta = 8 * kEntries;
+    // Join and weights in one launch while a lane has few (row, granule) pairs of an entry to look
+    // at in turn (36 sequences of 23 nodes, 14 heads and blocks of 32 tokens, 22 pairs, took 80 us
+    // this way and 43 us through the granules' totals).
+    const int64_t seq_rows = static_cast<int64_t>(p.max_q) * p.nq;
+    const bool few_each = NQ == 1 && plan.row_tiles == 1 && p.weights_out != nullptr &&
+                          seq_rows <= kFewRows && (seq_rows + 31) / 32 * (p.bs / 16) <= 8;
+    const int64_t per_cta = few_each ? 8 * kEntries : 8;
     const int64_t even = (p.total_blocks / std::max(p.num_seqs, 1) + per_cta) / per_cta;
     const int64_t most = std::max<int64_t>(1, 8 * kCtas / std::max(p.num_seqs, 1));
     const int shares = static_cast<int>(std::min(even, most));
     if constexpr (NQ == 1) {
-        // One launch for both, while the rows' lse fit in shared memory.
-        if (rows && p.weights_out != nullptr && plan.row_tiles == 1 && p.num_seqs > 0 &&
-            static_cast<int64_t>(p.max_q) * p.nq <= kFewRows) {
+        if (rows && few_each) {
             const int64_t grid = join_ctas + static_cast<int64_t>(p.num_seqs) * shares;
             if (grid > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
             auto finish = few ? finish_kernel<HD, 8> : finish_kernel<HD, 1>;
@@ -1533,6 +1608,18 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
         auto join = few ? join_kernel<HD, NQ, 8> : join_kernel<HD, NQ, 1>;
         if (launch_pdl(join, dim3(static_cast<unsigned>(join_ctas)), dim3(256), 0, stream, p,
                        plan.row_tiles, parts) != cudaSuccess)
+            return HSS_ERR_CUDA;
+    }
+    if (rows && p.weights_out != nullptr) {
+        // shares of a unit's jobs: two passes over all warps that the GPU holds
+        const int64_t grain_units = units * NQ;
+        const int64_t jobs = p.total_blocks * p.bs / 64 / std::max(p.num_seqs, 1) + 1;
+        const int64_t split = std::max<int64_t>(
+            1, std::min((jobs + 7) / 8, 8 * kCtas / std::max<int64_t>(grain_units, 1)));
+        if (grain_units * split > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
+        if (launch_pdl(grains_kernel<HD, NQ>, dim3(static_cast<unsigned>(grain_units * split)),
+                       dim3(256), 0, stream, p, plan.row_tiles, static_cast<int>(split)) !=
+            cudaSuccess)
             return HSS_ERR_CUDA;
     }
     if (p.weights_out != nullptr &&
