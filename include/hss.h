@@ -492,14 +492,17 @@ typedef struct hss_attend_args {
     float scale;                /* factor on the scores, finite; usually head_dim^-0.5 */
     float decay;                /* factor on weights_in, finite */
     void* workspace;            /* device, 256-byte aligned, hss_attend_tree_workspace_bytes(...);
-                                   zero it once before its first use.  Calls that share one must
-                                   not run at the same time. */
+                                   what it holds does not matter.  Calls that share one must not
+                                   run at the same time. */
     size_t workspace_bytes;
     int32_t* dev_status;        /* device int32 or NULL */
 } hss_attend_args;
 
 /* Bytes of the workspace: enough for every call with these dims and counts, or smaller ones
- * (0 if a count is negative or the dims are not valid). */
+ * (0 if a count is negative or the dims are not valid).  Without weights it holds what the CTAs
+ * have of the rows, about twice the outputs in fp32 and some 40 MB at most; with them also a
+ * float for every 16 tokens that a row sees, per query head: 13 MB for 64 sequences of 16k tokens
+ * and 32 query heads, 1.4 GB for 512 rows of 64 heads over 128k tokens. */
 size_t hss_attend_tree_workspace_bytes(const hss_dims* dims, int32_t num_seqs, int32_t max_q,
                                        int64_t total_blocks, int32_t with_weights);
 
@@ -528,7 +531,10 @@ size_t hss_attend_tree_workspace_bytes(const hss_dims* dims, int32_t num_seqs, i
  *                weights_in
  * Scores, softmax statistics and sums are fp32; the weights exp(s - m) enter the product with V
  * rounded to bf16, the statistics and block weights take them unrounded.
- * Supported: num_q_heads / num_kv_heads <= 128; num_seqs, max_q >= 0.  Device-side errors
+ * Up to three more launches follow the attention itself on the stream (the join of what several
+ * CTAs have of a row, and the block weights); a pipeline wait that runs out raises
+ * HSS_ERR_DEVICE_TIMEOUT like those of the other kernels.
+ * Supported: num_q_heads / num_kv_heads <= 128; num_seqs, max_q >= 0.  Other device-side errors
  * (*dev_status and the library's device error word): a block id outside [0, max_blocks) hides
  * its tokens and raises HSS_ERR_OUT_OF_RANGE; so does a table too short for ctx_len + nodes (the
  * tokens past it are hidden); a negative ctx_len counts as 0; a sequence with more than max_q
@@ -542,7 +548,8 @@ hss_status hss_attend_tree(const hss_attend_args* args, const uint16_t* Q,
 /*
  * Eviction from the cache by accumulated attention weight: cut every sequence's table to its
  * budget.  Sequence s (n entries) may lose its entries j with
- *   keep_first <= j < n - keep_last     and, with ctx_len, only whole ones, j < ctx_len[s] / block_size;
+ *   keep_first <= j < n - keep_last
+ * and, with ctx_len, whole ones only, j < ctx_len[s] / block_size;
  * of these it loses the max(n - budgets[s], 0) (or all, if there are fewer) with the least
  * (weight, index): -0 equals +0 and NaN ranks as +inf, as in hss_rank_victims.  The entries that
  * stay keep their order:

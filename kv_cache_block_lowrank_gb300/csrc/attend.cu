@@ -9,9 +9,11 @@
 // leaves them.
 //
 // Roles of a CTA (12 warps, one CTA per SM):
-//   warp 0       TMA of the queries and of K: looks up the block ids, one box per 16 or more tokens
-//   warp 1       TMA of V
-//   warps 2, 3   one thread each issues the products of one softmax group
+//   warps 0, 1   TMA: look up the block ids, one box per 16 or more tokens (K and V of one group's
+//                tiles each, or one K and one V); warp 0 also brings the queries
+//   warps 2, 3   issue the products of one softmax group each, as whole converged warps: with a
+//                lone thread's divergent branch every instruction first moved its operands to
+//                uniform registers, 60 to 80 cycles each, and a 512-row chunk took 1.8 ms, not 1.4
 //   warps 4..11  two softmax groups of four warps.  With at most 128 rows the groups take a
 //                sequence's even and odd tiles, each with its own O, m and l (joined later, like
 //                any two pieces of a split sequence); with more rows they take two row tiles over
@@ -20,20 +22,29 @@
 //
 // Split.  All (sequence, batch of row tiles, kv head, tile) units form one list, cut into equal
 // contiguous ranges: every SM gets the same number of tiles whatever the lengths are.  A range's
-// pieces of (sequence, batch, head) leave unnormalised O, m and l in the workspace and
-// join_kernel adds them up.  Row tiles beyond one (large trees, chunks) go to neighbouring CTAs
-// that walk the same range in step, so that K and V come from HBM once and from L2 to the rest.
+// pieces of (sequence, batch, head) leave unnormalised O, m and l in the workspace, and a second
+// kernel joins them.  Row tiles beyond one (large trees, chunks) go to neighbouring CTAs that
+// walk the same range in step, so that K and V come from HBM once and from L2 to the rest.
 //
 // Block weights: the softmax thread has the sum of every 16 of its tokens anyway (l is their
-// sum); with weights it stores them beside m, and weights_kernel scales each by exp2(m - lse)
-// and adds them up over rows and heads once lse is known.  Nothing is computed twice, and no
+// sum); with weights it stores them beside m, and once the rows' lse are known they are scaled by
+// exp2(m - lse) and added up over rows and heads.  No score is formed twice, and there are no
 // float atomics: the same call gives the same bits.
+//
+// What bounds it, and what it reaches on GB300 (HBM 6.79 TB/s and 1906 TFLOP/s bf16 measured):
+// few rows, the bytes of K and V: 64 sequences of 1k to 16k tokens, 32 query heads on 8 of 128, 373
+// us with weights and join, 6.1 TB/s; one sequence of 32k tokens 38 us, of which 20 are its bytes
+// and the rest the start (sequence lengths, block ids and the first tiles, one way through memory
+// after another, 7 us), the last tiles and the join (8 us).  Many rows, the products and the
+// exponentials between them, both near 1400 cycles for a job of 2 x 128 rows by 64 tokens: 512
+// rows of 64 heads over 131072 tokens 1.37 ms alone (1.6 PFLOP/s), 1.49 ms under the power cap of
+// a long run.
 //
 // Masked places.  Tokens of the context need no mask; a tile that holds nodes, the end of the
 // sequence or a bad block id gets 32 visibility bits per 32 tokens and row.  A zero weight does
 // not silence an infinite or NaN value in a matrix product, so before such a tile's second
 // product the group clears the values past the end and any non-finite element of a node's
-// value, and join_kernel adds those elements to the rows that do see the node.
+// value, and the join adds those elements to the rows that do see the node.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -632,7 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
             const uint32_t d_s = tmem + w * (kBuffers * 64);
             const uint32_t d_o = tmem + C::kOCols + w * HD;
-            uint32_t tile = 0, segs = 0, taken = 0;  // taken: bit b, parity of buffer b's next weights
+            uint32_t tile = 0, segs = 0;
+            uint32_t taken = 0;  // bit b: parity of buffer b's next weights
             bool ok = true;
             while (ok && walk.next(p, g)) {
                 if (g.n == 0) continue;
@@ -713,7 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t o_cols = lanes + C::kOCols + w * HD;
         const int gt = quarter * 32 + lane;  // thread of the group
         uint32_t tile = 0, segs = 0, values = 0;
-        uint32_t next = 0, ends = 0;  // bit b: parity of buffer b's next scores, next end of a piece
+        // bit b: parity of buffer b's next scores, of its next end of a piece
+        uint32_t next = 0, ends = 0;
         bool ok = true;
         walk.begin(p, bar.start, span);
         if (w >= NG) walk.f = walk.f1;
@@ -764,7 +777,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (pos0 + r >= x.tokens) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint4*>(at + swizzled_offset(r & 7, 16 * e, 128)) =
+                                *reinterpret_cast<uint4*>(
+                                    at + swizzled_offset(r & 7, 16 * e, 128)) =
                                     make_uint4(0, 0, 0, 0);
                             continue;
                         }
@@ -794,9 +808,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (found) {
-                        *(volatile int*)&bar.bad_value[w][segs & 1] = static_cast<int>(segs);
-                        if (NQ == 2)
-                            *(volatile int*)&bar.bad_value[w ^ 1][segs & 1] = static_cast<int>(segs);
+                        const int seg = static_cast<int>(segs);
+                        *(volatile int*)&bar.bad_value[w][seg & 1] = seg;
+                        if (NQ == 2) *(volatile int*)&bar.bad_value[w ^ 1][seg & 1] = seg;
                     }
                     fence_proxy_async_smem();
                     if (NQ == 2) {  // both groups read the tile: both wait until all of it is fit
@@ -823,8 +837,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         top = -INFINITY;
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            uint32_t bits = row < live ? visible32(p, x, node, pos0 + 32 * k, word0, word1)
-                                                  : 0u;
+                            uint32_t bits = 0;
+                            if (row < live)
+                                bits = visible32(p, x, node, pos0 + 32 * k, word0, word1);
                             if ((bad >> (2 * k)) & 1) bits &= 0xFFFF0000u;
                             if ((bad >> (2 * k)) & 2) bits &= 0x0000FFFFu;
 #pragma unroll
@@ -966,8 +981,8 @@ __device__ __forceinline__ void item_range(const AttendParams& p, const SeqInfo&
 
 // Adds the non-finite values of the nodes a row sees.
 template <int HD>
-__device__ __forceinline__ void add_bad_values(const AttendParams& p, const SeqInfo& x, int node, int h,
-                                            float* acc) {
+__device__ __forceinline__ void add_bad_values(const AttendParams& p, const SeqInfo& x,
+                                               int node, int h, float* acc) {
     const int lane = threadIdx.x & 31;
     for (int j = 0; j < x.nodes; ++j) {
         if (x.ctx + j >= x.tokens) break;
