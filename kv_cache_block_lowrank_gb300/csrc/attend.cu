@@ -23,7 +23,9 @@
 // Split.  All (sequence, batch of row tiles, kv head, tile) units form one list, cut into equal
 // contiguous ranges: every SM gets the same number of tiles whatever the lengths are.  A range's
 // pieces of (sequence, batch, head) leave unnormalised O, m and l in the workspace, and a second
-// kernel joins them.  Row tiles beyond one (large trees, chunks) go to neighbouring CTAs that
+// kernel joins them.  What one group saw from the first tile to the last needs no join: its rows
+// go out from here (a prompt of 4096 tokens 574 us, through the workspace 603; 50 trees of 248
+// nodes, head_dim 256, 453 against 595).  Row tiles beyond one (large trees, chunks) go to neighbouring CTAs that
 // walk the same range in step, so that K and V come from HBM once and from L2 to the rest.
 //
 // Block weights: the softmax thread has the sum of every 16 of its tokens anyway (l is their
@@ -75,6 +77,9 @@ struct Cfg {
     static constexpr int kJobs = kTile / 64;
     static constexpr int kGroups = HD == 256 ? 1 : 2;
     static constexpr int kBuffers = HD == 192 ? 1 : 2;
+    // One softmax group walks all tiles of a row: where a CTA has a whole item, it writes the
+    // result itself and the join has nothing to do for it.
+    static constexpr bool kWhole = NQ == 2 || kGroups == 1;
     static constexpr int kOCols = kGroups * kBuffers * 64;  // where O begins
     static constexpr int kStageBytes = kTile * HD * 2;
     static constexpr int kQBytes = NQ * kRows * HD * 2;
@@ -112,7 +117,7 @@ struct AttendParams {
     int32_t members;     // CTAs per group: row tiles (or pairs of them) walked in step
     int32_t groups;
     int32_t rowcap;      // rows of a tile that can be in use
-    int32_t head_dim;
+    int32_t ways;        // warps to a task of join_columns, or 0: part_o by row
     float c;             // |scale| log2(e), or 1 for scale 0
     float pre;           // 1, or -1 / 0 for a negative / zero scale: scores are multiplied first
     float decay;
@@ -122,7 +127,7 @@ struct AttendParams {
     int32_t* header;     // [0] tiles in all, [1] tiles per group
     int32_t* seq_tiles;  // [num_seqs] tiles before a sequence
     int32_t* seq_items;  // [num_seqs] (batch, head) items before a sequence
-    float* part_o;       // [slot][row][head_dim]
+    float* part_o;       // [slot][row][head_dim], or [slot][head_dim][row] with ways
     float2* part_ml;     // [slot][row] (m, l)
     int32_t* part_bad;   // [slot] a node's value was not finite
     float* row_lse;      // [unit row tile][row], log2
@@ -239,6 +244,10 @@ struct Walk {
             enter(p);
         }
         return false;
+    }
+    // Whether the segment that next() gave is all of its item.
+    __device__ __forceinline__ bool whole(const AttendParams& p, const Segment& g) const {
+        return g.ta == 0 && t == batch_tiles<TILE>(p, x, span, b);
     }
 };
 
@@ -383,6 +392,36 @@ struct Barriers {
     int scan[kThreads / 32];
     int scan_items[kThreads / 32];
 };
+
+// A whole item's row from tensor memory (anything, if it has no weight): row `to` of out, lse.
+template <int HD>
+__device__ __forceinline__ void write_whole(const AttendParams& p, uint32_t o_cols, bool live,
+                                            int64_t to, float m, float l,
+                                            float* row_lse) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+    for (int k = 0; k < HD; k += 32) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(o_cols + k, o);
+        tmem_ld_wait_for(o);
+        if (!live) continue;
+        uint4* at = reinterpret_cast<uint4*>(p.out + to * HD + k);
+#pragma unroll
+        for (int d = 0; d < 32; d += 8) {
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                u[i] = l == 0.0f ? 0u
+                                 : pack_bf16x2(__uint_as_float(o[d + 2 * i]) * inv,
+                                               __uint_as_float(o[d + 2 * i + 1]) * inv);
+            at[d / 8] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+    }
+    if (!live) return;
+    const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+    if (p.lse != nullptr) p.lse[to] = lse2 * 0.693147180559945309f;
+    if (row_lse != nullptr) *row_lse = lse2;
+}
 
 template <int HD, int NQ>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -931,25 +970,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int b = kBuffers == 2 ? (jobs - 1) & 1 : 0;  // the last product
                     if (!(ok = wait(&bar.o_done[w * kBuffers + b], (ends >> b) & 1))) break;
                     tc_fence_after_sync();
-                    float* to = p.part_o + (slot * p.rowcap + row) * HD;
-#pragma unroll
+                }
+                const bool bad =
+                    jobs > 0 && *(volatile int*)&bar.bad_value[w][segs & 1] ==
+                                    static_cast<int>(segs);
+                // (What is bad the join adds.)
+                if (C::kWhole && !bad && walk.whole(p, g)) {
+                    const int64_t to = (static_cast<int64_t>(x.q0) + node) * p.nq + walk.h * p.g +
+                                       row % p.g;
+                    write_whole<HD>(p, o_cols, row < live, to, m, l,
+                                    p.sums == nullptr
+                                        ? nullptr
+                                        : p.row_lse + ((static_cast<int64_t>(g.item) * p.members +
+                                                        walk.member) * NQ +
+                                                       (NQ == 2 ? w : 0)) * p.rowcap + row);
+                } else if (jobs > 0) {
+#pragma unroll 1
                     for (int k = 0; k < HD; k += 32) {
                         uint32_t o[32];
                         tmem_ld_32x32b_x32(o_cols + k, o);
                         tmem_ld_wait_for(o);
-                        if (row < live) {
+                        if (row < live && p.ways > 0) {
+                            float* at = p.part_o + (slot * HD + k) * p.rowcap + row;
+#pragma unroll
+                            for (int d = 0; d < 32; ++d)
+                                at[d * p.rowcap] = __uint_as_float(o[d]);
+                        } else if (row < live) {
+                            float* at = p.part_o + (slot * p.rowcap + row) * HD + k;
 #pragma unroll
                             for (int d = 0; d < 32; d += 4)
-                                *reinterpret_cast<uint4*>(to + k + d) =
+                                *reinterpret_cast<uint4*>(at + d) =
                                     make_uint4(o[d], o[d + 1], o[d + 2], o[d + 3]);
                         }
                     }
-                    tc_fence_before_sync();
                 }
+                tc_fence_before_sync();
                 if (row < live) p.part_ml[slot * p.rowcap + row] = make_float2(m, l);
-                if (row == 0)
-                    p.part_bad[slot] = jobs > 0 && *(volatile int*)&bar.bad_value[w][segs & 1] ==
-                                                       static_cast<int>(segs);
+                if (row == 0) p.part_bad[slot] = bad;
             }
             if (g.n > 0) ++segs;
             ends ^= jobs > 1 && kBuffers == 2 ? 3u : (jobs > 0 ? 1u : 0u);
@@ -1063,6 +1120,7 @@ __device__ __forceinline__ void join_rows(const AttendParams& p, int block, int 
         const int w = NQ == 2 ? qt : k % kPieceWidth;
         return ((item + g0 + grp) * p.members + member) * 2 + w;
     };
+    if (C::kWhole && mine && g0 == g1 && p.part_bad[slot_of(0)] == 0) return;
     float top = -INFINITY, l = 0.0f, acc[kEach];
     int bad = 0;
 #pragma unroll
@@ -1158,14 +1216,14 @@ __device__ __forceinline__ void join_rows(const AttendParams& p, int block, int 
 
 // Many rows: a warp takes four rows of one (sequence, row tile, head) at a time, eight lanes a row
 // for its pieces' m and l, so that the loads of several rows are in flight together.
-template <int HD, int NQ>
+template <int HD>
 __device__ __forceinline__ void join_many(const AttendParams& p, int block, int row_tiles,
                                           int row_parts) {
-    using C = Cfg<HD, NQ>;
+    using C = Cfg<HD, 1>;
     constexpr int TILE = C::kTile;
     constexpr int kEach = HD / 32;
-    constexpr int kPieceWidth = NQ == 1 ? C::kGroups : 1;
-    const int span = NQ * p.nodes_tile;
+    constexpr int kPieceWidth = C::kGroups;
+    const int span = p.nodes_tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = block % row_parts, unit = block / row_parts;
     const int rt = unit % row_tiles, h = unit / row_tiles % p.nkv, s = unit / row_tiles / p.nkv;
@@ -1181,11 +1239,10 @@ __device__ __forceinline__ void join_many(const AttendParams& p, int block, int 
     const int g0 = n > 0 ? f / per : 0, g1 = n > 0 ? (f + n - 1) / per : -1;
     const int pieces = (g1 - g0 + 1) * kPieceWidth;
     auto place_of = [&](int r, int k) -> int64_t {  // row r's piece k, in rows of the workspace
-        const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
-        const int w = NQ == 2 ? qt : k % kPieceWidth;
-        return (((item + g0 + k / kPieceWidth) * p.members + member) * 2 + w) * p.rowcap +
-               (r - qt * p.nodes_tile * p.g);
+        return (((item + g0 + k / kPieceWidth) * p.members + member) * 2 + k % kPieceWidth) *
+                   p.rowcap + r;
     };
+    if (C::kWhole && g0 == g1 && p.part_bad[place_of(0, 0) / p.rowcap] == 0) return;
     // m of the row: lane 8 q + i looks at pieces i, i + 8, ... of row r0 + q
     const int my_row = min(r0 + lane / 8, rows - 1);
     float top = -INFINITY, l = 0.0f;
@@ -1243,23 +1300,148 @@ __device__ __forceinline__ void join_many(const AttendParams& p, int block, int 
         const float mq = __shfl_sync(0xffffffffu, base, 8 * q);
         if (r >= rows) break;
         const int node = rt * span + r / p.g;
-        const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
         if (any_bad) add_bad_values<HD>(p, x, node, h, acc[q]);
         write_row<HD>(p, x, node, h * p.g + r % p.g, mq, lq, acc[q],
-                      ((item * p.members + member) * NQ + qt) * p.rowcap + r -
-                          qt * p.nodes_tile * p.g);
+                      (item * p.members + member) * p.rowcap + r);
+    }
+}
+
+// Many rows, part_o by column: a task of 32 rows (one a lane, so that reads are whole lines) by
+// kJoinCols columns, its pieces split over p.ways warps that put their sums together in shared
+// memory, from where the rows go out with their columns side by side.  (32 columns to a task take
+// 126 registers, half the warps: 41 trees of 76 nodes 65 us, with 16 columns 44.)
+constexpr int kJoinCols = 16;
+
+template <int HD, int NQ>
+__device__ __forceinline__ void join_columns(const AttendParams& p, int block, int row_tiles,
+                                             int row_parts) {
+    using C = Cfg<HD, NQ>;
+    constexpr int TILE = C::kTile;
+    constexpr int kPieceWidth = NQ == 1 ? C::kGroups : 1;
+    __shared__ float sums[8][32][kJoinCols + 1];
+    __shared__ float2 stats[8][32];
+    __shared__ int flags[8];
+    const int span = NQ * p.nodes_tile;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = block / row_parts, ways = p.ways;
+    const int way = warp % ways, task = (block % row_parts * 8 + warp) / ways;
+    const int rt = unit % row_tiles, h = unit / row_tiles % p.nkv, s = unit / row_tiles / p.nkv;
+    const int cb = task % (HD / kJoinCols), r32 = task / (HD / kJoinCols) % ceil_div(p.rowcap, 32);
+    const int qt = task / (HD / kJoinCols) / ceil_div(p.rowcap, 32);
+    const SeqInfo x = load_seq(p, s);
+    const int seq0 = p.seq_tiles[s], per = p.header[1];
+    const int b = rt / p.members, member = rt % p.members;
+    const int64_t item = p.seq_items[s] + b * p.nkv + h;
+    const int first = (rt * NQ + qt) * p.nodes_tile;  // node of the tile's first row
+    const int rows = qt < NQ ? min(max(x.nodes - first, 0), p.nodes_tile) * p.g : 0;
+    int f, n;
+    item_range<TILE>(p, x, span, seq0, b, h, f, n);
+    const int g0 = n > 0 ? f / per : 0, g1 = n > 0 ? (f + n - 1) / per : -1;
+    auto slot_of = [&](int k) -> int64_t {
+        return ((item + g0 + k / kPieceWidth) * p.members + member) * 2 +
+               (NQ == 2 ? qt : k % kPieceWidth);
+    };
+    const bool done =
+        C::kWhole && r32 * 32 < rows && g0 == g1 && p.part_bad[slot_of(0)] == 0;
+    if (r32 * 32 < rows && !done) {
+        const int pieces = (g1 - g0 + 1) * kPieceWidth;
+        const int lr = min(r32 * 32 + lane, rows - 1);
+        float top = -INFINITY, l = 0.0f, acc[kJoinCols];
+        int bad = 0;
+#pragma unroll
+        for (int c = 0; c < kJoinCols; ++c) acc[c] = 0.0f;
+#pragma unroll 2
+        for (int k = way; k < pieces; k += ways) {
+            const int64_t sl = slot_of(k);
+            const float2 ml = p.part_ml[sl * p.rowcap + lr];
+            bad |= p.part_bad[sl];
+            const float* o = p.part_o + (sl * HD + cb * kJoinCols) * p.rowcap + lr;
+            float v[kJoinCols];
+#pragma unroll
+            for (int c = 0; c < kJoinCols; ++c) v[c] = o[c * p.rowcap];
+            if (ml.y == 0.0f) continue;  // without weight O may be anything
+            const float m = fmaxf(top, ml.x);
+            const float shrink = exp2f(top - m), wt = exp2f(ml.x - m);
+            top = m;
+            l = l * shrink + wt * ml.y;
+#pragma unroll
+            for (int c = 0; c < kJoinCols; ++c) acc[c] = acc[c] * shrink + wt * v[c];
+        }
+#pragma unroll
+        for (int c = 0; c < kJoinCols; ++c) sums[warp][lane][c] = acc[c];
+        stats[warp][lane] = make_float2(top, l);
+        if (lane == 0) flags[warp] = bad;
+    }
+    __syncthreads();
+    // Eight columns of a row to a lane; the task's warps take rows in turn.
+    const int w0 = warp - way;
+    constexpr int kLanes = kJoinCols / 8;
+    for (int r0 = way * (32 / kLanes); r0 < 32; r0 += ways * (32 / kLanes)) {
+        const int r = r0 + lane / kLanes, at = r32 * 32 + r, col = lane % kLanes * 8;
+        if (at >= rows || done) break;
+        float top = -INFINITY;
+        int bad = 0;
+        for (int w = w0; w < w0 + ways; ++w) {
+            top = fmaxf(top, stats[w][r].x);
+            bad |= flags[w];
+        }
+        float l = 0.0f, acc[8] = {};
+        for (int w = w0; w < w0 + ways; ++w) {
+            const float2 ml = stats[w][r];
+            if (ml.y == 0.0f) continue;
+            const float wt = exp2f(ml.x - top);
+            l += wt * ml.y;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[c] += wt * sums[w][r][col + c];
+        }
+        const int node = first + at / p.g;
+        if (bad) {
+            // Non-finite values of the nodes this row sees.
+            for (int j = 0; j < x.nodes && x.ctx + j < x.tokens; ++j) {
+                if (!((node_word(p, x, node, j >> 6) >> (j & 63)) & 1)) continue;
+                const int pos = x.ctx + j;
+                const int64_t id = p.table[x.e0 + pos / p.bs];
+                if (id < 0 || id >= p.max_blocks) continue;
+                const uint16_t* v =
+                    p.V + ((id * p.bs + pos % p.bs) * p.nkv + h) * HD + cb * kJoinCols + col;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float e = __uint_as_float(static_cast<uint32_t>(v[c]) << 16);
+                    if (!isfinite(e)) acc[c] += e;
+                }
+            }
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint32_t o[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            o[c] = l == 0.0f ? 0u : pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+        uint16_t* to = p.out +
+                       ((static_cast<int64_t>(x.q0) + node) * p.nq + h * p.g + at % p.g) * HD +
+                       cb * kJoinCols + col;
+        *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (cb == 0 && col == 0) {
+            const float lse2 = l == 0.0f ? -INFINITY : top + log2f(l);
+            if (p.lse != nullptr)
+                p.lse[(static_cast<int64_t>(x.q0) + node) * p.nq + h * p.g + at % p.g] =
+                    lse2 * 0.693147180559945309f;
+            if (p.sums != nullptr)
+                p.row_lse[((item * p.members + member) * NQ + qt) * p.rowcap + at] = lse2;
+        }
     }
 }
 
 template <int HD, int NQ, int WPR>
-__global__ void __launch_bounds__(256) join_kernel(const AttendParams p, int row_tiles,
+__global__ void __launch_bounds__(256, 3) join_kernel(const AttendParams p, int row_tiles,
                                                    int row_parts) {
     grid_dependency_wait();
     grid_launch_dependents();
     if constexpr (WPR > 1)
         join_rows<HD, NQ, WPR>(p, blockIdx.x, row_tiles, row_parts);
+    else if (NQ == 2 || p.ways > 0)
+        join_columns<HD, NQ>(p, blockIdx.x, row_tiles, row_parts);
     else
-        join_many<HD, NQ>(p, blockIdx.x, row_tiles, row_parts);
+        join_many<HD>(p, blockIdx.x, row_tiles, row_parts);
 }
 
 // Few rows: the weights of kEntries table entries from e on of a sequence, by one warp: the sums
@@ -1419,7 +1601,7 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p, int 
 constexpr int kFewRows = 256;  // rows of a sequence, nodes times query heads
 
 template <int HD, int WPR>
-__global__ void __launch_bounds__(256) finish_kernel(const AttendParams p, int row_parts,
+__global__ void __launch_bounds__(256, 3) finish_kernel(const AttendParams p, int row_parts,
                                                      int join_ctas, int shares) {
     using C = Cfg<HD, 1>;
     __shared__ float sh_lse[kFewRows];
@@ -1428,8 +1610,10 @@ __global__ void __launch_bounds__(256) finish_kernel(const AttendParams p, int r
     if (static_cast<int>(blockIdx.x) < join_ctas) {
         if constexpr (WPR > 1)
             join_rows<HD, 1, WPR>(p, blockIdx.x, 1, row_parts);
+        else if (p.ways > 0)
+            join_columns<HD, 1>(p, blockIdx.x, 1, row_parts);
         else
-            join_many<HD, 1>(p, blockIdx.x, 1, row_parts);
+            join_many<HD>(p, blockIdx.x, 1, row_parts);
         return;
     }
     const int s = (blockIdx.x - join_ctas) / shares, share = (blockIdx.x - join_ctas) % shares;
@@ -1499,6 +1683,8 @@ struct Plan {
     int members, groups;
     int rowcap;
     int tile;
+    bool few;        // few rows in all: a CTA joins one
+    int tasks, ways;  // of join_columns: a unit's tasks and the warps to each, 0 for part_o by row
     int64_t slots, tiles, units;
     size_t header, seq_tiles, seq_items, part_o, part_ml, part_bad, row_lse, sums, sums_m, bytes;
 };
@@ -1530,6 +1716,22 @@ Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total
     }
     p.groups = std::max(1, kCtas / p.members);
     p.rowcap = std::min(kRows, g * std::min(max_q, p.nodes_tile));
+    // A CTA joins a row while that leaves SMs free (a lone sequence's 32 rows of 38 pieces).
+    const int64_t units = static_cast<int64_t>(p.row_tiles) * d.num_kv_heads * num_seqs;
+    p.few = units * std::min(max_q, span) * g <= 2 * kCtas;
+    // A thread has a row of O to store.  By column a warp's 32 rows are a line a store, by row 32
+    // lines that get 16 bytes each; but a join of few rows finds a row's columns quicker by row.
+    // By row and by column: 32 rows of 8 heads of 64 sequences 52 and 55 us, 64 rows of 8 heads of
+    // one sequence 61 and 43, a prompt of 4096 tokens 730 and 603.
+    p.tasks = p.nq_tiles * ((p.rowcap + 31) / 32) * (d.head_dim / kJoinCols);
+    p.ways = 0;
+    if (!p.few && p.rowcap > 32) {
+        // Warps to a task while there are pieces for them and the GPU has room.
+        const int width = p.nq_tiles == 1 && d.head_dim < 256 ? 2 : 1;  // softmax groups to a row
+        const int64_t pieces = (p.groups * p.members + units - 1) / units * width + 1;
+        for (p.ways = 1; p.ways < 8 && p.ways < pieces && units * p.tasks * p.ways < 32 * kCtas;)
+            p.ways *= 2;
+    }
     const int64_t batches = (p.row_tiles + p.members - 1) / p.members;
     const int64_t items = batches * d.num_kv_heads * num_seqs;
     p.units = items * p.members * p.nq_tiles;
@@ -1588,12 +1790,12 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
     if (launch_pdl(attend_kernel<HD, NQ>, dim3(plan.groups * plan.members), dim3(kThreads),
                    C::kSmemBytes, stream, mq, mk, mv, p) != cudaSuccess)
         return HSS_ERR_CUDA;
-    // A CTA to a row while that leaves SMs free (a lone sequence's 32 rows of 38 pieces), else a
-    // warp to four.
     const int unit_rows = std::min(p.max_q, NQ * plan.nodes_tile) * p.g;
     const int64_t units = static_cast<int64_t>(plan.row_tiles) * p.nkv * p.num_seqs;
-    const bool few = units * unit_rows <= 2 * kCtas;
-    const int parts = few ? unit_rows : (unit_rows + 31) / 32;
+    const bool few = plan.few;
+    const int parts = few          ? unit_rows
+                      : p.ways > 0 ? (plan.tasks * p.ways + 7) / 8
+                                   : (unit_rows + 31) / 32;
     const int64_t join_ctas = units * parts;
     // CTAs to a sequence's entries: an even share of all entries in one pass, if the sequences
     // are alike, within what the GPU holds at once.
@@ -1686,7 +1888,7 @@ hss_status launch_attend(const AttendArgs& r, cudaStream_t stream) {
     p.members = plan.members;
     p.groups = plan.groups;
     p.rowcap = plan.rowcap;
-    p.head_dim = d.head_dim;
+    p.ways = plan.ways;
     p.c = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * 1.44269504088896340736f;
     p.pre = a.scale == 0.0f ? 0.0f : (a.scale < 0.0f ? -1.0f : 1.0f);
     p.decay = a.decay;
