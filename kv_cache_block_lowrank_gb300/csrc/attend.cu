@@ -25,8 +25,9 @@
 // pieces of (sequence, batch, head) leave unnormalised O, m and l in the workspace, and a second
 // kernel joins them.  What one group saw from the first tile to the last needs no join: its rows
 // go out from here (a prompt of 4096 tokens 574 us, through the workspace 603; 50 trees of 248
-// nodes, head_dim 256, 453 against 595).  Row tiles beyond one (large trees, chunks) go to neighbouring CTAs that
-// walk the same range in step, so that K and V come from HBM once and from L2 to the rest.
+// nodes, head_dim 256, 453 against 595).  Row tiles beyond one (large trees, chunks) go to
+// neighbouring CTAs that walk the same range in step, so that K and V come from HBM once and from
+// L2 to the rest.
 //
 // Block weights: the softmax thread has the sum of every 16 of its tokens anyway (l is their
 // sum); with weights it stores them beside m, and once the rows' lse are known they are scaled by
@@ -394,28 +395,50 @@ struct Barriers {
 };
 
 // A whole item's row from tensor memory (anything, if it has no weight): row `to` of out, lse.
+// Four lanes exchange their 64 bytes of a row, so that a store brings them side by side (by 16
+// bytes of 32 rows it took 7400 cycles for 256 rows of 128).
 template <int HD>
 __device__ __forceinline__ void write_whole(const AttendParams& p, uint32_t o_cols, bool live,
-                                            int64_t to, float m, float l,
-                                            float* row_lse) {
+                                            int64_t to, float m, float l, float* row_lse) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int lane = threadIdx.x & 31;
+    uint16_t* at[4];  // where the lane's 16 bytes of its neighbours' rows go
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int64_t row = __shfl_sync(0xffffffffu, live ? to : -1, (lane & ~3) + r);
+        at[r] = row < 0 ? nullptr : p.out + row * HD + 8 * (lane & 3);
+    }
 #pragma unroll 1
     for (int k = 0; k < HD; k += 32) {
-        uint32_t o[32];
+        uint32_t o[32], u[4][4];
         tmem_ld_32x32b_x32(o_cols + k, o);
         tmem_ld_wait_for(o);
-        if (!live) continue;
-        uint4* at = reinterpret_cast<uint4*>(p.out + to * HD + k);
 #pragma unroll
-        for (int d = 0; d < 32; d += 8) {
-            uint32_t u[4];
+        for (int d = 0; d < 16; ++d)
+            u[d / 4][d % 4] = l == 0.0f ? 0u
+                                        : pack_bf16x2(__uint_as_float(o[2 * d]) * inv,
+                                                      __uint_as_float(o[2 * d + 1]) * inv);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                u[i] = l == 0.0f ? 0u
-                                 : pack_bf16x2(__uint_as_float(o[d + 2 * i]) * inv,
-                                               __uint_as_float(o[d + 2 * i + 1]) * inv);
-            at[d / 8] = make_uint4(u[0], u[1], u[2], u[3]);
-        }
+        for (int step = 1; step < 4; step *= 2)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i & step) continue;
+                const bool up = (lane & step) != 0;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const uint32_t give = up ? u[i][d] : u[i + step][d];
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, step);
+                    if (up)
+                        u[i][d] = got;
+                    else
+                        u[i + step][d] = got;
+                }
+            }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (at[r] != nullptr)
+                *reinterpret_cast<uint4*>(at[r] + k) =
+                    make_uint4(u[r][0], u[r][1], u[r][2], u[r][3]);
     }
     if (!live) return;
     const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
@@ -807,13 +830,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     place<C>(true, w, tile + j / kJobs, sv, par);
                     if (!(ok = wait(&bar.full[sv], par))) break;
                     uint8_t* part = sKV + sv * C::kStageBytes + half * (64 * HD * 2);
-                    bool found = false;
+                    bool found = false, wrote = false;
                     for (int k = gt + (NQ == 2 ? w * 128 : 0); k < 64 * kChunks;
                          k += NQ == 2 ? 256 : 128) {
                         const int r = k % 64, ch = k / 64;
                         if (pos0 + r < x.ctx) continue;
                         uint8_t* at = part + ((r >> 3) * kChunks + ch) * 1024;
                         if (pos0 + r >= x.tokens) {
+                            wrote = true;
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 *reinterpret_cast<uint4*>(
@@ -851,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *(volatile int*)&bar.bad_value[w][seg & 1] = seg;
                         if (NQ == 2) *(volatile int*)&bar.bad_value[w ^ 1][seg & 1] = seg;
                     }
-                    fence_proxy_async_smem();
+                    if (wrote || found) fence_proxy_async_smem();
                     if (NQ == 2) {  // both groups read the tile: both wait until all of it is fit
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar.values);
@@ -870,9 +894,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float t0 = top0;
                     order_after_wait(t0);
                     order_after_wait(top);
-                    top = fmaxf(top, t0);
-                    if (special) {
+                    if (!special) {
+                        top = fmaxf(top, t0);
+                    } else {
                         // What the row does not see goes to -inf.
+                        if (p.pre != 1.0f) {
+#pragma unroll
+                            for (int d = 0; d < 64; ++d)
+                                v[d] = __float_as_uint(__uint_as_float(v[d]) * p.pre);
+                        }
+                        const float seen[2] = {t0, top};
                         top = -INFINITY;
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
@@ -881,11 +912,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 bits = visible32(p, x, node, pos0 + 32 * k, word0, word1);
                             if ((bad >> (2 * k)) & 1) bits &= 0xFFFF0000u;
                             if ((bad >> (2 * k)) & 2) bits &= 0x0000FFFFu;
+                            if (__all_sync(0xffffffffu, bits == 0xFFFFFFFFu || row >= live) &&
+                                p.pre == 1.0f) {
+                                top = fmaxf(top, seen[k]);  // (unused rows may hold anything)
+                                continue;
+                            }
 #pragma unroll
                             for (int d = 0; d < 32; ++d) {
-                                const float s = (bits >> d) & 1
-                                                    ? __uint_as_float(v[32 * k + d]) * p.pre
-                                                    : -INFINITY;
+                                const float s = (bits >> d) & 1 ? __uint_as_float(v[32 * k + d])
+                                                                : -INFINITY;
                                 v[32 * k + d] = __float_as_uint(s);
                                 top = fmaxf(top, s);
                             }
