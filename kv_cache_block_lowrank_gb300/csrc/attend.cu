@@ -99,6 +99,11 @@ struct Cfg {
     static_assert(kRing0 + 2 <= kMetaRing, "tiles in flight");
 };
 
+// Where a CTA's range of the list begins: tile t of (sequence s, batch b, head h).
+struct Start {
+    int s, b, h, t, item0, total, per;
+};
+
 struct AttendParams {
     const uint16_t* V;
     uint16_t* out;
@@ -126,6 +131,7 @@ struct AttendParams {
     int32_t* lib_error;
     // workspace
     int32_t* header;     // [0] tiles in all, [1] tiles per group
+    Start* starts;       // [groups] where each range begins
     int32_t* seq_tiles;  // [num_seqs] tiles before a sequence
     int32_t* seq_items;  // [num_seqs] (batch, head) items before a sequence
     float* part_o;       // [slot][row][head_dim], or [slot][head_dim][row] with ways
@@ -161,7 +167,7 @@ __device__ __forceinline__ int tokens_upto(const AttendParams& p, const SeqInfo&
 }
 template <int TILE>
 __device__ __forceinline__ int tiles_upto(const AttendParams& p, const SeqInfo& x, int nodes) {
-    return (tokens_upto(p, x, nodes) + TILE - 1) / TILE;
+    return max(1, (tokens_upto(p, x, nodes) + TILE - 1) / TILE);
 }
 template <int TILE>
 __device__ __forceinline__ int batch_tiles(const AttendParams& p, const SeqInfo& x, int span,
@@ -179,10 +185,6 @@ __device__ __forceinline__ int seq_tiles(const AttendParams& p, const SeqInfo& x
     for (int b = 0; b < nb; ++b) w += batch_tiles<TILE>(p, x, span, b);
     return w * p.nkv;
 }
-
-struct Start {
-    int s, b, h, t, item0, total, per;
-};
 
 // One piece of this CTA's range: tiles [ta, ta + n) of (sequence, head) for row tile rt.
 struct Segment {
@@ -398,7 +400,8 @@ struct Barriers {
 // Four lanes exchange their 64 bytes of a row, so that a store brings them side by side (by 16
 // bytes of 32 rows it took 7400 cycles for 256 rows of 128).
 template <int HD>
-__device__ __forceinline__ void write_whole(const AttendParams& p, uint32_t o_cols, bool live,
+__device__ __forceinline__ void write_whole(const AttendParams& p, const SeqInfo& x, int node,
+                                            int h, bool bad, uint32_t o_cols, bool live,
                                             int64_t to, float m, float l, float* row_lse) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int lane = threadIdx.x & 31;
@@ -413,6 +416,21 @@ __device__ __forceinline__ void write_whole(const AttendParams& p, uint32_t o_co
         uint32_t o[32], u[4][4];
         tmem_ld_32x32b_x32(o_cols + k, o);
         tmem_ld_wait_for(o);
+        if (bad && live) {
+            // Non-finite values of the nodes this row sees.
+            for (int j = 0; j < x.nodes && x.ctx + j < x.tokens; ++j) {
+                if (!((node_word(p, x, node, j >> 6) >> (j & 63)) & 1)) continue;
+                const int pos = x.ctx + j;
+                const int64_t id = p.table[x.e0 + pos / p.bs];
+                if (id < 0 || id >= p.max_blocks) continue;
+                const uint16_t* v = p.V + ((id * p.bs + pos % p.bs) * p.nkv + h) * HD + k;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float e = __uint_as_float(static_cast<uint32_t>(v[c]) << 16);
+                    if (!isfinite(e)) o[c] = __float_as_uint(__uint_as_float(o[c]) + e);
+                }
+            }
+        }
 #pragma unroll
         for (int d = 0; d < 16; ++d)
             u[d / 4][d % 4] = l == 0.0f ? 0u
@@ -576,7 +594,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             before += n;
             items_before += nb * p.nkv;
         }
+        if (threadIdx.x == 0 && f0 >= total) bar.start.t = 0;  // no range: not within an item
         __syncthreads();
+        if (threadIdx.x == 0 && blockIdx.x % p.members == 0)
+            p.starts[blockIdx.x / p.members] = bar.start;
     }
     const uint32_t tmem = bar.tmem;
     volatile int* abort_flag = &bar.abort;
@@ -1009,11 +1030,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool bad =
                     jobs > 0 && *(volatile int*)&bar.bad_value[w][segs & 1] ==
                                     static_cast<int>(segs);
-                // (What is bad the join adds.)
-                if (C::kWhole && !bad && walk.whole(p, g)) {
+                if (C::kWhole && walk.whole(p, g)) {
                     const int64_t to = (static_cast<int64_t>(x.q0) + node) * p.nq + walk.h * p.g +
                                        row % p.g;
-                    write_whole<HD>(p, o_cols, row < live, to, m, l,
+                    write_whole<HD>(p, x, node, walk.h, bad, o_cols, row < live, to, m, l,
                                     p.sums == nullptr
                                         ? nullptr
                                         : p.row_lse + ((static_cast<int64_t>(g.item) * p.members +
@@ -1114,6 +1134,52 @@ __device__ __forceinline__ void write_row(const AttendParams& p, const SeqInfo& 
     }
 }
 
+// What a CTA of the join is about: (sequence, row tile, head) and where its pieces are.
+struct Unit {
+    SeqInfo x;
+    int s, rt, h, member, g0, g1;  // groups from g0 to g1 have pieces
+    int64_t item;
+};
+
+// By number; false if there is nothing to join.
+template <int HD, int NQ>
+__device__ __forceinline__ bool unit_by_number(const AttendParams& p, int unit, int row_tiles,
+                                               Unit& u) {
+    using C = Cfg<HD, NQ>;
+    u.rt = unit % row_tiles;
+    u.h = unit / row_tiles % p.nkv;
+    u.s = unit / row_tiles / p.nkv;
+    u.x = load_seq(p, u.s);
+    const int b = u.rt / p.members, per = p.header[1];
+    u.member = u.rt % p.members;
+    u.item = p.seq_items[u.s] + b * p.nkv + u.h;
+    if (u.rt * NQ * p.nodes_tile >= u.x.nodes) return false;
+    int f, n;
+    item_range<C::kTile>(p, u.x, NQ * p.nodes_tile, p.seq_tiles[u.s], b, u.h, f, n);
+    u.g0 = f / per;
+    u.g1 = (f + n - 1) / per;
+    return !(C::kWhole && u.g0 == u.g1);
+}
+
+// By the end of a group's range and the member: what was cut there.
+template <int HD, int NQ>
+__device__ __forceinline__ bool unit_by_cut(const AttendParams& p, int number, Unit& u) {
+    using C = Cfg<HD, NQ>;
+    const int group = 1 + number / p.members, per = p.header[1];
+    const Start st = p.starts[group];
+    const int f = group * per - st.t;  // the item's first tile
+    u.g0 = group - 1;
+    if (st.t == 0 || f / per != u.g0) return false;  // not cut here, or here not first
+    u.s = st.s;
+    u.h = st.h;
+    u.x = load_seq(p, u.s);
+    u.member = number % p.members;
+    u.rt = st.b * p.members + u.member;
+    u.item = st.item0 + st.b * p.nkv + st.h;
+    u.g1 = (f + batch_tiles<C::kTile>(p, u.x, NQ * p.nodes_tile, st.b) - 1) / per;
+    return u.rt * NQ * p.nodes_tile < u.x.nodes;
+}
+
 // Joins the pieces of the rows.  Few rows: a CTA takes 8 / WPR rows of one (sequence, row tile,
 // head), WPR warps to a row, so that the pieces of a row (a long sequence is cut into as many as
 // there are CTAs to share it) are on their way together.
@@ -1121,7 +1187,6 @@ template <int HD, int NQ, int WPR>
 __device__ __forceinline__ void join_rows(const AttendParams& p, int block, int row_tiles,
                                           int row_parts) {
     using C = Cfg<HD, NQ>;
-    constexpr int TILE = C::kTile;
     constexpr int kEach = HD / 32;  // elements of a row per lane, in pairs
     constexpr int kAtOnce = 32 / kEach;
     constexpr int kPieceWidth = NQ == 1 ? C::kGroups : 1;  // pieces of a row per CTA group
@@ -1130,22 +1195,16 @@ __device__ __forceinline__ void join_rows(const AttendParams& p, int block, int 
     const int span = NQ * p.nodes_tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = block % row_parts;
-    const int unit = block / row_parts;
-    const int rt = unit % row_tiles;
-    const int h = unit / row_tiles % p.nkv;
-    const int s = unit / row_tiles / p.nkv;
+    Unit u;
+    if (!unit_by_number<HD, NQ>(p, block / row_parts, row_tiles, u)) return;
+    const SeqInfo& x = u.x;
+    const int rt = u.rt, h = u.h, member = u.member, g0 = u.g0;
+    const int64_t item = u.item;
     const int sub = warp % WPR;
     const int r = part * (8 / WPR) + warp / WPR;
-    const SeqInfo x = load_seq(p, s);
-    const int seq0 = p.seq_tiles[s], per = p.header[1];
-    const int b = rt / p.members, member = rt % p.members;
-    const int64_t item = p.seq_items[s] + b * p.nkv + h;
     const int rows = min(max(x.nodes - rt * span, 0), span) * p.g;
     const bool mine = r < rows;
-    int f, n;
-    item_range<TILE>(p, x, span, seq0, b, h, f, n);
-    const int g0 = n > 0 ? f / per : 0, g1 = n > 0 ? (f + n - 1) / per : -1;
-    const int pieces = mine ? (g1 - g0 + 1) * kPieceWidth : 0;
+    const int pieces = mine ? (u.g1 - g0 + 1) * kPieceWidth : 0;
     const int node = rt * span + r / p.g;
     const int qt = NQ == 2 ? r / (p.nodes_tile * p.g) : 0;
     const int lr = r - qt * p.nodes_tile * p.g;
@@ -1155,7 +1214,6 @@ __device__ __forceinline__ void join_rows(const AttendParams& p, int block, int 
         const int w = NQ == 2 ? qt : k % kPieceWidth;
         return ((item + g0 + grp) * p.members + member) * 2 + w;
     };
-    if (C::kWhole && mine && g0 == g1 && p.part_bad[slot_of(0)] == 0) return;
     float top = -INFINITY, l = 0.0f, acc[kEach];
     int bad = 0;
 #pragma unroll
@@ -1255,29 +1313,27 @@ template <int HD>
 __device__ __forceinline__ void join_many(const AttendParams& p, int block, int row_tiles,
                                           int row_parts) {
     using C = Cfg<HD, 1>;
-    constexpr int TILE = C::kTile;
     constexpr int kEach = HD / 32;
     constexpr int kPieceWidth = C::kGroups;
     const int span = p.nodes_tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int part = block % row_parts, unit = block / row_parts;
-    const int rt = unit % row_tiles, h = unit / row_tiles % p.nkv, s = unit / row_tiles / p.nkv;
+    const int part = block % row_parts;
     const int r0 = part * 32 + warp * 4;
-    const SeqInfo x = load_seq(p, s);
-    const int seq0 = p.seq_tiles[s], per = p.header[1];
-    const int b = rt / p.members, member = rt % p.members;
-    const int64_t item = p.seq_items[s] + b * p.nkv + h;
+    Unit u;
+    if (!(C::kWhole && row_tiles == 0
+              ? unit_by_cut<HD, 1>(p, block / row_parts, u)
+              : unit_by_number<HD, 1>(p, block / row_parts, row_tiles, u)))
+        return;
+    const SeqInfo& x = u.x;
+    const int rt = u.rt, h = u.h, member = u.member, g0 = u.g0;
+    const int64_t item = u.item;
     const int rows = min(max(x.nodes - rt * span, 0), span) * p.g;
     if (r0 >= rows) return;
-    int f, n;
-    item_range<TILE>(p, x, span, seq0, b, h, f, n);
-    const int g0 = n > 0 ? f / per : 0, g1 = n > 0 ? (f + n - 1) / per : -1;
-    const int pieces = (g1 - g0 + 1) * kPieceWidth;
+    const int pieces = (u.g1 - g0 + 1) * kPieceWidth;
     auto place_of = [&](int r, int k) -> int64_t {  // row r's piece k, in rows of the workspace
         return (((item + g0 + k / kPieceWidth) * p.members + member) * 2 + k % kPieceWidth) *
                    p.rowcap + r;
     };
-    if (C::kWhole && g0 == g1 && p.part_bad[place_of(0, 0) / p.rowcap] == 0) return;
     // m of the row: lane 8 q + i looks at pieces i, i + 8, ... of row r0 + q
     const int my_row = min(r0 + lane / 8, rows - 1);
     float top = -INFINITY, l = 0.0f;
@@ -1351,35 +1407,31 @@ template <int HD, int NQ>
 __device__ __forceinline__ void join_columns(const AttendParams& p, int block, int row_tiles,
                                              int row_parts) {
     using C = Cfg<HD, NQ>;
-    constexpr int TILE = C::kTile;
     constexpr int kPieceWidth = NQ == 1 ? C::kGroups : 1;
     __shared__ float sums[8][32][kJoinCols + 1];
     __shared__ float2 stats[8][32];
     __shared__ int flags[8];
-    const int span = NQ * p.nodes_tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int unit = block / row_parts, ways = p.ways;
+    const int ways = p.ways;
     const int way = warp % ways, task = (block % row_parts * 8 + warp) / ways;
-    const int rt = unit % row_tiles, h = unit / row_tiles % p.nkv, s = unit / row_tiles / p.nkv;
     const int cb = task % (HD / kJoinCols), r32 = task / (HD / kJoinCols) % ceil_div(p.rowcap, 32);
     const int qt = task / (HD / kJoinCols) / ceil_div(p.rowcap, 32);
-    const SeqInfo x = load_seq(p, s);
-    const int seq0 = p.seq_tiles[s], per = p.header[1];
-    const int b = rt / p.members, member = rt % p.members;
-    const int64_t item = p.seq_items[s] + b * p.nkv + h;
+    Unit u;
+    if (!(C::kWhole && row_tiles == 0
+              ? unit_by_cut<HD, NQ>(p, block / row_parts, u)
+              : unit_by_number<HD, NQ>(p, block / row_parts, row_tiles, u)))
+        return;
+    const SeqInfo& x = u.x;
+    const int rt = u.rt, h = u.h, member = u.member, g0 = u.g0;
+    const int64_t item = u.item;
     const int first = (rt * NQ + qt) * p.nodes_tile;  // node of the tile's first row
     const int rows = qt < NQ ? min(max(x.nodes - first, 0), p.nodes_tile) * p.g : 0;
-    int f, n;
-    item_range<TILE>(p, x, span, seq0, b, h, f, n);
-    const int g0 = n > 0 ? f / per : 0, g1 = n > 0 ? (f + n - 1) / per : -1;
     auto slot_of = [&](int k) -> int64_t {
         return ((item + g0 + k / kPieceWidth) * p.members + member) * 2 +
                (NQ == 2 ? qt : k % kPieceWidth);
     };
-    const bool done =
-        C::kWhole && r32 * 32 < rows && g0 == g1 && p.part_bad[slot_of(0)] == 0;
-    if (r32 * 32 < rows && !done) {
-        const int pieces = (g1 - g0 + 1) * kPieceWidth;
+    if (r32 * 32 < rows) {
+        const int pieces = (u.g1 - g0 + 1) * kPieceWidth;
         const int lr = min(r32 * 32 + lane, rows - 1);
         float top = -INFINITY, l = 0.0f, acc[kJoinCols];
         int bad = 0;
@@ -1413,7 +1465,7 @@ __device__ __forceinline__ void join_columns(const AttendParams& p, int block, i
     constexpr int kLanes = kJoinCols / 8;
     for (int r0 = way * (32 / kLanes); r0 < 32; r0 += ways * (32 / kLanes)) {
         const int r = r0 + lane / kLanes, at = r32 * 32 + r, col = lane % kLanes * 8;
-        if (at >= rows || done) break;
+        if (at >= rows) break;
         float top = -INFINITY;
         int bad = 0;
         for (int w = w0; w < w0 + ways; ++w) {
@@ -1597,7 +1649,8 @@ __global__ void __launch_bounds__(256) grains_kernel(const AttendParams p, int r
 // Then an entry's weight is the sum of its granules' totals over heads and row tiles: a warp per
 // entry, its lanes on the (granule, head, row tile) triples.
 template <int HD, int NQ>
-__global__ void __launch_bounds__(256) weights_kernel(const AttendParams p, int shares) {
+__global__ void __launch_bounds__(256) weights_kernel(const AttendParams p, int shares,
+                                                      int ways) {
     using C = Cfg<HD, NQ>;
     constexpr int TILE = C::kTile, kGran = TILE / 16;
     const int span = NQ * p.nodes_tile;
@@ -1609,9 +1662,13 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p, int 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rts = ceil_div(x.nodes, span), grains = p.bs / 16;
     const int tiles = ceil_div(x.nodes, p.nodes_tile);  // row tiles with rows in use
-    for (int64_t e = x.e0 + share * 8 + warp; e < x.end; e += shares * 8) {
+    const int at_once = 8 / ways, way = warp % ways;
+    __shared__ float parts[8];
+    for (int64_t e0 = x.e0 + share * at_once; e0 < x.end; e0 += shares * at_once) {
+        const int64_t e = e0 + warp / ways;
         float sum = 0.0f;
-        for (int i = lane; i < grains * p.nkv * rts * NQ; i += 32) {
+        for (int i = way * 32 + lane; e < x.end && i < grains * p.nkv * rts * NQ;
+             i += ways * 32) {
             const int qt = i % NQ, rt = i / NQ % rts, h = i / NQ / rts % p.nkv;
             const int64_t gr = (e - x.e0) * grains + i / NQ / rts / p.nkv;
             const int seen = ceil_div(tokens_upto(p, x, min(x.nodes, (rt + 1) * span)), 16);
@@ -1625,7 +1682,13 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p, int 
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0)
+        if (ways > 1) {
+            __syncthreads();
+            if (lane == 0) parts[warp] = sum;
+            __syncthreads();
+            for (int k = 1; way == 0 && k < ways; ++k) sum += parts[warp + k];
+        }
+        if (lane == 0 && way == 0 && e < x.end)
             p.weights_out[e] = (p.weights_in != nullptr ? p.weights_in[e] * p.decay : 0.0f) + sum;
     }
 }
@@ -1636,8 +1699,9 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttendParams p, int 
 constexpr int kFewRows = 256;  // rows of a sequence, nodes times query heads
 
 template <int HD, int WPR>
-__global__ void __launch_bounds__(256, 3) finish_kernel(const AttendParams p, int row_parts,
-                                                     int join_ctas, int shares) {
+__global__ void __launch_bounds__(256, 3) finish_kernel(const AttendParams p, int row_tiles,
+                                                        int row_parts, int join_ctas,
+                                                        int shares) {
     using C = Cfg<HD, 1>;
     __shared__ float sh_lse[kFewRows];
     grid_dependency_wait();
@@ -1646,9 +1710,9 @@ __global__ void __launch_bounds__(256, 3) finish_kernel(const AttendParams p, in
         if constexpr (WPR > 1)
             join_rows<HD, 1, WPR>(p, blockIdx.x, 1, row_parts);
         else if (p.ways > 0)
-            join_columns<HD, 1>(p, blockIdx.x, 1, row_parts);
+            join_columns<HD, 1>(p, blockIdx.x, row_tiles, row_parts);
         else
-            join_many<HD>(p, blockIdx.x, 1, row_parts);
+            join_many<HD>(p, blockIdx.x, row_tiles, row_parts);
         return;
     }
     const int s = (blockIdx.x - join_ctas) / shares, share = (blockIdx.x - join_ctas) % shares;
@@ -1721,7 +1785,8 @@ struct Plan {
     bool few;        // few rows in all: a CTA joins one
     int tasks, ways;  // of join_columns: a unit's tasks and the warps to each, 0 for part_o by row
     int64_t slots, tiles, units;
-    size_t header, seq_tiles, seq_items, part_o, part_ml, part_bad, row_lse, sums, sums_m, bytes;
+    size_t header, starts, seq_tiles, seq_items, part_o, part_ml, part_bad, row_lse, sums, sums_m,
+        bytes;
 };
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
@@ -1764,7 +1829,8 @@ Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total
         // Warps to a task while there are pieces for them and the GPU has room.
         const int width = p.nq_tiles == 1 && d.head_dim < 256 ? 2 : 1;  // softmax groups to a row
         const int64_t pieces = (p.groups * p.members + units - 1) / units * width + 1;
-        for (p.ways = 1; p.ways < 8 && p.ways < pieces && units * p.tasks * p.ways < 32 * kCtas;)
+        const int64_t cut = width == 2 ? units : std::min(units, int64_t{p.groups} * p.members);
+        for (p.ways = 1; p.ways < 8 && p.ways < pieces && cut * p.tasks * p.ways < 32 * kCtas;)
             p.ways *= 2;
     }
     const int64_t batches = (p.row_tiles + p.members - 1) / p.members;
@@ -1779,6 +1845,7 @@ Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total
         return here;
     };
     p.header = take(8);
+    p.starts = take(p.groups * sizeof(Start));
     p.seq_tiles = take(static_cast<size_t>(num_seqs) * 4);
     p.seq_items = take(static_cast<size_t>(num_seqs) * 4);
     p.part_bad = take(static_cast<size_t>(p.slots) * 4);
@@ -1831,7 +1898,13 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
     const int parts = few          ? unit_rows
                       : p.ways > 0 ? (plan.tasks * p.ways + 7) / 8
                                    : (unit_rows + 31) / 32;
-    const int64_t join_ctas = units * parts;
+    // What one group saw whole needs no join: where there are more units than cuts of the list, the
+    // join goes by the cuts (43 trees of 202 nodes, 2408 units and 144 cuts: 60 us by unit, 4 by
+    // cut; 3 trees of 31 to 95 nodes, 6 units and 150 cuts: 11 and 18).
+    const int64_t cuts = static_cast<int64_t>(plan.groups - 1) * plan.members;
+    const bool by_cut = C::kWhole && !few && cuts < units;
+    const int64_t join_ctas = (by_cut ? cuts : units) * parts;
+    const int row_tiles = by_cut ? 0 : plan.row_tiles;  // (0: by cut)
     // CTAs to a sequence's entries: an even share of all entries in one pass, if the sequences
     // are alike, within what the GPU holds at once.
     // Join and weights in one launch while a lane has few (row, granule) pairs of an entry to look
@@ -1840,7 +1913,12 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
     const int64_t seq_rows = static_cast<int64_t>(p.max_q) * p.nq;
     const bool few_each = NQ == 1 && plan.row_tiles == 1 && p.weights_out != nullptr &&
                           seq_rows <= kFewRows && (seq_rows + 31) / 32 * (p.bs / 16) <= 8;
-    const int64_t per_cta = few_each ? 8 * kEntries : 8;
+    // Warps to an entry: one for every 32 of its (granule, row tile, head) sums.  (8 trees of 81 to
+    // 245 nodes of 128 heads: 32 us with one warp an entry, 9 with eight.)
+    const int64_t each = static_cast<int64_t>(p.bs / 16) * p.nkv * plan.row_tiles * NQ;
+    int ways = 1;
+    while (ways < 8 && ways * 32 < each) ways *= 2;
+    const int64_t per_cta = few_each ? 8 * kEntries : 8 / ways;
     const int64_t even = (p.total_blocks / std::max(p.num_seqs, 1) + per_cta) / per_cta;
     const int64_t most = std::max<int64_t>(1, 8 * kCtas / std::max(p.num_seqs, 1));
     const int shares = static_cast<int>(std::min(even, most));
@@ -1850,16 +1928,16 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
             if (grid > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
             auto finish = few ? finish_kernel<HD, 8> : finish_kernel<HD, 1>;
             if (launch_pdl(finish, dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, p,
-                           parts, static_cast<int>(join_ctas), shares) != cudaSuccess)
+                           row_tiles, parts, static_cast<int>(join_ctas), shares) != cudaSuccess)
                 return HSS_ERR_CUDA;
             return HSS_OK;
         }
     }
-    if (rows) {
+    if (rows && join_ctas > 0) {
         if (join_ctas > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
         auto join = few ? join_kernel<HD, NQ, 8> : join_kernel<HD, NQ, 1>;
         if (launch_pdl(join, dim3(static_cast<unsigned>(join_ctas)), dim3(256), 0, stream, p,
-                       plan.row_tiles, parts) != cudaSuccess)
+                       row_tiles, parts) != cudaSuccess)
             return HSS_ERR_CUDA;
     }
     if (rows && p.weights_out != nullptr) {
@@ -1876,7 +1954,7 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
     }
     if (p.weights_out != nullptr &&
         launch_pdl(weights_kernel<HD, NQ>, dim3(static_cast<unsigned>(p.num_seqs * shares)),
-                   dim3(256), 0, stream, p, shares) != cudaSuccess)
+                   dim3(256), 0, stream, p, shares, ways) != cudaSuccess)
         return HSS_ERR_CUDA;
     return HSS_OK;
 }
@@ -1931,6 +2009,7 @@ hss_status launch_attend(const AttendArgs& r, cudaStream_t stream) {
     p.lib_error = dev->error_word;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     p.header = reinterpret_cast<int32_t*>(ws + plan.header);
+    p.starts = reinterpret_cast<Start*>(ws + plan.starts);
     p.seq_tiles = reinterpret_cast<int32_t*>(ws + plan.seq_tiles);
     p.seq_items = reinterpret_cast<int32_t*>(ws + plan.seq_items);
     p.part_o = reinterpret_cast<float*>(ws + plan.part_o);

@@ -397,3 +397,60 @@ def test_cache_past_32_bits():
     c = Case(128, 8, 8, 16, [700], [3], "tree", seed=24, max_blocks=150000)
     assert int(c.table.min()) * 16 * 8 * 128 > 2 ** 31
     c.check(c.gpu())
+
+
+# Many short sequences of many rows: most (sequence, head) items lie whole in one CTA's range.
+@pytest.mark.parametrize("hd,nq,nkv,bs", [(64, 16, 4, 16), (128, 21, 3, 48), (192, 8, 2, 16),
+                                          (256, 12, 4, 32)])
+@pytest.mark.parametrize("kind", ["tree", "chain", "holes"])
+def test_many_short_sequences_of_many_rows(hd, nq, nkv, bs, kind):
+    ctx = [(37 * i) % 131 for i in range(45)]
+    nodes = [1 + (53 * i) % 97 for i in range(45)]
+    c = Case(hd, nq, nkv, bs, ctx, nodes, kind, seed=40 + hd)
+    c.check(c.gpu())
+
+
+@pytest.mark.parametrize("hd", [64, 128, 192, 256])
+def test_a_bad_value_among_many_short_sequences(hd):
+    n = 70
+    c = Case(hd, 8, 2, 16, [(29 * i) % 90 for i in range(40)], [n] * 40, "tree", seed=50, std=0.5)
+    for s in range(0, 40, 3):
+        c.v[s][c.ctx[s] + 3, 1, 5] = math.inf
+        c.v[s][c.ctx[s] + 66, 0, 60] = math.nan
+    out, lse, w = c.gpu()
+    assert w.isfinite().all() and lse.isfinite().all()
+    o = out.cpu().view(40, n, 8, hd)
+    for s in range(40):
+        for node, head, dim in ((3, 1, 5), (66, 0, 60)):
+            rows = c.sees[s][:, node] if s % 3 == 0 else torch.zeros(n, dtype=torch.bool)
+            part = o[s, :, head * 4:head * 4 + 4, dim]
+            assert not part[rows].isfinite().any() and part[~rows].isfinite().all()
+    o = o.clone()
+    o[:, :, 4:, 5] = 0
+    o[:, :, :4, 60] = 0
+    assert o.isfinite().all()
+
+
+@pytest.mark.parametrize("hd,nodes", [(64, [150, 150, 80]), (128, [3, 2, 4]), (192, [90, 1, 2]),
+                                      (256, [150, 70, 80])])
+def test_rows_of_a_sequence_without_tokens_are_zero(hd, nodes):
+    c = Case(hd, 8, 2, 16, [0, 0, 30], nodes, "tree", seed=60)
+    a, b = c.blocks[0], c.blocks[0] + c.blocks[1]
+    c.table = torch.cat([c.table[:a], c.table[b:]])
+    c.w_in = torch.cat([c.w_in[:a], c.w_in[b:]])
+    c.blocks[1] = 0
+    c.total_blocks = sum(c.blocks)
+    keep = c.k[1], c.v[1]
+    c.k[1], c.v[1] = keep[0][:0], keep[1][:0]
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = c.gpu(status=st)
+    assert st.item() == hss.HSS_ERR_OUT_OF_RANGE
+    hss.hss_read_device_error()
+    c.k[1], c.v[1] = keep
+    hide = [torch.zeros(x + t, dtype=torch.bool) for x, t in zip(c.ctx, c.nodes)]
+    hide[1][:] = True
+    # (nothing of the hidden sequence's weights can be asked for: it has no entries)
+    lse, at = got[1], c.nodes[0]
+    assert (got[0][at:at + c.nodes[1]] == 0).all()
+    assert (lse[at:at + c.nodes[1]] == -math.inf).all()
+    c.check((got[0], lse, None), hide=hide)
