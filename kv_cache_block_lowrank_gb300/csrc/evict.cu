@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_kernel(const EvictArgs e) {
     const int slice = rounds * kWarps * step;
     const int slice0 = rank * slice;
     const float* w_in = e.weights + first;
+    const int32_t* table = e.table + first;
     uint32_t key[kKeys];
     // (entries that may not go get the largest key and are never counted)
     auto load = [&](int q) {
@@ -116,11 +117,27 @@ __global__ void __launch_bounds__(kThreads, 1) evict_kernel(const EvictArgs e) {
             key[j] = in ? rankdev::score_key(__ldg(w_in + i)) : 0xFFFFFFFFu;
         }
     };
+    // What is packed, all of a round on its way together and ahead of the ranks (one entry after
+    // another, each of a thread's 16 waited for its own loads: 8 sequences of 65536 entries 27 us,
+    // so 22).
+    int32_t id[kKeys];
+    float weight[kKeys];
+    auto fetch = [&](int q) {
+        const int base = slice0 + (q * kWarps + warp) * step + lane;
+#pragma unroll
+        for (int j = 0; j < kKeys; ++j) {
+            const int i = base + 32 * j;
+            const bool there = 32 * j < step && i < c.n;
+            id[j] = there ? __ldg(table + i) : 0;
+            weight[j] = there ? __ldg(w_in + i) : 0.0f;
+        }
+    };
     auto inside = [&](int q, int j, int& i) {
         i = slice0 + (q * kWarps + warp) * step + 32 * j + lane;
         return 32 * j < step && i >= c.lo && i < c.hi;
     };
     if (c.lost > 0) load(0);
+    fetch(0);
 
     // Radix select of the c.lost-th smallest key.
     uint32_t prefix = 0, need = static_cast<uint32_t>(c.lost);
@@ -218,9 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1) evict_kernel(const EvictArgs e) {
     }
 
     // Pack, round by round in index order.
-    const int32_t* table = e.table + first;
     for (int q = 0; q < rounds; ++q) {
         if (rounds > 1 && c.lost > 0) load(q);
+        if (q > 0) fetch(q);
         uint32_t wl = 0, we = 0;
         if (c.lost > 0) {
 #pragma unroll
@@ -266,13 +283,12 @@ __global__ void __launch_bounds__(kThreads, 1) evict_kernel(const EvictArgs e) {
             const uint32_t going = __ballot_sync(0xffffffffu, goes);
             const uint32_t gone = lost + __popc(going & lanes_before);
             if (i < c.n) {
-                const int32_t id = __ldg(table + i);
                 if (goes) {
-                    e.freed[lost_before + gone] = id;
+                    e.freed[lost_before + gone] = id[j];
                 } else {
                     const int64_t to = kept_before + i - gone;
-                    e.new_table[to] = id;
-                    e.new_weights[to] = __ldg(w_in + i);
+                    e.new_table[to] = id[j];
+                    e.new_weights[to] = weight[j];
                 }
             }
             t += __popc(tie);
