@@ -51,6 +51,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "ptx.cuh"
@@ -1791,31 +1792,69 @@ struct Plan {
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
-Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total_blocks,
-               bool with_weights) {
-    Plan p;
+// The plan without its split: what does not depend on the members of a group.
+Plan row_plan(const hss_dims& d, int32_t max_q) {
+    Plan p = {};
     const int g = d.num_q_heads / d.num_kv_heads;
     p.nodes_tile = kRows / g;
     p.tile = d.head_dim <= 128 ? 128 : 64;
     p.nq_tiles = max_q > p.nodes_tile && d.head_dim < 256 ? 2 : 1;
     const int span = p.nq_tiles * p.nodes_tile;
     p.row_tiles = std::max(1, (max_q + span - 1) / span);
-    // Members of a group: row tiles in step.  The choice that leaves the fewest CTAs idle (in
-    // groups that do not fill the GPU, in a last batch that is not full), larger on a tie.
-    double best = -1.0;
-    p.members = 1;
-    for (int r = 1; r <= std::min(p.row_tiles, 19); ++r) {
-        if (p.row_tiles >= 4 && r < 4) continue;
-        const int batches = (p.row_tiles + r - 1) / r;
-        const double use = static_cast<double>(kCtas / r * r) / kCtas *
-                           (static_cast<double>(p.row_tiles) / (batches * r));
-        if (use >= best) {
-            best = use;
-            p.members = r;
+    p.rowcap = std::min(kRows, g * std::min(max_q, p.nodes_tile));
+    return p;
+}
+
+constexpr int kMostMembers = 19;  // kCtas / 8
+
+// Members of a group, row tiles in step: many read K and V less often, few leave fewer CTAs
+// waiting (in a last batch that is not full, in the upper rows of a chain, in groups that do not
+// fill the GPU).  The estimate adds up the tiles that a sequence's batches walk, at 1500 cycles for
+// 64 tokens under two row tiles and 1050 under one, with as many as three tiles' time for what an
+// item costs besides, against the bytes at the memory's rate; the sequences' nodes are taken to lie
+// evenly about their mean.  Measured, in us: 8 trees of 33 nodes, head_dim 256, by 1 member 577, by
+// 3 410; 32 prompts of 512 tokens by 8 252, by 2 200; a prompt of 4096 by 2 508, by 8 496; 16
+// prompts of 100 to 300 by 5 102, by 2 82.
+int members_for(const Plan& p, const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total_q,
+                int64_t total_blocks, bool chain) {
+    if (p.row_tiles == 1) return 1;
+    const double seqs = std::max(num_seqs, 1);
+    const double nodes = std::min<double>(total_q / seqs, max_q);
+    const double fewest = std::max(1.0, 2.0 * nodes - max_q);
+    const double context =
+        std::max(0.0, (total_blocks / seqs - 0.5) * d.block_size - nodes) / p.tile;
+    const int span = p.nq_tiles * p.nodes_tile;
+    const double cycles = (p.nq_tiles == 2 ? 1500.0 : 1050.0) * (p.tile / 64);
+    const double bytes = p.tile * d.head_dim * 4.0 / 3570.0;  // in cycles: 6.79 TB/s at 1.9 GHz
+    double best = INFINITY;
+    int members = 1;
+    for (int r = 1; r <= std::min(p.row_tiles, kMostMembers); ++r) {
+        double tiles = 0.0;
+        for (int i = 0; i < 4; ++i) {
+            const double n = max_q - (max_q - fewest) * i / 3.0;
+            const double batches = std::ceil(n / (static_cast<double>(span) * r));
+            const double last = batches * span * r - n;  // nodes that the last one lacks
+            const double seen = chain ? span * r * batches * (batches + 1.0) / 2.0 - last
+                                      : batches * n;
+            tiles += batches * (context + 3.0) + seen / p.tile;
+        }
+        const double compute = tiles / (kCtas / r) * cycles, memory = tiles * bytes;
+        const double cost = std::max(compute, 1.2 * memory) + 0.3 * memory;
+        if (cost <= best) {
+            best = cost;
+            members = r;
         }
     }
+    return members;
+}
+
+Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total_blocks,
+               bool with_weights, int members) {
+    Plan p = row_plan(d, max_q);
+    const int g = d.num_q_heads / d.num_kv_heads;
+    const int span = p.nq_tiles * p.nodes_tile;
+    p.members = members;
     p.groups = std::max(1, kCtas / p.members);
-    p.rowcap = std::min(kRows, g * std::min(max_q, p.nodes_tile));
     // A CTA joins a row while that leaves SMs free (a lone sequence's 32 rows of 38 pieces).
     const int64_t units = static_cast<int64_t>(p.row_tiles) * d.num_kv_heads * num_seqs;
     p.few = units * std::min(max_q, span) * g <= 2 * kCtas;
@@ -1963,7 +2002,11 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
 
 size_t attend_workspace_bytes(const hss_dims& d, int32_t num_seqs, int32_t max_q,
                               int64_t total_blocks, bool with_weights) {
-    return make_plan(d, num_seqs, max_q, total_blocks, with_weights).bytes;
+    // (the members depend on more than the sizes given here)
+    size_t most = 0;
+    for (int r = 1; r <= std::min(row_plan(d, max_q).row_tiles, kMostMembers); ++r)
+        most = std::max(most, make_plan(d, num_seqs, max_q, total_blocks, with_weights, r).bytes);
+    return most;
 }
 
 hss_status launch_attend(const AttendArgs& r, cudaStream_t stream) {
@@ -1972,7 +2015,9 @@ hss_status launch_attend(const AttendArgs& r, cudaStream_t stream) {
     if (dev == nullptr) return HSS_ERR_CUDA;
     const hss_dims& d = a.dims;
     const bool weigh = r.weights_out != nullptr;
-    const Plan plan = make_plan(d, a.num_seqs, a.max_q, a.total_blocks, weigh);
+    const int members = members_for(row_plan(d, a.max_q), d, a.num_seqs, a.max_q, a.total_q,
+                                    a.total_blocks, a.tree_mask == nullptr);
+    const Plan plan = make_plan(d, a.num_seqs, a.max_q, a.total_blocks, weigh, members);
     if (plan.tiles > (1 << 30) || plan.slots > (1 << 30)) return HSS_ERR_INVALID_ARGUMENT;
     auto enc = tensor_map_encoder();
     if (enc == nullptr) return HSS_ERR_CUDA;
