@@ -170,10 +170,17 @@ template <int TILE>
 __device__ __forceinline__ int tiles_upto(const AttendParams& p, const SeqInfo& x, int nodes) {
     return max(1, (tokens_upto(p, x, nodes) + TILE - 1) / TILE);
 }
+// In the list an item is longer than its tiles by what it costs besides (its last product, its
+// rows' way out, the next queries), so that ranges of equal length take equal time: one tile of
+// 128 tokens, three of 64.  (None, so, and twice that: a prompt of 4096 tokens 496, 448 and 455
+// us; 4 of 1000 to 2000 210, 173 and 179; 50 trees of 248 nodes, head_dim 256, 385, 370 and 371.)
+template <int TILE>
+constexpr int kBeside = TILE == 128 ? 1 : 3;
+
 template <int TILE>
 __device__ __forceinline__ int batch_tiles(const AttendParams& p, const SeqInfo& x, int span,
                                            int b) {
-    return tiles_upto<TILE>(p, x, min(x.nodes, (b + 1) * p.members * span));
+    return tiles_upto<TILE>(p, x, min(x.nodes, (b + 1) * p.members * span)) + kBeside<TILE>;
 }
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -222,8 +229,9 @@ struct Walk {
     __device__ __forceinline__ bool next(const AttendParams& p, Segment& g) {
         while (f < f1) {
             const int n = nb > 0 ? batch_tiles<TILE>(p, x, span, b) : 0;
-            if (t < n) {
-                const int take = min(n - t, f1 - f);
+            const int real = n - kBeside<TILE>;
+            if (t < real) {
+                const int take = min(real - t, f1 - f);
                 g.x = x;
                 g.h = h;
                 g.rt = b * p.members + member;
@@ -238,6 +246,7 @@ struct Walk {
                 t += take;
                 return true;
             }
+            f += max(n - t, 0);
             t = 0;
             if (++h < p.nkv) continue;
             h = 0;
@@ -251,7 +260,7 @@ struct Walk {
     }
     // Whether the segment that next() gave is all of its item.
     __device__ __forceinline__ bool whole(const AttendParams& p, const Segment& g) const {
-        return g.ta == 0 && t == batch_tiles<TILE>(p, x, span, b);
+        return g.ta == 0 && t == batch_tiles<TILE>(p, x, span, b) - kBeside<TILE>;
     }
 };
 
@@ -1158,7 +1167,7 @@ __device__ __forceinline__ bool unit_by_number(const AttendParams& p, int unit, 
     int f, n;
     item_range<C::kTile>(p, u.x, NQ * p.nodes_tile, p.seq_tiles[u.s], b, u.h, f, n);
     u.g0 = f / per;
-    u.g1 = (f + n - 1) / per;
+    u.g1 = (f + n - kBeside<C::kTile> - 1) / per;
     return !(C::kWhole && u.g0 == u.g1);
 }
 
@@ -1174,10 +1183,12 @@ __device__ __forceinline__ bool unit_by_cut(const AttendParams& p, int number, U
     u.s = st.s;
     u.h = st.h;
     u.x = load_seq(p, u.s);
+    const int n = batch_tiles<C::kTile>(p, u.x, NQ * p.nodes_tile, st.b) - kBeside<C::kTile>;
+    if (st.t >= n) return false;  // cut behind its tiles
     u.member = number % p.members;
     u.rt = st.b * p.members + u.member;
     u.item = st.item0 + st.b * p.nkv + st.h;
-    u.g1 = (f + batch_tiles<C::kTile>(p, u.x, NQ * p.nodes_tile, st.b) - 1) / per;
+    u.g1 = (f + n - 1) / per;
     return u.rt * NQ * p.nodes_tile < u.x.nodes;
 }
 
@@ -1551,7 +1562,7 @@ __device__ __forceinline__ void entry_weights(const AttendParams& p, const SeqIn
     for (int q = 0; q < kEntries; ++q) sum[q] = 0.0f;
     const int seen = ceil_div(tokens_upto(p, x, x.nodes), 16);
     const int rows = x.nodes * p.g;
-    const int n = tiles_upto<TILE>(p, x, x.nodes);
+    const int n = batch_tiles<TILE>(p, x, p.nodes_tile, 0);  // (one batch)
     for (int i = lane; i < rows * p.nkv; i += 32) {
         const int h = i / rows, r = i - h * rows;
         const float lse = lse_of[i];
@@ -1724,7 +1735,7 @@ __global__ void __launch_bounds__(256, 3) finish_kernel(const AttendParams p, in
     const int rows = x.nodes * p.g;  // of a head
     const int entries = x.end - x.e0;
     if (share * 8 * kEntries >= entries) return;
-    const int n = tiles_upto<C::kTile>(p, x, x.nodes);
+    const int n = batch_tiles<C::kTile>(p, x, p.nodes_tile, 0);  // (one batch)
     // lse of row i = (head, row): as many lanes to a row as keep the CTA busy
     const int all = rows * p.nkv;
     const int lanes = all <= 8 ? 32 : all <= 16 ? 16 : all <= 32 ? 8 : all <= 64 ? 4 : 1;
@@ -1735,7 +1746,7 @@ __global__ void __launch_bounds__(256, 3) finish_kernel(const AttendParams p, in
         if (i < all && n > 0) {
             const int h = i / rows, lr = i % rows;
             const int f = seq0 + h * n;
-            const int g0 = f / per, g1 = (f + n - 1) / per;
+            const int g0 = f / per, g1 = (f + n - kBeside<C::kTile> - 1) / per;
             const int pieces = (g1 - g0 + 1) * C::kGroups;
             for (int k0 = at; k0 < pieces; k0 += 8 * lanes) {
                 float2 ml[8];
@@ -1876,7 +1887,9 @@ Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total
     const int64_t items = batches * d.num_kv_heads * num_seqs;
     p.units = items * p.members * p.nq_tiles;
     p.slots = (items + p.groups) * p.members * 2;
-    p.tiles = batches * d.num_kv_heads * (total_blocks * d.block_size / p.tile + num_seqs);
+    const int beside = p.tile == 128 ? kBeside<128> : kBeside<64>;
+    p.tiles = batches * d.num_kv_heads *
+              (total_blocks * d.block_size / p.tile + int64_t{1 + beside} * num_seqs);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
