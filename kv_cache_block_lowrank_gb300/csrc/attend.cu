@@ -21,7 +21,7 @@
 //                group's products.
 //
 // Split.  All (sequence, batch of row tiles, kv head, tile) units form one list, cut into equal
-// contiguous ranges: every SM gets the same number of tiles whatever the lengths are.  A range's
+// contiguous ranges: every SM gets the same work whatever the lengths are.  A range's
 // pieces of (sequence, batch, head) leave unnormalised O, m and l in the workspace, and a second
 // kernel joins them.  What one group saw from the first tile to the last needs no join: its rows
 // go out from here (a prompt of 4096 tokens 574 us, through the workspace 603; 50 trees of 248
@@ -35,19 +35,21 @@
 // float atomics: the same call gives the same bits.
 //
 // What bounds it, and what it reaches on GB300 (HBM 6.79 TB/s and 1906 TFLOP/s bf16 measured):
-// few rows, the bytes of K and V: 64 sequences of 1k to 16k tokens, 32 query heads on 8 of 128, 373
+// few rows, the bytes of K and V: 64 sequences of 1k to 16k tokens, 32 query heads on 8 of 128, 372
 // us with weights and join, 6.1 TB/s; one sequence of 32k tokens 38 us, of which 20 are its bytes
 // and the rest the start (sequence lengths, block ids and the first tiles, one way through memory
 // after another, 7 us), the last tiles and the join (8 us).  Many rows, the products and the
 // exponentials between them, both near 1400 cycles for a job of 2 x 128 rows by 64 tokens: 512
-// rows of 64 heads over 131072 tokens 1.37 ms alone (1.6 PFLOP/s), 1.49 ms under the power cap of
-// a long run.
+// rows of 64 heads over 131072 tokens 1.34 ms alone (1.6 PFLOP/s), 1.48 ms under the power cap of
+// a long run.  Many short items, what each costs besides its tiles (4 to 5 us): a prompt of 4096
+// tokens, 64 heads, 449 us (1.2 PFLOP/s); 43 trees of 202 nodes over nothing 146 us, of which 42
+// are the bytes of queries and results.
 //
 // Masked places.  Tokens of the context need no mask; a tile that holds nodes, the end of the
 // sequence or a bad block id gets 32 visibility bits per 32 tokens and row.  A zero weight does
 // not silence an infinite or NaN value in a matrix product, so before such a tile's second
 // product the group clears the values past the end and any non-finite element of a node's
-// value, and the join adds those elements to the rows that do see the node.
+// value, and whoever writes the rows adds those elements to those that do see the node.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -1050,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                         walk.member) * NQ +
                                                        (NQ == 2 ? w : 0)) * p.rowcap + row);
                 } else if (jobs > 0) {
-#pragma unroll 1
+#pragma unroll 2
                     for (int k = 0; k < HD; k += 32) {
                         uint32_t o[32];
                         tmem_ld_32x32b_x32(o_cols + k, o);
