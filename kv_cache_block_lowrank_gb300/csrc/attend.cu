@@ -42,10 +42,10 @@
 // exponentials between them, both near 1400 cycles for a job of 2 x 128 rows by 64 tokens: 512
 // rows of 64 heads over 131072 tokens 1.34 ms alone (1.6 PFLOP/s), 1.48 ms under the power cap of
 // a long run.  Many short items, what each costs besides its tiles (4 to 5 us): a prompt of 4096
-// tokens, 64 heads, 449 us (1.2 PFLOP/s); 43 trees of 202 nodes over nothing 146 us, of which 42
-// are the bytes of queries and results.
+// tokens, 64 heads, 282 us (1 PFLOP/s of what its rows see); 43 chains of 202 nodes over nothing
+// 132 us, of which 42 are the bytes of queries and results.
 //
-// Masked places.  Tokens of the context need no mask; a tile that holds nodes, the end of the
+// Masked places.  Tokens that all rows see need no mask; a tile that holds others, the end of the
 // sequence or a bad block id gets 32 visibility bits per 32 tokens and row.  A zero weight does
 // not silence an infinite or NaN value in a matrix product, so before such a tile's second
 // product the group clears the values past the end and any non-finite element of a node's
@@ -843,6 +843,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 word0 = node_word(p, x, node, 0);
                 if (x.nodes > 64) word1 = node_word(p, x, node, 1);
             }
+            // Tokens that every row of the CTA sees, and every row of this warp: the context, and
+            // of a chain the nodes up to the first row's.  (With all of a chain's tiles masked
+            // and their values looked over, a prompt of 4096 tokens took 447 us, so 282.)
+            const bool chain = p.mask == nullptr;
+            const int open_cta = min(x.ctx + (chain ? g.rt * span + 1 : 0), x.tokens);
+            const int open = min(x.ctx + (chain ? first + quarter * 32 / p.g + 1 : 0), x.tokens);
             const int64_t unit0 =
                 (static_cast<int64_t>(g.f) * p.members + walk.member) * NQ + (NQ == 2 ? w : 0);
             for (int j = 0; j < jobs; ++j) {
@@ -855,8 +861,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t bad =
                     *(volatile uint32_t*)&bar.bad_ids[C::kOwnTiles ? w : 0]
                                                      [(tile + j / kJobs) % kMetaRing] >> (4 * half);
-                const bool special = pos0 + 64 > x.ctx || (bad & 15) != 0 || p.pre != 1.0f;
-                if (pos0 + 64 > x.ctx) {
+                const bool special = pos0 + 64 > open || (bad & 15) != 0 || p.pre != 1.0f;
+                if (pos0 + 64 > open_cta) {
                     // Values past the end become zero; so do a node's non-finite elements.
                     int sv;
                     uint32_t par;
@@ -867,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = gt + (NQ == 2 ? w * 128 : 0); k < 64 * kChunks;
                          k += NQ == 2 ? 256 : 128) {
                         const int r = k % 64, ch = k / 64;
-                        if (pos0 + r < x.ctx) continue;
+                        if (pos0 + r < open_cta) continue;
                         uint8_t* at = part + ((r >> 3) * kChunks + ch) * 1024;
                         if (pos0 + r >= x.tokens) {
                             wrote = true;
@@ -1953,7 +1959,7 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
                       : p.ways > 0 ? (plan.tasks * p.ways + 7) / 8
                                    : (unit_rows + 31) / 32;
     // What one group saw whole needs no join: where there are more units than cuts of the list, the
-    // join goes by the cuts (43 trees of 202 nodes, 2408 units and 144 cuts: 60 us by unit, 4 by
+    // join goes by the cuts (43 chains of 202 nodes, 2064 units and 144 cuts: 60 us by unit, 4 by
     // cut; 3 trees of 31 to 95 nodes, 6 units and 150 cuts: 11 and 18).
     const int64_t cuts = static_cast<int64_t>(plan.groups - 1) * plan.members;
     const bool by_cut = C::kWhole && !few && cuts < units;

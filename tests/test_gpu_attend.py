@@ -454,3 +454,22 @@ def test_rows_of_a_sequence_without_tokens_are_zero(hd, nodes):
     assert (got[0][at:at + c.nodes[1]] == 0).all()
     assert (lse[at:at + c.nodes[1]] == -math.inf).all()
     c.check((got[0], lse, None), hide=hide)
+
+
+@pytest.mark.parametrize("hd,ctx", [(64, 0), (128, 37), (192, 0), (256, 70)])
+def test_a_bad_value_in_a_long_chain_reaches_the_rows_from_its_node_on(hd, ctx):
+    n = 300
+    c = Case(hd, 8, 2, 16, [ctx, ctx + 5], [n, n], "chain", seed=70, std=0.5)
+    spots = ((3, 1, 5, math.inf), (130, 0, 60, math.nan), (131, 1, 7, -math.inf),
+             (n - 1, 0, 1, math.inf))
+    for node, head, dim, bad in spots:
+        c.v[0][ctx + node, head, dim] = bad
+    out, lse, w = c.gpu()
+    assert w.isfinite().all() and lse.isfinite().all()
+    o = out.cpu().view(2, n, 8, hd).clone()
+    assert o[1].isfinite().all()
+    for node, head, dim, bad in spots:
+        part = o[0, :, head * 4:head * 4 + 4, dim]
+        assert part[:node].isfinite().all() and not part[node:].isfinite().any()
+        part[node:] = 0
+    assert o.isfinite().all()
