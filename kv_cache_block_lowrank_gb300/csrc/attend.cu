@@ -67,6 +67,15 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kRows = 128;          // UMMA M
 constexpr int kMetaRing = 16;       // bad-id bits of the tiles in flight
+// Flags of pieces with a non-finite value.  A flag is set by any of the group's warps (with two row
+// tiles, by the other group's too) and read at the piece's end, with no barrier of its own, so a
+// slot must not be set again before every warp has read it.  Pieces count where the group has jobs.
+// A warp that is at piece n has seen its scores, which were issued after all products of the
+// group's piece n - 1, and those wait for weights from all four warps of the group: they have
+// left piece n - 2.  The other group can be one piece further behind: its queries for piece n were
+// loaded once its last scores of n - 1 were done, two of which need no weights of n - 1, but all
+// products of n - 2: its warps have left piece n - 3.
+constexpr int kFlagSlots = 3;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kCtas = 152;          // GB300's SMs; the workspace does not depend on the device
 constexpr float kLazy = 8.0f;       // the maximum may lag by 2^8 before O is rescaled
@@ -400,7 +409,7 @@ struct Barriers {
     uint64_t full[12], empty[12];
     uint64_t q_full, q_empty, s_full[4], p_full[4], o_done[4], values;
     uint32_t bad_ids[2][kMetaRing];  // [ring] per tile in flight: 16-token granules with a bad id
-    int bad_value[2][2];          // [group][segment parity]: last segment with such a value
+    int bad_value[2][kFlagSlots];    // [group][piece mod kFlagSlots]: last piece with such a value
     int abort;
     uint32_t tmem;
     Start start;
@@ -513,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar.p_full[i], 4);
             mbar_init(&bar.o_done[i], 1);
         }
-        for (int i = 0; i < 2; ++i) bar.bad_value[i][0] = bar.bad_value[i][1] = -1;
+        for (int i = 0; i < 2 * kFlagSlots; ++i) (&bar.bad_value[0][0])[i] = -1;
         mbar_init(&bar.values, 8);
         bar.abort = 0;
         fence_mbarrier_init();
@@ -819,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t o_cols = lanes + C::kOCols + w * HD;
         const int gt = quarter * 32 + lane;  // thread of the group
-        uint32_t tile = 0, segs = 0, values = 0;
+        uint32_t tile = 0, pieces = 0, values = 0;
         // bit b: parity of buffer b's next scores, of its next end of a piece
         uint32_t next = 0, ends = 0;
         bool ok = true;
@@ -910,9 +919,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (found) {
-                        const int seg = static_cast<int>(segs);
-                        *(volatile int*)&bar.bad_value[w][seg & 1] = seg;
-                        if (NQ == 2) *(volatile int*)&bar.bad_value[w ^ 1][seg & 1] = seg;
+                        const int slot = pieces % kFlagSlots;
+                        *(volatile int*)&bar.bad_value[w][slot] = static_cast<int>(pieces);
+                        if (NQ == 2)
+                            *(volatile int*)&bar.bad_value[w ^ 1][slot] = static_cast<int>(pieces);
                     }
                     if (wrote || found) fence_proxy_async_smem();
                     if (NQ == 2) {  // both groups read the tile: both wait until all of it is fit
@@ -1046,8 +1056,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after_sync();
                 }
                 const bool bad =
-                    jobs > 0 && *(volatile int*)&bar.bad_value[w][segs & 1] ==
-                                    static_cast<int>(segs);
+                    jobs > 0 && *(volatile int*)&bar.bad_value[w][pieces % kFlagSlots] ==
+                                    static_cast<int>(pieces);
                 if (C::kWhole && walk.whole(p, g)) {
                     const int64_t to = (static_cast<int64_t>(x.q0) + node) * p.nq + walk.h * p.g +
                                        row % p.g;
@@ -1081,7 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (row < live) p.part_ml[slot * p.rowcap + row] = make_float2(m, l);
                 if (row == 0) p.part_bad[slot] = bad;
             }
-            if (g.n > 0) ++segs;
+            if (jobs > 0) ++pieces;
             ends ^= jobs > 1 && kBuffers == 2 ? 3u : (jobs > 0 ? 1u : 0u);
             tile += tiles;
         }
