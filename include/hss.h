@@ -481,7 +481,7 @@ typedef struct hss_attend_args {
     const int32_t* q_offsets;   /* device, [num_seqs + 1]: sequence s owns the rows
                                    q_offsets[s] .. q_offsets[s + 1] - 1, its tree's nodes */
     int64_t total_q;            /* rows in all, q_offsets[num_seqs] */
-    int32_t max_q;              /* at least the largest tree's nodes */
+    int32_t max_q;              /* at least the largest tree's nodes; the workspace goes by it */
     int32_t mask_words;         /* 64-bit words of a row's mask (tree_mask != NULL: >= 1) */
     const uint64_t* tree_mask;  /* device, [total_q, mask_words], 8-byte aligned, or NULL */
     const int32_t* block_table; /* device, [total_blocks] physical block ids */
@@ -499,7 +499,8 @@ typedef struct hss_attend_args {
 } hss_attend_args;
 
 /* Bytes of the workspace: enough for every call with these dims and counts, or smaller ones
- * (0 if a count is negative or the dims are not valid).  Without weights it holds what the CTAs
+ * (0 if a count is negative, the dims are not valid, or the call would be refused as too large:
+ * 2^30 tiles of tokens under a row tile, or pieces of a row tile, at most).  Without weights it holds what the CTAs
  * have of the rows, about twice the outputs in fp32 and some 40 MB at most; with them also a
  * float for every 16 tokens that a row sees, per query head: 13 MB for 64 sequences of 16k tokens
  * and 32 query heads, 1.4 GB for 512 rows of 64 heads over 128k tokens. */
@@ -534,7 +535,8 @@ size_t hss_attend_tree_workspace_bytes(const hss_dims* dims, int32_t num_seqs, i
  * Up to three more launches follow the attention itself on the stream (the join of what several
  * CTAs have of a row, and the block weights); a pipeline wait that runs out raises
  * HSS_ERR_DEVICE_TIMEOUT like those of the other kernels.
- * Supported: num_q_heads / num_kv_heads <= 128; num_seqs, max_q >= 0.  Other device-side errors
+ * Supported: num_q_heads / num_kv_heads <= 128; num_seqs, max_q >= 0; HSS_ERR_INVALID_ARGUMENT if
+ * the counts are too large for hss_attend_tree_workspace_bytes.  Other device-side errors
  * (*dev_status and the library's device error word): a block id outside [0, max_blocks) hides
  * its tokens and raises HSS_ERR_OUT_OF_RANGE; so does a table too short for ctx_len + nodes (the
  * tokens past it are hidden); a negative ctx_len counts as 0; a sequence with more than max_q

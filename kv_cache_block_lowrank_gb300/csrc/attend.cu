@@ -1814,6 +1814,7 @@ struct Plan {
     int tile;
     bool few;        // few rows in all: a CTA joins one
     int tasks, ways;  // of join_columns: a unit's tasks and the warps to each, 0 for part_o by row
+    bool fits;  // slots and tiles are few enough for 32-bit positions; else nothing below is set
     int64_t slots, tiles, units;
     size_t header, starts, seq_tiles, seq_items, part_o, part_ml, part_bad, row_lse, sums, sums_m,
         bytes;
@@ -1829,7 +1830,8 @@ Plan row_plan(const hss_dims& d, int32_t max_q) {
     p.tile = d.head_dim <= 128 ? 128 : 64;
     p.nq_tiles = max_q > p.nodes_tile && d.head_dim < 256 ? 2 : 1;
     const int span = p.nq_tiles * p.nodes_tile;
-    p.row_tiles = std::max(1, (max_q + span - 1) / span);
+    // (max_q may be anything up to 2^31 - 1)
+    p.row_tiles = static_cast<int>(std::max<int64_t>(1, (int64_t{max_q} + span - 1) / span));
     p.rowcap = std::min(kRows, g * std::min(max_q, p.nodes_tile));
     return p;
 }
@@ -1884,6 +1886,18 @@ Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total
     const int span = p.nq_tiles * p.nodes_tile;
     p.members = members;
     p.groups = std::max(1, kCtas / p.members);
+    const int64_t batches = (int64_t{p.row_tiles} + p.members - 1) / p.members;
+    const int beside = p.tile == 128 ? kBeside<128> : kBeside<64>;
+    {
+        // In floating point first: the products of the largest counts pass 64 bits.
+        const double items = static_cast<double>(batches) * d.num_kv_heads * num_seqs;
+        const double slots = (items + p.groups) * p.members * 2;
+        const double tiles = static_cast<double>(batches) * d.num_kv_heads *
+                             (static_cast<double>(total_blocks) * d.block_size / p.tile +
+                              (1.0 + beside) * num_seqs);
+        p.fits = slots <= (1 << 30) && tiles <= (1 << 30);
+        if (!p.fits) return p;
+    }
     // A CTA joins a row while that leaves SMs free (a lone sequence's 32 rows of 38 pieces).
     const int64_t units = static_cast<int64_t>(p.row_tiles) * d.num_kv_heads * num_seqs;
     p.few = units * std::min(max_q, span) * g <= 2 * kCtas;
@@ -1901,11 +1915,9 @@ Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total
         for (p.ways = 1; p.ways < 8 && p.ways < pieces && cut * p.tasks * p.ways < 32 * kCtas;)
             p.ways *= 2;
     }
-    const int64_t batches = (p.row_tiles + p.members - 1) / p.members;
     const int64_t items = batches * d.num_kv_heads * num_seqs;
     p.units = items * p.members * p.nq_tiles;
     p.slots = (items + p.groups) * p.members * 2;
-    const int beside = p.tile == 128 ? kBeside<128> : kBeside<64>;
     p.tiles = batches * d.num_kv_heads *
               (total_blocks * d.block_size / p.tile + int64_t{1 + beside} * num_seqs);
     size_t at = 0;
@@ -2042,14 +2054,14 @@ size_t attend_workspace_bytes(const hss_dims& d, int32_t num_seqs, int32_t max_q
 
 hss_status launch_attend(const AttendArgs& r, cudaStream_t stream) {
     const hss_attend_args& a = *r.a;
-    const DeviceInfo* dev = current_device_info();
-    if (dev == nullptr) return HSS_ERR_CUDA;
     const hss_dims& d = a.dims;
     const bool weigh = r.weights_out != nullptr;
     const int members = members_for(row_plan(d, a.max_q), d, a.num_seqs, a.max_q, a.total_q,
                                     a.total_blocks, a.tree_mask == nullptr);
     const Plan plan = make_plan(d, a.num_seqs, a.max_q, a.total_blocks, weigh, members);
-    if (plan.tiles > (1 << 30) || plan.slots > (1 << 30)) return HSS_ERR_INVALID_ARGUMENT;
+    if (!plan.fits) return HSS_ERR_INVALID_ARGUMENT;
+    const DeviceInfo* dev = current_device_info();
+    if (dev == nullptr) return HSS_ERR_CUDA;
     auto enc = tensor_map_encoder();
     if (enc == nullptr) return HSS_ERR_CUDA;
     AttendParams p;
