@@ -498,12 +498,20 @@ typedef struct hss_attend_args {
     int32_t* dev_status;        /* device int32 or NULL */
 } hss_attend_args;
 
-/* Bytes of the workspace: enough for every call with these dims and counts, or smaller ones
- * (0 if a count is negative, the dims are not valid, or the call would be refused as too large:
- * 2^30 tiles of tokens under a row tile, or pieces of a row tile, at most).  Without weights it holds what the CTAs
- * have of the rows, about twice the outputs in fp32 and some 40 MB at most; with them also a
- * float for every 16 tokens that a row sees, per query head: 13 MB for 64 sequences of 16k tokens
- * and 32 query heads, 1.4 GB for 512 rows of 64 heads over 128k tokens. */
+/* Bytes of the workspace: enough for every call with these dims and counts, or smaller ones (0 if a
+ * count is negative, the dims are not valid, or the call would be refused as too large: 2^30 tiles
+ * of tokens under a row tile, or pieces of a row tile, at most).
+ * Without weights it holds what the CTAs have of the rows in fp32, with room for max_q rows of every
+ * sequence: max_q as whole row tiles of 128 / (num_q_heads / num_kv_heads) nodes, two by two where
+ * there are more than one and head_dim is below 256; twice that where max_q is at most one row tile
+ * or head_dim is 256; up to a third more for an odd few row tiles; and at most 42 MB besides.  With
+ * weights also five bytes for every 16 tokens that such a row may see, per query head.  64 single
+ * tokens over 16k tokens each (32 heads of 128), with weights: 13 MB; 512 rows of 64 heads of 128
+ * over 128k tokens: 39 MB, with weights 1.6 GB.
+ * It goes by max_q and not by the rows there are: a chunk of 2048 rows among 63 single tokens, all
+ * over 4k tokens (64 heads of 128), takes 4.8 GB, with weights 17.4 GB, where a call of the chunk
+ * alone takes 95 MB (382 MB) and one of the single tokens 5.5 MB (11 MB).  Call such sequences
+ * apart. */
 size_t hss_attend_tree_workspace_bytes(const hss_dims* dims, int32_t num_seqs, int32_t max_q,
                                        int64_t total_blocks, int32_t with_weights);
 

@@ -1838,6 +1838,13 @@ Plan row_plan(const hss_dims& d, int32_t max_q) {
 
 constexpr int kMostMembers = 19;  // kCtas / 8
 
+// Only numbers of members that leave no batch emptier than it must be: the workspace has room for
+// every member of every batch (16 row tiles by 15 members would be two batches, 30 row tiles).
+bool members_allowed(int row_tiles, int r) {
+    const int batches = (row_tiles - 1) / r + 1;
+    return r == (row_tiles - 1) / batches + 1;
+}
+
 // Members of a group, row tiles in step: many read K and V less often, few leave fewer CTAs
 // waiting (in a last batch that is not full, in the upper rows of a chain, in groups that do not
 // fill the GPU).  The estimate adds up the tiles that a sequence's batches walk, at 1500 cycles for
@@ -1860,6 +1867,7 @@ int members_for(const Plan& p, const hss_dims& d, int32_t num_seqs, int32_t max_
     double best = INFINITY;
     int members = 1;
     for (int r = 1; r <= std::min(p.row_tiles, kMostMembers); ++r) {
+        if (!members_allowed(p.row_tiles, r)) continue;
         double tiles = 0.0;
         for (int i = 0; i < 4; ++i) {
             const double n = max_q - (max_q - fewest) * i / 3.0;
@@ -2047,8 +2055,11 @@ size_t attend_workspace_bytes(const hss_dims& d, int32_t num_seqs, int32_t max_q
                               int64_t total_blocks, bool with_weights) {
     // (the members depend on more than the sizes given here)
     size_t most = 0;
-    for (int r = 1; r <= std::min(row_plan(d, max_q).row_tiles, kMostMembers); ++r)
-        most = std::max(most, make_plan(d, num_seqs, max_q, total_blocks, with_weights, r).bytes);
+    const int row_tiles = row_plan(d, max_q).row_tiles;
+    for (int r = 1; r <= std::min(row_tiles, kMostMembers); ++r)
+        if (members_allowed(row_tiles, r))
+            most = std::max(most,
+                            make_plan(d, num_seqs, max_q, total_blocks, with_weights, r).bytes);
     return most;
 }
 

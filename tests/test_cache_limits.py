@@ -38,3 +38,42 @@ def test_counts_whose_products_pass_64_bits_are_refused():
     assert size_of(d, 1, 1, 2 ** 62, True) == 0
     assert status_of(attend, d, S=INT_MAX, total_q=INT_MAX, max_q=INT_MAX, total=INT_MAX,
                      wsb=1 << 62) == hss.HSS_ERR_INVALID_ARGUMENT
+
+
+HEADS = dict(num_q_heads=64, num_kv_heads=8, head_dim=128, block_size=16)
+
+
+@pytest.mark.parametrize("seqs,max_q,blocks,heads,plain,weighted", [
+    # what hss.h says, in MB
+    (64, 1, 64 * 1024 + 64, {"num_q_heads": 32}, None, 13),
+    (1, 512, 8192 + 32, {}, 39, 1560),
+    (64, 2048, 64 * 257 + 128, {}, 4790, 17440),
+    (1, 2048, 257 + 127, {}, 95, 382),
+    (63, 1, 63 * 257, {}, 5.5, 11)])
+def test_workspace_bytes_as_documented(seqs, max_q, blocks, heads, plain, weighted):
+    d = dims(**(HEADS | heads))
+    for want, weights in ((plain, False), (weighted, True)):
+        if want is not None:
+            assert size_of(d, seqs, max_q, blocks, weights) / 1e6 == pytest.approx(want, rel=0.04)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 192, 256])
+@pytest.mark.parametrize("g", [1, 3, 8, 16, 42, 65, 128])
+@pytest.mark.parametrize("nkv,seqs", [(1, 1), (8, 1), (8, 64), (2, 300)])
+def test_workspace_within_its_bound(hd, g, nkv, seqs):
+    d = dims(head_dim=hd, num_q_heads=g * nkv, num_kv_heads=nkv)
+    tile = 128 // g
+    for max_q in list(range(1, 300)) + [333, 511, 512, 513, 1000, 2047, 2048, 2049, 4096, 10000]:
+        one = max_q <= tile
+        step = 1 if one else (tile if hd == 256 else 2 * tile)
+        nodes = (max_q + step - 1) // step * step
+        # a row's O, and its maximum and sum; a flag of a piece and a start of a range besides
+        rows = seqs * nodes * g * nkv * (4 * hd + 8)
+        bound = rows * (2 if one or hd == 256 else 1) * 4 / 3 + 42e6 + 40 * seqs * nodes * nkv
+        size = size_of(d, seqs, max_q, seqs * 600, False)
+        assert 0 < size <= bound, (max_q, size, bound)
+        # with weights, five bytes more for 16 tokens of a row (the tokens as whole tiles, with
+        # what the list holds besides: three tiles of 128 or four of 64 a sequence), and its lse
+        tokens = seqs * (600 * 16 + 400)
+        more = nodes * g * nkv * (tokens * 5 / 16 + 4 * seqs) * 4 / 3 + 4096
+        assert size_of(d, seqs, max_q, seqs * 600, True) <= bound + more, max_q
