@@ -1814,8 +1814,14 @@ struct Plan {
     int tile;
     bool few;        // few rows in all: a CTA joins one
     int tasks, ways;  // of join_columns: a unit's tasks and the warps to each, 0 for part_o by row
-    bool fits;  // slots and tiles are few enough for 32-bit positions; else nothing below is set
+    bool fits;  // few enough slots and tiles for 32-bit positions, and CTAs for a grid
     int64_t slots, tiles, units;
+    // The grids behind the attention itself.
+    int parts;                // CTAs of a unit that is joined
+    int join_tiles;           // row_tiles, or 0: the join goes by the cuts of the list
+    int shares, entry_ways;   // CTAs to a sequence's entries, warps to one
+    int grain_shares;         // CTAs to a unit's jobs
+    int64_t join_ctas, finish_ctas, grain_ctas;  // finish_ctas 0: join and weights by themselves
     size_t header, starts, seq_tiles, seq_items, part_o, part_ml, part_bad, row_lse, sums, sums_m,
         bytes;
 };
@@ -1887,6 +1893,47 @@ int members_for(const Plan& p, const hss_dims& d, int32_t num_seqs, int32_t max_
     return members;
 }
 
+// The grids of the join and of the weights, once the rows' part of the plan is there.
+void plan_grids(Plan& p, const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total_blocks,
+                bool with_weights) {
+    const int g = d.num_q_heads / d.num_kv_heads, grains = d.block_size / 16;
+    const bool whole = p.nq_tiles == 2 || d.head_dim == 256;  // as Cfg::kWhole
+    const int unit_rows = std::min(max_q, p.nq_tiles * p.nodes_tile) * g;
+    const int64_t units = static_cast<int64_t>(p.row_tiles) * d.num_kv_heads * num_seqs;
+    p.parts = p.few ? unit_rows : p.ways > 0 ? (p.tasks * p.ways + 7) / 8 : (unit_rows + 31) / 32;
+    // What one group saw whole needs no join: where there are more units than cuts of the list, the
+    // join goes by the cuts (43 chains of 202 nodes, 2064 units and 144 cuts: 60 us by unit, 4 by
+    // cut; 3 trees of 31 to 95 nodes, 6 units and 150 cuts: 11 and 18).
+    const int64_t cuts = static_cast<int64_t>(p.groups - 1) * p.members;
+    const bool by_cut = whole && !p.few && cuts < units;
+    p.join_ctas = (by_cut ? cuts : units) * p.parts;
+    p.join_tiles = by_cut ? 0 : p.row_tiles;
+    // Join and weights in one launch while a lane has few (row, granule) pairs of an entry to look
+    // at in turn (36 sequences of 23 nodes, 14 heads and blocks of 32 tokens, 22 pairs, took 80 us
+    // this way and 43 us through the granules' totals).
+    const int64_t seq_rows = static_cast<int64_t>(max_q) * d.num_q_heads;
+    const bool few_each = p.nq_tiles == 1 && p.row_tiles == 1 && with_weights &&
+                          seq_rows <= kFewRows && (seq_rows + 31) / 32 * grains <= 8;
+    // Warps to an entry: one for every 32 of its (granule, row tile, head) sums.  (8 trees of 81 to
+    // 245 nodes of 128 heads: 32 us with one warp an entry, 9 with eight.)
+    const int64_t each = static_cast<int64_t>(grains) * d.num_kv_heads * p.row_tiles * p.nq_tiles;
+    p.entry_ways = 1;
+    while (p.entry_ways < 8 && p.entry_ways * 32 < each) p.entry_ways *= 2;
+    // CTAs to a sequence's entries: an even share of all entries in one pass, if the sequences
+    // are alike, within what the GPU holds at once.
+    const int64_t seqs = std::max(num_seqs, 1);
+    const int64_t per_cta = few_each ? 8 * kEntries : 8 / p.entry_ways;
+    const int64_t even = (total_blocks / seqs + per_cta) / per_cta;
+    p.shares = static_cast<int>(std::min(even, std::max<int64_t>(1, 8 * kCtas / seqs)));
+    p.finish_ctas = few_each ? p.join_ctas + static_cast<int64_t>(num_seqs) * p.shares : 0;
+    // Shares of a unit's jobs: two passes over all warps that the GPU holds.
+    const int64_t grain_units = units * p.nq_tiles;
+    const int64_t jobs = total_blocks * d.block_size / 64 / seqs + 1;
+    p.grain_shares = static_cast<int>(std::max<int64_t>(
+        1, std::min((jobs + 7) / 8, 8 * kCtas / std::max<int64_t>(grain_units, 1))));
+    p.grain_ctas = with_weights ? grain_units * p.grain_shares : 0;
+}
+
 Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total_blocks,
                bool with_weights, int members) {
     Plan p = row_plan(d, max_q);
@@ -1949,6 +1996,10 @@ Plan make_plan(const hss_dims& d, int32_t num_seqs, int32_t max_q, int64_t total
         p.sums = take(lanes * (p.tile / 16) * 4);
     }
     p.bytes = at;
+    plan_grids(p, d, num_seqs, max_q, total_blocks, with_weights);
+    p.fits = p.join_ctas <= 0x7FFFFFFF && p.finish_ctas <= 0x7FFFFFFF &&
+             p.grain_ctas <= 0x7FFFFFFF;
+    if (!p.fits) p.bytes = 0;
     return p;
 }
 
@@ -1982,69 +2033,30 @@ hss_status launch_all(const AttendParams& p, const Plan& plan, const CUtensorMap
     if (launch_pdl(attend_kernel<HD, NQ>, dim3(plan.groups * plan.members), dim3(kThreads),
                    C::kSmemBytes, stream, mq, mk, mv, p) != cudaSuccess)
         return HSS_ERR_CUDA;
-    const int unit_rows = std::min(p.max_q, NQ * plan.nodes_tile) * p.g;
-    const int64_t units = static_cast<int64_t>(plan.row_tiles) * p.nkv * p.num_seqs;
-    const bool few = plan.few;
-    const int parts = few          ? unit_rows
-                      : p.ways > 0 ? (plan.tasks * p.ways + 7) / 8
-                                   : (unit_rows + 31) / 32;
-    // What one group saw whole needs no join: where there are more units than cuts of the list, the
-    // join goes by the cuts (43 chains of 202 nodes, 2064 units and 144 cuts: 60 us by unit, 4 by
-    // cut; 3 trees of 31 to 95 nodes, 6 units and 150 cuts: 11 and 18).
-    const int64_t cuts = static_cast<int64_t>(plan.groups - 1) * plan.members;
-    const bool by_cut = C::kWhole && !few && cuts < units;
-    const int64_t join_ctas = (by_cut ? cuts : units) * parts;
-    const int row_tiles = by_cut ? 0 : plan.row_tiles;  // (0: by cut)
-    // CTAs to a sequence's entries: an even share of all entries in one pass, if the sequences
-    // are alike, within what the GPU holds at once.
-    // Join and weights in one launch while a lane has few (row, granule) pairs of an entry to look
-    // at in turn (36 sequences of 23 nodes, 14 heads and blocks of 32 tokens, 22 pairs, took 80 us
-    // this way and 43 us through the granules' totals).
-    const int64_t seq_rows = static_cast<int64_t>(p.max_q) * p.nq;
-    const bool few_each = NQ == 1 && plan.row_tiles == 1 && p.weights_out != nullptr &&
-                          seq_rows <= kFewRows && (seq_rows + 31) / 32 * (p.bs / 16) <= 8;
-    // Warps to an entry: one for every 32 of its (granule, row tile, head) sums.  (8 trees of 81 to
-    // 245 nodes of 128 heads: 32 us with one warp an entry, 9 with eight.)
-    const int64_t each = static_cast<int64_t>(p.bs / 16) * p.nkv * plan.row_tiles * NQ;
-    int ways = 1;
-    while (ways < 8 && ways * 32 < each) ways *= 2;
-    const int64_t per_cta = few_each ? 8 * kEntries : 8 / ways;
-    const int64_t even = (p.total_blocks / std::max(p.num_seqs, 1) + per_cta) / per_cta;
-    const int64_t most = std::max<int64_t>(1, 8 * kCtas / std::max(p.num_seqs, 1));
-    const int shares = static_cast<int>(std::min(even, most));
     if constexpr (NQ == 1) {
-        if (rows && few_each) {
-            const int64_t grid = join_ctas + static_cast<int64_t>(p.num_seqs) * shares;
-            if (grid > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
-            auto finish = few ? finish_kernel<HD, 8> : finish_kernel<HD, 1>;
-            if (launch_pdl(finish, dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, p,
-                           row_tiles, parts, static_cast<int>(join_ctas), shares) != cudaSuccess)
+        if (rows && plan.finish_ctas > 0) {
+            auto finish = plan.few ? finish_kernel<HD, 8> : finish_kernel<HD, 1>;
+            if (launch_pdl(finish, dim3(static_cast<unsigned>(plan.finish_ctas)), dim3(256), 0,
+                           stream, p, plan.join_tiles, plan.parts,
+                           static_cast<int>(plan.join_ctas), plan.shares) != cudaSuccess)
                 return HSS_ERR_CUDA;
             return HSS_OK;
         }
     }
-    if (rows && join_ctas > 0) {
-        if (join_ctas > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
-        auto join = few ? join_kernel<HD, NQ, 8> : join_kernel<HD, NQ, 1>;
-        if (launch_pdl(join, dim3(static_cast<unsigned>(join_ctas)), dim3(256), 0, stream, p,
-                       row_tiles, parts) != cudaSuccess)
+    if (rows && plan.join_ctas > 0) {
+        auto join = plan.few ? join_kernel<HD, NQ, 8> : join_kernel<HD, NQ, 1>;
+        if (launch_pdl(join, dim3(static_cast<unsigned>(plan.join_ctas)), dim3(256), 0, stream, p,
+                       plan.join_tiles, plan.parts) != cudaSuccess)
             return HSS_ERR_CUDA;
     }
-    if (rows && p.weights_out != nullptr) {
-        // shares of a unit's jobs: two passes over all warps that the GPU holds
-        const int64_t grain_units = units * NQ;
-        const int64_t jobs = p.total_blocks * p.bs / 64 / std::max(p.num_seqs, 1) + 1;
-        const int64_t split = std::max<int64_t>(
-            1, std::min((jobs + 7) / 8, 8 * kCtas / std::max<int64_t>(grain_units, 1)));
-        if (grain_units * split > 0x7FFFFFFF) return HSS_ERR_INVALID_ARGUMENT;
-        if (launch_pdl(grains_kernel<HD, NQ>, dim3(static_cast<unsigned>(grain_units * split)),
-                       dim3(256), 0, stream, p, plan.row_tiles, static_cast<int>(split)) !=
-            cudaSuccess)
-            return HSS_ERR_CUDA;
-    }
-    if (p.weights_out != nullptr &&
-        launch_pdl(weights_kernel<HD, NQ>, dim3(static_cast<unsigned>(p.num_seqs * shares)),
-                   dim3(256), 0, stream, p, shares, ways) != cudaSuccess)
+    if (p.weights_out == nullptr) return HSS_OK;
+    if (rows && launch_pdl(grains_kernel<HD, NQ>, dim3(static_cast<unsigned>(plan.grain_ctas)),
+                           dim3(256), 0, stream, p, plan.row_tiles, plan.grain_shares) !=
+                    cudaSuccess)
+        return HSS_ERR_CUDA;
+    // (without rows this is all, with the shares of a call that has some)
+    if (launch_pdl(weights_kernel<HD, NQ>, dim3(static_cast<unsigned>(p.num_seqs * plan.shares)),
+                   dim3(256), 0, stream, p, plan.shares, plan.entry_ways) != cudaSuccess)
         return HSS_ERR_CUDA;
     return HSS_OK;
 }

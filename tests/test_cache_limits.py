@@ -77,3 +77,13 @@ def test_workspace_within_its_bound(hd, g, nkv, seqs):
         tokens = seqs * (600 * 16 + 400)
         more = nodes * g * nkv * (tokens * 5 / 16 + 4 * seqs) * 4 / 3 + 4096
         assert size_of(d, seqs, max_q, seqs * 600, True) <= bound + more, max_q
+
+
+def test_a_grid_that_is_too_large_is_refused_before_any_launch():
+    # 2^29 sequences of one row of 128 heads: the attention's own grid is 152 CTAs, the join's and
+    # the weights' together more than 2^31
+    d = dims(num_q_heads=128, num_kv_heads=1)
+    seqs = 2 ** 29 - 200
+    assert size_of(d, seqs, 1, 10, True) == 0 < size_of(d, seqs, 1, 10, False)
+    assert status_of(attend, d, S=seqs, total_q=1, max_q=1, total=10, wsb=1 << 62) == \
+        hss.HSS_ERR_INVALID_ARGUMENT
