@@ -435,6 +435,7 @@ __device__ __forceinline__ void write_whole(const AttendParams& p, const SeqInfo
 #pragma unroll 1
     for (int k = 0; k < HD; k += 32) {
         uint32_t o[32], u[4][4];
+        __syncwarp();  // (the rows went out lane by lane, the last time)
         tmem_ld_32x32b_x32(o_cols + k, o);
         tmem_ld_wait_for(o);
         if (bad && live) {
@@ -925,8 +926,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *(volatile int*)&bar.bad_value[w ^ 1][slot] = static_cast<int>(pieces);
                     }
                     if (wrote || found) fence_proxy_async_smem();
+                    __syncwarp();  // what reads tensor memory wants the warp as one
                     if (NQ == 2) {  // both groups read the tile: both wait until all of it is fit
-                        __syncwarp();
                         if (lane == 0) mbar_arrive(&bar.values);
                         if (!(ok = wait(&bar.values, values & 1))) break;
                         ++values;
@@ -1071,6 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 2
                     for (int k = 0; k < HD; k += 32) {
                         uint32_t o[32];
+                        __syncwarp();
                         tmem_ld_32x32b_x32(o_cols + k, o);
                         tmem_ld_wait_for(o);
                         if (row < live && p.ways > 0) {
