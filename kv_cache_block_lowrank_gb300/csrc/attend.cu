@@ -156,6 +156,7 @@ struct AttendParams {
 
 struct SeqInfo {
     int q0, nodes, ctx, tokens, e0, end;
+    bool cut;  // the table is too short for ctx_len + nodes
 };
 
 __device__ __forceinline__ SeqInfo load_seq(const AttendParams& p, int s) {
@@ -169,6 +170,10 @@ __device__ __forceinline__ SeqInfo load_seq(const AttendParams& p, int s) {
     const int64_t room = static_cast<int64_t>(x.end - x.e0) * p.bs;
     const int64_t want = static_cast<int64_t>(x.ctx) + x.nodes;
     x.tokens = static_cast<int>(min(min(room, want), static_cast<int64_t>(0x7FFFFF00)));
+    // What the table has no room for is hidden, so that a context past its end is no longer than
+    // the tokens (and sums of its length and a node's number stay in 32 bits).
+    x.cut = x.tokens < want;
+    x.ctx = min(x.ctx, max(x.tokens, 0));
     return x;
 }
 
@@ -550,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (blockIdx.x == 0) {
                 if (__ldg(p.q_offsets + s + 1) - x.q0 > p.max_q)
                     raise_error(p.dev_status, p.lib_error, HSS_ERR_INVALID_ARGUMENT);
-                if (x.tokens < static_cast<int64_t>(x.ctx) + x.nodes)
+                if (x.cut)
                     raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
             }
         }

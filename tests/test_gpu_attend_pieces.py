@@ -6,6 +6,8 @@ import pytest
 import torch
 from test_gpu_attend import DEV, Case, built  # noqa: F401 (the fixture builds the library)
 
+import kv_cache_block_lowrank_gb300 as hss
+
 pytestmark = pytest.mark.gpu
 
 
@@ -50,3 +52,44 @@ def test_a_bad_value_stays_with_its_piece(hd, kind, nq, nkv, pattern, n):
     assert not got[0][expected].isfinite().any()
     assert torch.equal(bits(got[0])[~expected], bits(clean[0])[~expected])
     assert torch.equal(got[1], clean[1]) and torch.equal(got[2], clean[2])
+
+
+@pytest.mark.parametrize("hd,nodes", [(64, [2, 90, 1]), (128, [3, 5, 0]), (192, [40, 2, 1]),
+                                      (256, [3, 20, 1])])
+@pytest.mark.parametrize("kind", ["chain", "tree"])
+@pytest.mark.parametrize("far", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 65, 2 ** 20])
+def test_a_context_far_past_the_table(hd, nodes, kind, far):
+    # every token of the table counts as context, a non-finite one too, and no node is seen
+    c = Case(hd, 8, 2, 16, [93, 70, 128], nodes, kind, seed=90 + hd, std=0.5, fill=0.0)
+    keep = [b * 16 for b in c.blocks]
+    c.v[0][40, 1, 5] = math.inf
+    c.v[1][69, 0, 60] = math.nan  # (the last whole tile of the table, which is looked over)
+    ctx = c.ctx
+    c.ctx = [far, far - 1, far]
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse, w = c.gpu(status=st)
+    assert st.item() == hss.HSS_ERR_OUT_OF_RANGE
+    hss.hss_read_device_error()
+    # the same as chains whose nodes no row sees, over contexts as long as the table
+    pad = lambda x, n: torch.cat([x, torch.zeros(n - x.shape[0], *x.shape[1:]).bfloat16()])
+    d = Case(hd, 8, 2, 16, keep, nodes, "tree", seed=1)
+    d.q, d.w_in, d.fill = c.q, c.w_in.new_zeros(d.total_blocks), c.fill
+    at = 0
+    for s, n in enumerate(c.blocks):
+        d.w_in[sum(d.blocks[:s]):sum(d.blocks[:s]) + n] = c.w_in[at:at + n]
+        at += n
+        d.k[s], d.v[s] = pad(c.k[s], keep[s] + nodes[s]), pad(c.v[s], keep[s] + nodes[s])
+        d.sees[s] = torch.zeros(nodes[s], nodes[s], dtype=torch.bool)
+    d.mask = torch.zeros(d.total_q, d.words, dtype=torch.int64)
+    want = d.gpu()
+    assert torch.equal(out.isfinite(), want[0].isfinite())
+    assert not out[:nodes[0], 4:, 5].isfinite().any()
+    assert not out[nodes[0]:nodes[0] + nodes[1], :4, 60].isfinite().any()
+    some = out.isfinite()
+    assert ((out.float() - want[0].float())[some].abs() <= 2.0 ** -6).all()
+    assert torch.allclose(lse, want[1], rtol=1e-5, atol=1e-5)
+    at = 0
+    for s, n in enumerate(c.blocks):
+        b = sum(d.blocks[:s])
+        assert torch.allclose(w[at:at + n], want[2][b:b + n], rtol=1e-4, atol=1e-5)
+        at += n
