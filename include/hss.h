@@ -429,7 +429,7 @@ typedef struct hss_rope {
 
 /* The table turns[rot_dim / 2] of a rope, computed on the host in double (a host array; the
  * caller copies it to the device once).  HSS_ERR_INVALID_ARGUMENT for values outside the ranges
- * above or not finite. */
+ * above or not finite, a stretched base or a high - low past the range of a double included. */
 hss_status hss_rope_table(const hss_rope* rope, uint64_t* turns);
 
 /* What the layers of one step share in hss_rope_tokens. */

@@ -38,11 +38,13 @@ hss_status hss_rope_table(const hss_rope* rope, uint64_t* turns) {
         case HSS_ROPE_SCALE_BASE:
             if (rot == 2) return HSS_ERR_INVALID_ARGUMENT;
             base *= std::pow(rope->factor, rot / (rot - 2.0));
+            // (a base past the range of a double would leave pairs unturned)
+            if (!(base > 0) || !std::isfinite(base)) return HSS_ERR_INVALID_ARGUMENT;
             break;
         case HSS_ROPE_SCALE_RAMP:
             if (!(rope->original_ctx > 0) || !std::isfinite(rope->original_ctx) ||
                 !std::isfinite(rope->low) || !std::isfinite(rope->high) ||
-                !(rope->low < rope->high))
+                !(rope->low < rope->high) || !std::isfinite(rope->high - rope->low))
                 return HSS_ERR_INVALID_ARGUMENT;
             break;
         default: return HSS_ERR_INVALID_ARGUMENT;

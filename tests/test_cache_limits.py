@@ -1,5 +1,8 @@
 """The paged-cache operators' arguments at their limits, on the host: sizes that pass 32 bits, and
 refusals that must come before anything is enqueued."""
+import math
+
+import numpy as np
 import pytest
 from test_cache_abi import FAKE, attend, dims, lib, status_of  # noqa: F401 (lib builds)
 
@@ -87,3 +90,22 @@ def test_a_grid_that_is_too_large_is_refused_before_any_launch():
     assert size_of(d, seqs, 1, 10, True) == 0 < size_of(d, seqs, 1, 10, False)
     assert status_of(attend, d, S=seqs, total_q=1, max_q=1, total=10, wsb=1 << 62) == \
         hss.HSS_ERR_INVALID_ARGUMENT
+
+
+@pytest.mark.parametrize("rope", [
+    (4, hss.HSS_ROPE_SCALE_BASE, 1e4, 1e155, 0, 0, 0),    # base 1e314
+    (128, hss.HSS_ROPE_SCALE_BASE, 1e300, 1e9, 0, 0, 0),
+    (4, hss.HSS_ROPE_SCALE_BASE, 1e-300, 1e-20, 0, 0, 0),  # base 0
+    (64, hss.HSS_ROPE_SCALE_RAMP, 1e4, 4.0, 8192, -1e308, 1e308)])
+def test_rope_table_refuses_what_passes_a_double(rope):
+    out = np.zeros(128, dtype=np.uint64)
+    assert status_of(hss.hss_rope_table, hss.hss_rope(*rope), out.ctypes.data) == \
+        hss.HSS_ERR_INVALID_ARGUMENT
+
+
+def test_rope_table_of_a_base_near_the_end_of_a_double():
+    out = np.zeros(2, dtype=np.uint64)
+    hss.hss_rope_table(hss.hss_rope(4, hss.HSS_ROPE_SCALE_BASE, 1e4, 1e150, 0, 0, 0),
+                       out.ctypes.data)
+    # base 1e304, the second frequency 1e-152: less than half of a 2^-64th of a turn
+    assert out[0] == pytest.approx(2 ** 64 / (2 * math.pi), rel=1e-15) and out[1] == 0
