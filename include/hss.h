@@ -136,7 +136,8 @@ hss_status hss_project_kv_blocks(const hss_dims* dims, const uint16_t* P, const 
  *   slots    device, [num_tokens] int64, 8-byte aligned.  A negative slot marks a padding
  *            token: nothing is written for it.  A slot >= max_blocks * block_size is skipped
  *            and raises HSS_ERR_OUT_OF_RANGE in *dev_status (if not NULL) and the library's
- *            device error word.  If two tokens name one slot, either may win.
+ *            device error word.  If two tokens name one slot, each 16 bytes of
+ *            its rows are one token's or the other's: name it once.
  *   K_cache  device, [max_blocks, block_size, num_kv_heads, head_dim] bf16, 16-byte aligned:
  *            this layer's paged key cache (each block in the page's k_block layout), or NULL
  *            to write A_g only
@@ -468,8 +469,8 @@ typedef struct hss_rope_args {
  *             aligned: this layer's caches, or NULL
  * A negative slot marks padding (the cache is left alone, Q_out and K_out are still written); a
  * slot >= max_blocks * block_size is skipped and raises HSS_ERR_OUT_OF_RANGE in *dev_status and
- * the library's device error word.  If two tokens name one slot, either may win.  No output may
- * overlap an input.
+ * the library's device error word.  If two tokens name one slot, each 16 bytes of its rows are one
+ * token's or the other's: name it once.  No output may overlap an input.
  */
 hss_status hss_rope_tokens(const hss_rope_args* args, const uint16_t* Q, const uint16_t* K,
                            const uint16_t* V, uint16_t* Q_out, uint16_t* K_out,
