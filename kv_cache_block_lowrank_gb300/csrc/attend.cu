@@ -74,8 +74,9 @@ constexpr int kMetaRing = 16;       // bad-id bits of the tiles in flight
 // group's piece n - 1, and those wait for weights from all four warps of the group: they have
 // left piece n - 2.  The other group can be one piece further behind: its queries for piece n were
 // loaded once its last scores of n - 1 were done, two of which need no weights of n - 1, but all
-// products of n - 2: its warps have left piece n - 3.
-constexpr int kFlagSlots = 3;
+// products of n - 2: its warps have left piece n - 3.  Three slots would do; four count by a mask
+// (with three, 512 rows over 16384 tokens 211 us, so 209).
+constexpr int kFlagSlots = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kCtas = 152;          // GB300's SMs; the workspace does not depend on the device
 constexpr float kLazy = 8.0f;       // the maximum may lag by 2^8 before O is rescaled
@@ -925,10 +926,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (found) {
-                        const int slot = pieces % kFlagSlots;
-                        *(volatile int*)&bar.bad_value[w][slot] = static_cast<int>(pieces);
+                        const int piece = static_cast<int>(pieces), slot = piece & (kFlagSlots - 1);
+                        *(volatile int*)&bar.bad_value[w][slot] = piece;
                         if (NQ == 2)
-                            *(volatile int*)&bar.bad_value[w ^ 1][slot] = static_cast<int>(pieces);
+                            *(volatile int*)&bar.bad_value[w ^ 1][slot] = piece;
                     }
                     if (wrote || found) fence_proxy_async_smem();
                     __syncwarp();  // what reads tensor memory wants the warp as one
@@ -1062,7 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after_sync();
                 }
                 const bool bad =
-                    jobs > 0 && *(volatile int*)&bar.bad_value[w][pieces % kFlagSlots] ==
+                    jobs > 0 && *(volatile int*)&bar.bad_value[w][pieces & (kFlagSlots - 1)] ==
                                     static_cast<int>(pieces);
                 if (C::kWhole && walk.whole(p, g)) {
                     const int64_t to = (static_cast<int64_t>(x.q0) + node) * p.nq + walk.h * p.g +
@@ -1098,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (row < live) p.part_ml[slot * p.rowcap + row] = make_float2(m, l);
                 if (row == 0) p.part_bad[slot] = bad;
             }
-            if (jobs > 0) ++pieces;
+            if (C::kOwnTiles ? jobs > 0 : g.n > 0) ++pieces;
             ends ^= jobs > 1 && kBuffers == 2 ? 3u : (jobs > 0 ? 1u : 0u);
             tile += tiles;
         }
