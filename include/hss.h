@@ -403,10 +403,11 @@ hss_status hss_layer_step_static(const hss_dims* dims, const uint16_t* P, const 
  * pairs, pair i of a token at position pos by the angle
  *     a(pos, i) = 2 pi frac(pos * turns[i] / 2^64),
  * where turns[i] is the pair's frequency as a 64-bit fixed-point fraction of a turn per
- * position.  The product of two whole numbers modulo 2^64 is exact, so an angle is as good at
- * position 2^40 as at 1 (a 32-bit frequency times a position of 131072 is off by up to 0.008
- * radians), and a negative position turns back by the same angle (the transposed rotation,
- * which the gradient of a rotated row needs).
+ * position.  The product of two whole numbers modulo 2^64 is exact, so an angle is as good as its
+ * frequency, which hss_rope_table gives within a few parts in 2^53: at position 2^27 it is off by
+ * less than the 1e-7 radians of its rounding to fp32, at 2^40 by up to 1e-3 (a 32-bit frequency
+ * times a position of 131072 is off by up to 0.008 radians).  A negative position turns back by the
+ * same angle (the transposed rotation, which the gradient of a rotated row needs).
  */
 #define HSS_ROPE_HALF 0        /* pair i = elements (i, i + rot_dim / 2) */
 #define HSS_ROPE_INTERLEAVED 1 /* pair i = elements (2 i, 2 i + 1) */
@@ -540,7 +541,9 @@ size_t hss_attend_tree_workspace_bytes(const hss_dims* dims, int32_t num_seqs, i
  *   weights_out  device, [total_blocks] f32, or NULL (weights_in is then not read); it may be
  *                weights_in
  * Scores, softmax statistics and sums are fp32; the weights exp(s - m) enter the product with V
- * rounded to bf16, the statistics and block weights take them unrounded.
+ * rounded to bf16, the statistics and block weights take them unrounded.  That rounding moves an
+ * element of out by at most 2^-9 sum_p exp(s - lse) |v_p|, beside the 2^-9 |out| of its own rounding
+ * to bf16; of the outputs' norm the two come to 0.0023 together, where the second alone is 0.0017.
  * Up to three more launches follow the attention itself on the stream (the join of what several
  * CTAs have of a row, and the block weights); a pipeline wait that runs out raises
  * HSS_ERR_DEVICE_TIMEOUT like those of the other kernels.

@@ -1017,7 +1017,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 c2 = make_float2(p.c, p.c), b2 = make_float2(base, base);
                     // The weights, packed to bf16, and their sums over 16 tokens (which stay in
                     // registers until the end: a branch in between would keep the exponentials
-                    // of different granules from overlapping).
+                    // of different granules from overlapping).  bf16, because both operands of
+                    // a product have one type and V comes as it lies in the cache: an output is
+                    // off by up to 2^-9 sum p |v| more for it.  What the rounding leaves, as a
+                    // second product, would take that away for half as much tensor time again,
+                    // where products and exponentials are what bounds many rows.  The sums take
+                    // the weights before the rounding: lse and block weights are theirs.
                     float grain[4];
                     uint32_t packed[32];
 #pragma unroll

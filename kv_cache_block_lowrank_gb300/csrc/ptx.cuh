@@ -226,9 +226,8 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 
 // umma_bf16 for a whole, converged warp, whose leader alone issues it: then the operands can stay
-// in uniform registers, where the instruction takes them from.  Descriptors as low words; their
-// high words come once, as HI (both operands' alike) or A in tensor memory (lane = row of A, each
-// 32-bit column two consecutive bf16 elements along K).
+// in uniform registers, where the instruction takes them from.  A descriptor comes as its two words,
+// of which the higher one stays the same along an operand.
 __device__ __forceinline__ void umma_bf16_warp(uint32_t leader, uint32_t d_tmem, uint32_t a_lo,
                                                uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
                                                uint32_t idesc, uint32_t accumulate) {
@@ -243,6 +242,8 @@ __device__ __forceinline__ void umma_bf16_warp(uint32_t leader, uint32_t d_tmem,
         : "memory");
 }
 
+// The same with A in tensor memory: lane = row of A, each 32-bit column two consecutive bf16 elements
+// along K.
 __device__ __forceinline__ void umma_bf16_ts_warp(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
                                                   uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                                   uint32_t accumulate) {
