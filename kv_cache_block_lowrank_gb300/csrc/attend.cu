@@ -35,13 +35,13 @@
 // float atomics: the same call gives the same bits.
 //
 // What bounds it, and what it reaches on GB300 (HBM 6.79 TB/s and 1906 TFLOP/s bf16 measured):
-// few rows, the bytes of K and V: 64 sequences of 1k to 16k tokens, 32 query heads on 8 of 128, 372
-// us with weights and join, 6.1 TB/s; one sequence of 32k tokens 38 us, of which 20 are its bytes
+// few rows, the bytes of K and V: 64 sequences of 1k to 16k tokens, 32 query heads on 8 of 128, 380
+// us with weights and join, 6.0 TB/s; one sequence of 32k tokens 38 us, of which 20 are its bytes
 // and the rest the start (sequence lengths, block ids and the first tiles, one way through memory
 // after another, 7 us), the last tiles and the join (8 us).  Many rows, the products and the
 // exponentials between them, both near 1400 cycles for a job of 2 x 128 rows by 64 tokens: 512
-// rows of 64 heads over 131072 tokens 1.34 ms alone (1.6 PFLOP/s), 1.48 ms under the power cap of
-// a long run.  Many short items, what each costs besides its tiles (4 to 5 us): a prompt of 4096
+// rows of 64 heads over 131072 tokens 1.36 ms in the first calls after a pause (1.6 PFLOP/s), 1.47
+// to 1.49 ms under the power cap of a long run.  Many short items, what each costs besides its tiles (4 to 5 us): a prompt of 4096
 // tokens, 64 heads, 282 us (1 PFLOP/s of what its rows see); 43 chains of 202 nodes over nothing
 // 132 us, of which 42 are the bytes of queries and results.
 //
