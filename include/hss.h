@@ -588,6 +588,233 @@ hss_status hss_evict_blocks(const float* weights, const int32_t* block_table,
                             int32_t* new_ctx_len, int32_t* freed, int32_t* freed_offsets,
                             void* stream);
 
+/* What the layers of one step share in hss_norm_rope_tokens. */
+typedef struct hss_norm_rope_args {
+    hss_rope_args rope;      /* as in hss_rope_tokens */
+    int64_t q_weight_stride; /* elements from head to head of the weights: 0 (the heads share one */
+    int64_t k_weight_stride; /* row), or a multiple of 8, at least head_dim */
+    float eps;               /* >= 0, finite */
+    float weight_offset;     /* added to every weight, finite (1 where weights are kept around 0) */
+} hss_norm_rope_args;
+
+/*
+ * hss_rope_tokens with a root-mean-square norm of every query and key head before the rotation,
+ * in the same launch:
+ *   y[i] = x[i] / sqrt(mean_j x[j]^2 + eps) * (weight[i] + weight_offset),
+ * over the whole head (head_dim elements, the ones past rot_dim too), then rotated and written as
+ * there.  Values are not normed.  Norm and rotation are computed in fp32 and rounded once to bf16;
+ * the sum of squares is fp32 too, so that a head whose sum passes 3.4e38 comes out as 0.
+ *   q_weight, k_weight  device, [head_dim] or, with a stride, [heads, head_dim] bf16, 16-byte
+ *             aligned; NULL: 1 (weight_offset is then not added)
+ * The other arguments, the refusals and the device-side errors are those of hss_rope_tokens.
+ */
+hss_status hss_norm_rope_tokens(const hss_norm_rope_args* args, const uint16_t* Q,
+                                const uint16_t* K, const uint16_t* V, const uint16_t* q_weight,
+                                const uint16_t* k_weight, uint16_t* Q_out, uint16_t* K_out,
+                                uint16_t* K_cache, uint16_t* V_cache, void* stream);
+
+/*
+ * A paged cache in 4 bits.  Every 32 consecutive elements of a head share a bf16 scale; an element
+ * is a code from -7 to 7 times its group's scale, 4.5 bits an element in all.  A page holds keys
+ * and values, in tiles of 16 tokens of one head:
+ *     cache[max_blocks][num_kv_heads][block_size / 16][tile]
+ * with head_dim = 32 G and a tile of 18 head_dim bytes,
+ *     [ codes of K: 8 head_dim bytes | codes of V: 8 head_dim bytes |
+ *       scales of K: bf16 [16][G] | scales of V: bf16 [16][G] ],
+ * a code being kept as code + 8 in a nibble (the low nibble of a byte first).  Of token t (0 .. 15)
+ * and element d the nibble lies
+ *   K: in byte t head_dim / 2 + (d % 32 / 8) 4 G + d / 32 * 4 + d % 8 / 2, the low one if d is even
+ *   V: in byte ((d / 64) 32 + (d % 8) 4 + t % 8 / 2) 16 + d % 64 / 16 * 4 + t % 2 * 2 + t / 8,
+ *      the low one if d % 16 < 8
+ * so that a thread of the attention finds its operands of the matrix products side by side, and no
+ * byte holds two tokens.  (A nibble of 0 counts as -8; packing writes none.)
+ */
+/* Bytes of one page: num_kv_heads * block_size / 16 * 18 * head_dim (0 if the dims are invalid). */
+size_t hss_packed_page_bytes(const hss_dims* dims);
+
+/* What the layers of one step share in hss_pack_kv_tokens and hss_unpack_kv_tokens. */
+typedef struct hss_pack_args {
+    hss_dims dims;
+    const int64_t* slots;      /* device, [num_tokens], as in hss_write_kv_tokens */
+    int64_t num_tokens;
+    int64_t k_stride, v_stride; /* elements from token to token of K and V: multiples of 8, at least
+                                   num_kv_heads * head_dim */
+    int32_t* dev_status;       /* device int32 or NULL */
+} hss_pack_args;
+
+/*
+ * Write tokens into the packed cache.  Per token, kv head and group of 32 elements x, all in fp32:
+ *   scale = bf16(max |x| / 7),  code = max(-7, min(7, rint(x / scale)))    (ties to even)
+ * A group whose scale is 0 has codes 0; one with a NaN or an infinity gets the scale NaN, and reads
+ * as NaN.  The result is exact: the same bits wherever and with whatever else a token is packed.
+ *   K, V      device, token i's heads at i * stride, dense [heads, head_dim] bf16, 16-byte aligned;
+ *             either may be NULL (that half of the tokens is then left as it was)
+ *   cache     device, one layer's pages, 16-byte aligned
+ * A negative slot marks padding; a slot >= max_blocks * block_size is skipped and raises
+ * HSS_ERR_OUT_OF_RANGE in *dev_status and the library's device error word.  Name a slot once: what
+ * two tokens of one call leave in it is a mixture of both.  (One call packs whole tiles where 16
+ * tokens in a row fill one, so that tokens in the order of their slots are written fastest.)
+ */
+hss_status hss_pack_kv_tokens(const hss_pack_args* args, const uint16_t* K, const uint16_t* V,
+                              uint8_t* cache, void* stream);
+
+/*
+ * Read tokens back from the packed cache: code * scale, rounded once to bf16 (the keys of a packed
+ * cache for hss_project_kv_blocks, or a cache to be packed anew).  K and V are outputs here, laid
+ * out as above, and either may be NULL.  Rows of tokens with a negative slot, or one that is out of
+ * range (which raises the error), are left as they were.
+ */
+hss_status hss_unpack_kv_tokens(const hss_pack_args* args, const uint8_t* cache, uint16_t* K,
+                                uint16_t* V, void* stream);
+
+/* What the layers of one step share in hss_attend_packed. */
+typedef struct hss_packed_args {
+    hss_dims dims;
+    const int32_t* q_offsets;   /* device, [num_seqs + 1], as in hss_attend_tree */
+    int64_t total_q;            /* rows in all, q_offsets[num_seqs] */
+    int32_t max_q;              /* at least the most rows of a sequence */
+    int32_t window;             /* tokens that a row sees back from its own, >= 1; or 0: all */
+    int32_t sinks;              /* first tokens that stay visible behind the window, >= 0 */
+    const int32_t* block_table; /* device, [total_blocks] physical block ids */
+    const int32_t* seq_offsets; /* device, [num_seqs + 1], as in hss_score_blocks */
+    const int32_t* ctx_len;     /* device, [num_seqs]: cached tokens before the rows */
+    int64_t total_blocks;
+    int32_t num_seqs;
+    float scale;                /* factor on the scores, finite; usually head_dim^-0.5 */
+    void* workspace;            /* device, 256-byte aligned,
+                                   hss_attend_packed_workspace_bytes(...); what it holds does not
+                                   matter.  Calls that share one must not run at the same time. */
+    size_t workspace_bytes;
+    int32_t* dev_status;        /* device int32 or NULL */
+} hss_packed_args;
+
+/* Bytes of the workspace: enough for every call with these dims, window and sinks and these counts
+ * or smaller ones (0 if a count is negative or the dims are not valid). */
+size_t hss_attend_packed_workspace_bytes(const hss_dims* dims, int32_t num_seqs, int32_t max_q,
+                                         int64_t total_blocks, int32_t window, int32_t sinks);
+
+/*
+ * Attention over the packed cache: of the new token of a decode step, of a few drafted tokens in a
+ * row, or of a chunk of prompt tokens, with an optional sliding window behind which the first
+ * tokens stay visible.  Sequence s has ctx_len[s] cached tokens and then its rows' own tokens: row
+ * i's is at position ctx_len[s] + i (write them first, with hss_pack_kv_tokens).  It sees the
+ * positions
+ *   p <= ctx_len[s] + i,  and with a window only those with
+ *   p > ctx_len[s] + i - window  or  p < sinks.
+ * Position p is token p % block_size of the sequence's table entry p / block_size.  Pages that no
+ * row sees are not read, and their entries may hold anything (an evicted page's id).  Query head
+ * h reads kv head h / (num_q_heads / num_kv_heads).  Over the tokens that a row sees:
+ *   lse[row][h] = ln sum_p exp(scale q.k_p)
+ *   out[row][h] = sum_p exp(scale q.k_p - lse) v_p
+ * A row that sees nothing (its sequence's table does not reach that far) gets out 0 and lse -inf.
+ * Tokens that a row does not see may hold anything, scales of NaN included.
+ *   Q        device, [total_q, num_q_heads, head_dim] bf16, 16-byte aligned
+ *   cache    device, one layer's pages, 16-byte aligned
+ *   out      device, [total_q, num_q_heads, head_dim] bf16, 16-byte aligned
+ *   lse      device, [total_q, num_q_heads] f32, or NULL
+ * Scores, softmax statistics and sums are fp32.  The weights exp(s - m), each times its value's
+ * scale, enter the product with the codes rounded to bf16; the statistics take them unrounded.
+ * One more launch follows the attention itself on the stream (the join of what several CTAs have
+ * of a row); a pipeline wait that runs out raises HSS_ERR_DEVICE_TIMEOUT like those of the other
+ * kernels.
+ * Supported: num_q_heads / num_kv_heads <= 128, at most 2^30 rows of a sequence and kv head
+ * together; window, sinks >= 0; positions below 2^31 - 512.  Device-side errors
+ * (*dev_status and the library's device error word): a block id outside [0, max_blocks) of a page
+ * that a row sees hides its tokens and raises HSS_ERR_OUT_OF_RANGE; so does a table too short for
+ * ctx_len + rows (the tokens past it are hidden); a negative ctx_len counts as 0; a sequence with
+ * more than max_q rows raises HSS_ERR_INVALID_ARGUMENT and its rows past max_q are not written.
+ */
+hss_status hss_attend_packed(const hss_packed_args* args, const uint16_t* Q, const uint8_t* cache,
+                             uint16_t* out, float* lse, void* stream);
+
+/*
+ * Pages that sequences share.  refs[p] counts who holds page p: the table entries that name it, and
+ * whoever else the caller counts (a cache of prompt prefixes); 0: the page is free.  The two plans
+ * below take the tables and counts as they are and write new ones, so that a call can be repeated;
+ * the page copies they ask for are then made by hss_copy_pages, once per cache.
+ */
+
+/* Bytes of the workspace of hss_fork_pages and hss_compact_pages (0 if a count is negative). */
+size_t hss_fork_pages_workspace_bytes(int32_t num_new, int64_t max_blocks);
+size_t hss_compact_pages_workspace_bytes(int64_t max_blocks);
+
+/*
+ * The tables of the next step: num_new sequences, each the continuation of one of the present ones.
+ * New sequence i keeps the first len_i = min(lengths[i], what its parent's table has room for)
+ * tokens of sequence parents[i] (-1: none, len_i = 0) and gets room for room[i] more: its table has
+ * ceil((len_i + room[i]) / block_size) entries, of which the first kept_i = ceil(len_i /
+ * block_size) are the parent's.  So a sequence can go on (once), be forked (more than once), be cut
+ * back (a smaller length), grow, and be dropped (not at all; its pages lose a reference).
+ *   A last kept page that is partly filled will be written, if room[i] > 0.  It stays the new
+ * sequence's own if all its other references are such sequences too and i is the least of them;
+ * otherwise the new sequence gets a fresh page there, and the pair (old page, fresh page) is one of
+ * the copies.  The other entries past the kept ones are fresh pages as well.  Fresh pages are those
+ * whose count is then 0, handed out by ascending id in the order of (sequence, entry).
+ *   block_table, seq_offsets, num_seqs, total_blocks  the present tables, as in hss_score_blocks
+ *   refs       [max_blocks] in;  new_refs [max_blocks] out
+ *   released   [num_released] page ids that lose one reference besides (what hss_evict_blocks has
+ *              freed: entries of -1 are skipped), or NULL with num_released = 0
+ *   parents, lengths, room   [num_new]; negative lengths and room count as 0
+ *   new_table  [table_room], the tables packed, the rest -1;  new_offsets [num_new + 1]
+ *   copy_src, copy_dst  [num_new], the copies by sequence, packed, the rest -1
+ *   counts     [4]: entries of the new tables, copies, pages in use, fresh pages that were missing
+ * All arrays are on the device and int32, 4-byte aligned; no output overlaps an input.  The result
+ * is exact and the same on every run.  Device-side errors, in *dev_status and the library's device
+ * error word: a parent outside [-1, num_seqs) counts as -1 and raises HSS_ERR_OUT_OF_RANGE; so does
+ * an id outside [0, max_blocks) in a present table or (but for -1) in released, which is counted
+ * nowhere and kept as it is.  If there are not enough free pages, the last entries are -1 (a copy
+ * to such an entry has copy_dst -1) and HSS_ERR_OUT_OF_RANGE is raised; if the new tables need more
+ * than table_room entries, HSS_ERR_INVALID_ARGUMENT is, and nothing but counts[0] and new_offsets
+ * is then of use; so is it if a page has a smaller count than the present tables and released give
+ * up of it, and its page may then be handed out.
+ * num_seqs, num_new <= 2^20, total_blocks, table_room, num_released, max_blocks <= 2^30.
+ */
+hss_status hss_fork_pages(const int32_t* block_table, const int32_t* seq_offsets,
+                          int32_t num_seqs, int64_t total_blocks, const int32_t* refs,
+                          int64_t max_blocks, const int32_t* released, int64_t num_released,
+                          const int32_t* parents, const int32_t* lengths, const int32_t* room,
+                          int32_t num_new, int32_t block_size, int64_t table_room,
+                          int32_t* new_table, int32_t* new_offsets, int32_t* new_refs,
+                          int32_t* copy_src, int32_t* copy_dst, int32_t* counts, void* workspace,
+                          size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * Move pages to the front of the pool, so that its end can be given up.  With `used` pages that are
+ * not free, the free pages below `used` are filled in ascending order by the used pages from
+ * `used` on in descending order, at most move_room of them (the rest of the work is left for
+ * another call):
+ *   new_table  [total_blocks] the table with the moved ids replaced
+ *   new_refs   [max_blocks] the counts moved along
+ *   copy_src, copy_dst  [move_room] the moves, in that order, the rest -1
+ *   counts     [4]: moves, pages in use, the last used page + 1 after the moves, moves left over
+ * Whoever holds ids besides the table (refs counts them) has to follow the moves too.  Arrays,
+ * limits are as in hss_fork_pages; an id outside [0, max_blocks) other than -1 is kept and raises
+ * HSS_ERR_OUT_OF_RANGE, a negative count raises HSS_ERR_INVALID_ARGUMENT (its page counts as used);
+ * move_room <= 2^30.
+ */
+hss_status hss_compact_pages(const int32_t* block_table, int64_t total_blocks, const int32_t* refs,
+                             int64_t max_blocks, int64_t move_room, int32_t* new_table,
+                             int32_t* new_refs, int32_t* copy_src, int32_t* copy_dst,
+                             int32_t* counts, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream);
+
+/*
+ * Copy pages within one or two pools, in every layer of them:
+ *   pool[layer][copy_dst[i]] = pool[layer][copy_src[i]]    i < *num_copies, layer < num_layers
+ *   copy_src, copy_dst  device, [max_copies] int32; a pair with a negative id is skipped, one with
+ *              an id >= max_blocks too, which raises HSS_ERR_OUT_OF_RANGE.  The destinations are
+ *              distinct and none of them is a source.
+ *   num_copies device int32, or NULL for max_copies (values outside [0, max_copies] are clipped)
+ *   pool0, pool1  device, [num_layers][max_blocks][page_bytes], 16-byte aligned (the K and the V
+ *              cache); pool1 may be NULL
+ *   page_bytes a multiple of 16, 16 .. 2^30
+ * max_copies, max_blocks <= 2^30; num_layers <= 65535.
+ */
+hss_status hss_copy_pages(const int32_t* copy_src, const int32_t* copy_dst,
+                          const int32_t* num_copies, int64_t max_copies, void* pool0, void* pool1,
+                          int64_t page_bytes, int64_t max_blocks, int32_t num_layers,
+                          int32_t* dev_status, void* stream);
+
 /*
  * Failure-detection self-test.  Every pipeline wait in the tensor-core kernels gives up
  * after a time limit and reports HSS_ERR_DEVICE_TIMEOUT instead of hanging the GPU.  This

@@ -52,6 +52,10 @@ EXPORTED = (
     "hss_select_rows", "hss_self_test_wait_timeout", "hss_self_test_spread_wait",
     "hss_layer_step_bound", "hss_rope_table", "hss_rope_tokens", "hss_attend_tree",
     "hss_attend_tree_workspace_bytes", "hss_evict_blocks",
+    "hss_norm_rope_tokens", "hss_packed_page_bytes", "hss_pack_kv_tokens",
+    "hss_unpack_kv_tokens", "hss_attend_packed_workspace_bytes", "hss_attend_packed",
+    "hss_fork_pages_workspace_bytes", "hss_compact_pages_workspace_bytes", "hss_fork_pages",
+    "hss_compact_pages", "hss_copy_pages",
 )
 
 
@@ -154,6 +158,29 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.hss_evict_blocks.restype = i32
     lib.hss_evict_blocks.argtypes = [vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, vp, vp, vp, vp,
                                      vp, vp, vp]
+    lib.hss_norm_rope_tokens.restype = i32
+    lib.hss_norm_rope_tokens.argtypes = [ctypes.POINTER(hss_norm_rope_args)] + [vp] * 10
+    lib.hss_packed_page_bytes.restype = sz
+    lib.hss_packed_page_bytes.argtypes = [dp]
+    lib.hss_pack_kv_tokens.restype = i32
+    lib.hss_pack_kv_tokens.argtypes = [ctypes.POINTER(hss_pack_args)] + [vp] * 4
+    lib.hss_unpack_kv_tokens.restype = i32
+    lib.hss_unpack_kv_tokens.argtypes = [ctypes.POINTER(hss_pack_args)] + [vp] * 4
+    lib.hss_attend_packed_workspace_bytes.restype = sz
+    lib.hss_attend_packed_workspace_bytes.argtypes = [dp, i32, i32, i64, i32, i32]
+    lib.hss_attend_packed.restype = i32
+    lib.hss_attend_packed.argtypes = [ctypes.POINTER(hss_packed_args)] + [vp] * 5
+    lib.hss_fork_pages_workspace_bytes.restype = sz
+    lib.hss_fork_pages_workspace_bytes.argtypes = [i32, i64]
+    lib.hss_compact_pages_workspace_bytes.restype = sz
+    lib.hss_compact_pages_workspace_bytes.argtypes = [i64]
+    lib.hss_fork_pages.restype = i32
+    lib.hss_fork_pages.argtypes = [vp, vp, i32, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, i64,
+                                   vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.hss_compact_pages.restype = i32
+    lib.hss_compact_pages.argtypes = [vp, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.hss_copy_pages.restype = i32
+    lib.hss_copy_pages.argtypes = [vp, vp, vp, i64, vp, vp, i64, i64, i32, vp, vp]
     _lib = lib
     return lib
 
@@ -479,6 +506,186 @@ def hss_evict_blocks(weights, block_table, seq_offsets, ctx_len, budgets, num_se
                                  _ptr(new_ctx_len), _ptr(freed), _ptr(freed_offsets),
                                  _stream(stream))
     _check(st, "hss_evict_blocks")
+
+
+class hss_norm_rope_args(ctypes.Structure):
+    """What the layers of one step share in hss_norm_rope_tokens (hss_norm_rope_args in hss.h)."""
+
+    _fields_ = [
+        ("rope", hss_rope_args),
+        ("q_weight_stride", ctypes.c_int64),
+        ("k_weight_stride", ctypes.c_int64),
+        ("eps", ctypes.c_float),
+        ("weight_offset", ctypes.c_float),
+    ]
+
+
+class NormRopeTokens:
+    """hss_norm_rope_tokens with what the layers of one step share bound once.
+
+    Each call norms and rotates one layer's queries and keys, with that layer's weights, and
+    writes its keys and values into the paged caches; what a call does not want is None.  The
+    tensors bound here are kept alive.
+    """
+
+    def __init__(self, dims, rot_dim: int, layout: int, turns, magnitude: float, positions, slots,
+                 num_tokens: int, q_stride: int, k_stride: int, v_stride: int,
+                 q_weight_stride: int, k_weight_stride: int, eps: float,
+                 weight_offset: float = 0.0, dev_status=None):
+        self._fn = load().hss_norm_rope_tokens
+        self._keep = (turns, positions, slots, dev_status)
+        self._args = hss_norm_rope_args(
+            hss_rope_args(hss_dims.of(dims), int(rot_dim), int(layout), _ptr(turns),
+                          float(magnitude), _ptr(positions), _ptr(slots), int(num_tokens),
+                          int(q_stride), int(k_stride), int(v_stride), _ptr(dev_status)),
+            int(q_weight_stride), int(k_weight_stride), float(eps), float(weight_offset))
+        self._ref = ctypes.byref(self._args)
+
+    def __call__(self, Q, K, V, q_weight, k_weight, Q_out, K_out, K_cache, V_cache,
+                 stream=None) -> None:
+        st = self._fn(self._ref, _ptr(Q), _ptr(K), _ptr(V), _ptr(q_weight), _ptr(k_weight),
+                      _ptr(Q_out), _ptr(K_out), _ptr(K_cache), _ptr(V_cache), _stream(stream))
+        _check(st, "hss_norm_rope_tokens")
+
+
+def hss_packed_page_bytes(dims) -> int:
+    """Bytes of one page of the packed cache (0 if the dims are invalid)."""
+    return load().hss_packed_page_bytes(ctypes.byref(hss_dims.of(dims)))
+
+
+class hss_pack_args(ctypes.Structure):
+    """What the layers of one step share in packing and unpacking (hss_pack_args in hss.h)."""
+
+    _fields_ = [
+        ("dims", hss_dims),
+        ("slots", ctypes.c_void_p),
+        ("num_tokens", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("dev_status", ctypes.c_void_p),
+    ]
+
+
+class PackTokens:
+    """hss_pack_kv_tokens and hss_unpack_kv_tokens with the step's slots and strides bound once.
+
+    pack writes one layer's keys and values of the tokens into its packed cache, unpack reads
+    them back; K or V may be None.  The tensors bound here are kept alive.
+    """
+
+    def __init__(self, dims, slots, num_tokens: int, k_stride: int, v_stride: int,
+                 dev_status=None):
+        lib = load()
+        self._pack, self._unpack = lib.hss_pack_kv_tokens, lib.hss_unpack_kv_tokens
+        self._keep = (slots, dev_status)
+        self._args = hss_pack_args(hss_dims.of(dims), _ptr(slots), int(num_tokens), int(k_stride),
+                                   int(v_stride), _ptr(dev_status))
+        self._ref = ctypes.byref(self._args)
+
+    def pack(self, K, V, cache, stream=None) -> None:
+        st = self._pack(self._ref, _ptr(K), _ptr(V), _ptr(cache), _stream(stream))
+        _check(st, "hss_pack_kv_tokens")
+
+    def unpack(self, cache, K, V, stream=None) -> None:
+        st = self._unpack(self._ref, _ptr(cache), _ptr(K), _ptr(V), _stream(stream))
+        _check(st, "hss_unpack_kv_tokens")
+
+
+class hss_packed_args(ctypes.Structure):
+    """What the layers of one step share in hss_attend_packed (hss_packed_args in hss.h)."""
+
+    _fields_ = [
+        ("dims", hss_dims),
+        ("q_offsets", ctypes.c_void_p),
+        ("total_q", ctypes.c_int64),
+        ("max_q", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("sinks", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p),
+        ("seq_offsets", ctypes.c_void_p),
+        ("ctx_len", ctypes.c_void_p),
+        ("total_blocks", ctypes.c_int64),
+        ("num_seqs", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("dev_status", ctypes.c_void_p),
+    ]
+
+
+def hss_attend_packed_workspace_bytes(dims, num_seqs: int, max_q: int, total_blocks: int,
+                                      window: int = 0, sinks: int = 0) -> int:
+    return load().hss_attend_packed_workspace_bytes(
+        ctypes.byref(hss_dims.of(dims)), int(num_seqs), int(max_q), int(total_blocks),
+        int(window), int(sinks))
+
+
+class AttendPacked:
+    """hss_attend_packed with what the layers of one step share bound once.
+
+    Each call attends one layer's rows over its packed cache: out, and where asked for the rows'
+    lse.  The tensors bound here are kept alive.
+    """
+
+    def __init__(self, dims, q_offsets, total_q: int, max_q: int, block_table, seq_offsets,
+                 ctx_len, num_seqs: int, total_blocks: int, window: int, sinks: int,
+                 scale: float, workspace, workspace_bytes: int, dev_status=None):
+        self._fn = load().hss_attend_packed
+        self._keep = (q_offsets, block_table, seq_offsets, ctx_len, workspace, dev_status)
+        self._args = hss_packed_args(
+            hss_dims.of(dims), _ptr(q_offsets), int(total_q), int(max_q), int(window), int(sinks),
+            _ptr(block_table), _ptr(seq_offsets), _ptr(ctx_len), int(total_blocks),
+            int(num_seqs), float(scale), _ptr(workspace), int(workspace_bytes), _ptr(dev_status))
+        self._ref = ctypes.byref(self._args)
+
+    def __call__(self, Q, cache, out, lse=None, stream=None) -> None:
+        st = self._fn(self._ref, _ptr(Q), _ptr(cache), _ptr(out), _ptr(lse), _stream(stream))
+        _check(st, "hss_attend_packed")
+
+
+def hss_fork_pages_workspace_bytes(num_new: int, max_blocks: int) -> int:
+    return load().hss_fork_pages_workspace_bytes(int(num_new), int(max_blocks))
+
+
+def hss_compact_pages_workspace_bytes(max_blocks: int) -> int:
+    return load().hss_compact_pages_workspace_bytes(int(max_blocks))
+
+
+def hss_fork_pages(block_table, seq_offsets, num_seqs: int, total_blocks: int, refs,
+                   max_blocks: int, released, num_released: int, parents, lengths, room,
+                   num_new: int, block_size: int, table_room: int, new_table, new_offsets,
+                   new_refs, copy_src, copy_dst, counts, workspace, workspace_bytes: int,
+                   dev_status=None, stream=None) -> None:
+    """The next step's tables and page counts: sequences go on, fork, are cut, dropped or grow."""
+    st = load().hss_fork_pages(
+        _ptr(block_table), _ptr(seq_offsets), int(num_seqs), int(total_blocks), _ptr(refs),
+        int(max_blocks), _ptr(released), int(num_released), _ptr(parents), _ptr(lengths),
+        _ptr(room), int(num_new), int(block_size), int(table_room), _ptr(new_table),
+        _ptr(new_offsets), _ptr(new_refs), _ptr(copy_src), _ptr(copy_dst), _ptr(counts),
+        _ptr(workspace), int(workspace_bytes), _ptr(dev_status), _stream(stream))
+    _check(st, "hss_fork_pages")
+
+
+def hss_compact_pages(block_table, total_blocks: int, refs, max_blocks: int, move_room: int,
+                      new_table, new_refs, copy_src, copy_dst, counts, workspace,
+                      workspace_bytes: int, dev_status=None, stream=None) -> None:
+    """Plan the moves of used pages into the free ones at the front of the pool."""
+    st = load().hss_compact_pages(
+        _ptr(block_table), int(total_blocks), _ptr(refs), int(max_blocks), int(move_room),
+        _ptr(new_table), _ptr(new_refs), _ptr(copy_src), _ptr(copy_dst), _ptr(counts),
+        _ptr(workspace), int(workspace_bytes), _ptr(dev_status), _stream(stream))
+    _check(st, "hss_compact_pages")
+
+
+def hss_copy_pages(copy_src, copy_dst, num_copies, max_copies: int, pool0, pool1,
+                   page_bytes: int, max_blocks: int, num_layers: int, dev_status=None,
+                   stream=None) -> None:
+    """pool[layer][copy_dst[i]] = pool[layer][copy_src[i]] for every planned copy and layer."""
+    st = load().hss_copy_pages(
+        _ptr(copy_src), _ptr(copy_dst), _ptr(num_copies), int(max_copies), _ptr(pool0),
+        _ptr(pool1), int(page_bytes), int(max_blocks), int(num_layers), _ptr(dev_status),
+        _stream(stream))
+    _check(st, "hss_copy_pages")
 
 
 def hss_layer_step_static_max_seqs() -> int:

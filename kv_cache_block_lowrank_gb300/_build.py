@@ -16,8 +16,11 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["hss_api.cu", "project_tc.cu", "score_decode.cu", "score_decode_k1.cu",
            "score_decode_k2.cu", "score_decode_k4.cu", "score_decode_k8.cu", "score_tc.cu",
            "rank.cu", "no_alloc.cu", "selftest.cu", "cache_api.cu", "rope.cu", "attend.cu",
-           "evict.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "rank_device.cuh", "score_decode_kernel.cuh"]
+           "evict.cu", "packed_api.cu", "norm_rope.cu", "pack.cu", "pages.cu", "attend_packed.cu",
+           "attend_packed_64.cu", "attend_packed_128.cu", "attend_packed_192.cu",
+           "attend_packed_256.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "rank_device.cuh", "score_decode_kernel.cuh", "packed.cuh",
+           "attend_packed.cuh"]
 
 
 def nvcc() -> str:

@@ -18,6 +18,42 @@ bool bad_stride(int64_t stride, int64_t width) {
     return stride < width || stride % 8 != 0 || stride > (int64_t{1} << 32);
 }
 
+// The checks of hss_rope_tokens and hss_norm_rope_tokens; *nothing: no work is asked for.
+hss_status check_rope(const hss_rope_args& args, const uint16_t* Q, const uint16_t* K,
+                      const uint16_t* V, const uint16_t* Q_out, const uint16_t* K_out,
+                      const uint16_t* K_cache, const uint16_t* V_cache, bool* nothing) {
+    const hss_dims& d = args.dims;
+    *nothing = true;
+    const hss_status st = hss_validate_dims(&d);
+    if (st != HSS_OK) return st;
+    if (args.rot_dim < 2 || args.rot_dim % 2 != 0 || args.rot_dim > d.head_dim ||
+        (args.layout != HSS_ROPE_HALF && args.layout != HSS_ROPE_INTERLEAVED) ||
+        !std::isfinite(args.magnitude) || args.num_tokens < 0 ||
+        args.num_tokens > (int64_t{1} << 30))
+        return HSS_ERR_INVALID_ARGUMENT;
+    if (args.num_tokens == 0) return HSS_OK;
+    const bool k_asked = K_out != nullptr || K_cache != nullptr;
+    if ((Q_out != nullptr && Q == nullptr) || (k_asked && K == nullptr) ||
+        (V_cache != nullptr && V == nullptr))
+        return HSS_ERR_NULL_POINTER;
+    if ((Q_out != nullptr || k_asked) && (args.turns == nullptr || args.positions == nullptr))
+        return HSS_ERR_NULL_POINTER;
+    if ((K_cache != nullptr || V_cache != nullptr) && args.slots == nullptr)
+        return HSS_ERR_NULL_POINTER;
+    if (misaligned(Q, 16) || misaligned(K, 16) || misaligned(V, 16) || misaligned(Q_out, 16) ||
+        misaligned(K_out, 16) || misaligned(K_cache, 16) || misaligned(V_cache, 16) ||
+        misaligned(args.turns, 8) || misaligned(args.positions, 8) ||
+        misaligned(args.slots, 8) || misaligned(args.dev_status, 4))
+        return HSS_ERR_MISALIGNED;
+    const int64_t hd = d.head_dim;
+    if ((Q_out != nullptr && bad_stride(args.q_stride, d.num_q_heads * hd)) ||
+        (k_asked && bad_stride(args.k_stride, d.num_kv_heads * hd)) ||
+        (V_cache != nullptr && bad_stride(args.v_stride, d.num_kv_heads * hd)))
+        return HSS_ERR_INVALID_ARGUMENT;
+    *nothing = Q_out == nullptr && !k_asked && V_cache == nullptr;
+    return HSS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -70,36 +106,33 @@ hss_status hss_rope_tokens(const hss_rope_args* args, const uint16_t* Q, const u
                            const uint16_t* V, uint16_t* Q_out, uint16_t* K_out,
                            uint16_t* K_cache, uint16_t* V_cache, void* stream) {
     if (args == nullptr) return HSS_ERR_NULL_POINTER;
-    const hss_dims& d = args->dims;
-    const hss_status st = hss_validate_dims(&d);
-    if (st != HSS_OK) return st;
-    if (args->rot_dim < 2 || args->rot_dim % 2 != 0 || args->rot_dim > d.head_dim ||
-        (args->layout != HSS_ROPE_HALF && args->layout != HSS_ROPE_INTERLEAVED) ||
-        !std::isfinite(args->magnitude) || args->num_tokens < 0 ||
-        args->num_tokens > (int64_t{1} << 30))
-        return HSS_ERR_INVALID_ARGUMENT;
-    if (args->num_tokens == 0) return HSS_OK;
-    const bool k_asked = K_out != nullptr || K_cache != nullptr;
-    if ((Q_out != nullptr && Q == nullptr) || (k_asked && K == nullptr) ||
-        (V_cache != nullptr && V == nullptr))
-        return HSS_ERR_NULL_POINTER;
-    if ((Q_out != nullptr || k_asked) && (args->turns == nullptr || args->positions == nullptr))
-        return HSS_ERR_NULL_POINTER;
-    if ((K_cache != nullptr || V_cache != nullptr) && args->slots == nullptr)
-        return HSS_ERR_NULL_POINTER;
-    if (misaligned(Q, 16) || misaligned(K, 16) || misaligned(V, 16) || misaligned(Q_out, 16) ||
-        misaligned(K_out, 16) || misaligned(K_cache, 16) || misaligned(V_cache, 16) ||
-        misaligned(args->turns, 8) || misaligned(args->positions, 8) ||
-        misaligned(args->slots, 8) || misaligned(args->dev_status, 4))
-        return HSS_ERR_MISALIGNED;
-    const int64_t hd = d.head_dim;
-    if ((Q_out != nullptr && bad_stride(args->q_stride, d.num_q_heads * hd)) ||
-        (k_asked && bad_stride(args->k_stride, d.num_kv_heads * hd)) ||
-        (V_cache != nullptr && bad_stride(args->v_stride, d.num_kv_heads * hd)))
-        return HSS_ERR_INVALID_ARGUMENT;
-    if (Q_out == nullptr && !k_asked && V_cache == nullptr) return HSS_OK;
+    bool nothing;
+    const hss_status st =
+        check_rope(*args, Q, K, V, Q_out, K_out, K_cache, V_cache, &nothing);
+    if (st != HSS_OK || nothing) return st;
     return launch_rope(RopeArgs{args, Q, K, V, Q_out, K_out, K_cache, V_cache},
                        static_cast<cudaStream_t>(stream));
+}
+
+hss_status hss_norm_rope_tokens(const hss_norm_rope_args* args, const uint16_t* Q,
+                                const uint16_t* K, const uint16_t* V, const uint16_t* q_weight,
+                                const uint16_t* k_weight, uint16_t* Q_out, uint16_t* K_out,
+                                uint16_t* K_cache, uint16_t* V_cache, void* stream) {
+    if (args == nullptr) return HSS_ERR_NULL_POINTER;
+    bool nothing;
+    const hss_status st =
+        check_rope(args->rope, Q, K, V, Q_out, K_out, K_cache, V_cache, &nothing);
+    if (st != HSS_OK) return st;
+    const int64_t hd = args->rope.dims.head_dim;
+    if (!(args->eps >= 0) || !std::isfinite(args->eps) || !std::isfinite(args->weight_offset) ||
+        (args->q_weight_stride != 0 && bad_stride(args->q_weight_stride, hd)) ||
+        (args->k_weight_stride != 0 && bad_stride(args->k_weight_stride, hd)))
+        return HSS_ERR_INVALID_ARGUMENT;
+    if (misaligned(q_weight, 16) || misaligned(k_weight, 16)) return HSS_ERR_MISALIGNED;
+    if (nothing) return HSS_OK;
+    return launch_norm_rope(NormRopeArgs{args, Q, K, V, q_weight, k_weight, Q_out, K_out, K_cache,
+                                         V_cache},
+                            static_cast<cudaStream_t>(stream));
 }
 
 size_t hss_attend_tree_workspace_bytes(const hss_dims* dims, int32_t num_seqs, int32_t max_q,

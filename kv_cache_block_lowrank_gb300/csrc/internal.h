@@ -202,6 +202,97 @@ struct EvictArgs {
 };
 hss_status launch_evict(const EvictArgs& e, cudaStream_t stream);
 
+// ------------------------------------------------------------------- normed rotary writes
+struct NormRopeArgs {
+    const hss_norm_rope_args* a;
+    const uint16_t* Q;
+    const uint16_t* K;
+    const uint16_t* V;
+    const uint16_t* q_weight;
+    const uint16_t* k_weight;
+    uint16_t* Q_out;
+    uint16_t* K_out;
+    uint16_t* K_cache;
+    uint16_t* V_cache;
+};
+hss_status launch_norm_rope(const NormRopeArgs& r, cudaStream_t stream);
+
+// ------------------------------------------------------------------- packed cache
+hss_status launch_pack(const hss_pack_args& a, const uint16_t* K, const uint16_t* V,
+                       uint8_t* cache, cudaStream_t stream);
+hss_status launch_unpack(const hss_pack_args& a, const uint8_t* cache, uint16_t* K, uint16_t* V,
+                         cudaStream_t stream);
+
+struct PackedArgs {
+    const hss_packed_args* a;
+    const uint16_t* Q;
+    const uint8_t* cache;
+    uint16_t* out;
+    float* lse;
+};
+size_t attend_packed_workspace_bytes(const hss_dims& d, int32_t num_seqs, int32_t max_q,
+                                     int64_t total_blocks, int32_t window, int32_t sinks);
+hss_status launch_attend_packed(const PackedArgs& a, cudaStream_t stream);
+
+// ------------------------------------------------------------------- pages
+struct ForkArgs {
+    const int32_t* table;
+    const int32_t* seq_offsets;
+    int32_t num_seqs;
+    int64_t total;
+    const int32_t* refs;
+    int64_t max_blocks;
+    const int32_t* released;
+    int64_t num_released;
+    const int32_t* parents;
+    const int32_t* lengths;
+    const int32_t* room;
+    int32_t num_new;
+    int32_t block_size;
+    int64_t table_room;
+    int32_t* new_table;
+    int32_t* new_offsets;
+    int32_t* new_refs;
+    int32_t* copy_src;
+    int32_t* copy_dst;
+    int32_t* counts;
+    int32_t* workspace;
+    int32_t* dev_status;
+};
+size_t fork_workspace_bytes(int32_t num_new, int64_t max_blocks);
+hss_status launch_fork(const ForkArgs& f, cudaStream_t stream);
+
+struct CompactArgs {
+    const int32_t* table;
+    int64_t total;
+    const int32_t* refs;
+    int64_t max_blocks;
+    int64_t move_room;
+    int32_t* new_table;
+    int32_t* new_refs;
+    int32_t* copy_src;
+    int32_t* copy_dst;
+    int32_t* counts;
+    int32_t* workspace;
+    int32_t* dev_status;
+};
+size_t compact_workspace_bytes(int64_t max_blocks);
+hss_status launch_compact(const CompactArgs& c, cudaStream_t stream);
+
+struct CopyArgs {
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* num_copies;
+    int64_t max_copies;
+    void* pool0;
+    void* pool1;
+    int64_t page_bytes;
+    int64_t max_blocks;
+    int32_t num_layers;
+    int32_t* dev_status;
+};
+hss_status launch_copy_pages(const CopyArgs& c, cudaStream_t stream);
+
 // ------------------------------------------------------------------- layer step
 // Every argument check of hss_layer_step, and the path it takes, decided before anything is
 // enqueued (hss_layer_step and hss_layer_step_static both run it first).
