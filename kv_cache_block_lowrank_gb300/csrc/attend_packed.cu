@@ -6,9 +6,9 @@
 namespace hss {
 namespace {
 
-using packed::kGrid;
-
-constexpr int kMostRows = 16;  // of a row tile
+// Ranges of the list, and their rows, that the workspace has room for.
+constexpr int kRanges = 4 * packed::kSms;
+constexpr int kRangeRows = 8 * kRanges;
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -22,9 +22,9 @@ int n_tiles(const hss_dims& d, int64_t max_q) {
 
 size_t attend_packed_workspace_bytes(const hss_dims& d, int32_t, int32_t, int64_t, int32_t,
                                      int32_t) {
-    return round_up(kGrid * sizeof(packed::Start)) +
-           round_up(2 * kGrid * kMostRows * sizeof(float2)) +
-           static_cast<size_t>(2 * kGrid * kMostRows) * d.head_dim * sizeof(float);
+    return round_up(kRanges * sizeof(packed::Start)) +
+           round_up(2 * kRangeRows * sizeof(float2)) +
+           static_cast<size_t>(2 * kRangeRows) * d.head_dim * sizeof(float);
 }
 
 hss_status launch_attend_packed(const PackedArgs& a, cudaStream_t stream) {
@@ -55,9 +55,9 @@ hss_status launch_attend_packed(const PackedArgs& a, cudaStream_t stream) {
     p.lib_error = dev->error_word;
     uint8_t* w = static_cast<uint8_t*>(x.workspace);
     p.starts = reinterpret_cast<packed::Start*>(w);
-    w += round_up(kGrid * sizeof(packed::Start));
+    w += round_up(kRanges * sizeof(packed::Start));
     p.part_ml = reinterpret_cast<float2*>(w);
-    w += round_up(2 * kGrid * kMostRows * sizeof(float2));
+    w += round_up(2 * kRangeRows * sizeof(float2));
     p.part_o = reinterpret_cast<float*>(w);
     const int n = n_tiles(x.dims, p.max_q);
     switch (x.dims.head_dim) {

@@ -6,8 +6,7 @@
 //   S^T = K Q^T,  P = exp2(c S - m),  O^T = V^T P^T,  l = sum P
 // with mma.m16n8k16: tokens (of V^T: elements) are the 16 rows of the product and query rows its 8
 // columns, so that K and V, which are what there is much of, are the operand that goes from packed
-// words straight into registers, and eight query rows fill an instruction.  Four bits become bf16
-// by placing a nibble under the exponent of 128 and subtracting 136, exactly.  A group's scale
+// words straight into registers, and eight query rows fill an instruction.  A group's scale
 // multiplies what the group adds to S, and for V the weight of its token: P is scaled, rounded to
 // bf16 and transposed (movmatrix) once for each group of 32 elements.
 //
@@ -16,23 +15,28 @@
 //
 // Split.  All (sequence, row tile, kv head, tile) form one list, cut into equal contiguous ranges, a
 // CTA each.  Within a CTA the warps take the tiles of a unit (sequence, row tile, head) in turn,
-// each with a ring of its own that bulk copies fill (a tile is contiguous), and put m, l and O
-// together in shared memory at the unit's end or the range's.  What a range does not have whole
+// each with a ring of its own that its asynchronous copies fill, and put m, l and O together in shared memory at the unit's end or the range's.  What a range does not have whole
 // goes to the workspace and a second kernel joins it.
 #pragma once
+
+#include <type_traits>
 
 #include "packed.cuh"
 
 namespace hss {
 namespace packed {
 
-constexpr int kGrid = 152;         // GB300's SMs; the workspace does not depend on the device
+constexpr int kSms = 152;          // GB300's; the workspace does not depend on the device
 constexpr float kLazy = 8.0f;
+constexpr int kMostWarps = 6;
+constexpr int kMostSlots = 4;       // of a warp's ring
+constexpr int kControlBytes = 2048;  // barriers, and from 512 on the warps' walks
 
 struct Start {
     int64_t total, per;  // the list's length, of a range
     int64_t t, cost;     // where the CTA's range begins in a unit, and the unit's length
-    int32_t s, rt, h, pad;
+    int32_t s, rt, h;
+    int32_t q0, r0, live;  // the sequence's first query row, the unit's rows of it
 };
 
 struct Params {
@@ -53,25 +57,32 @@ struct Params {
     int32_t* dev_status;
     int32_t* lib_error;
     // workspace
-    Start* starts;    // [kGrid]
-    float2* part_ml;  // [2 kGrid][R] (m, l)
-    float* part_o;    // [2 kGrid][R][head_dim]
+    Start* starts;    // [ranges]
+    float2* part_ml;  // [2 ranges][R] (m, l)
+    float* part_o;    // [2 ranges][R][head_dim]
 };
 
 template <int HD, int NT>
 struct Shape {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kWarps = 8;
+    // Few rows: nibbles go into the products as they are (see raw_codes), two tiles at a time.
+    static constexpr bool kRaw = NT == 1 && HD <= 128;
+    static constexpr int kWarps = kRaw ? 6 : 4;
+    static constexpr int kTiles = kRaw ? 2 : 1;  // of a step, and of a ring's slot
+    static constexpr int kCtas = 2;   // of an SM
+    static constexpr int kRanges = kSms * kCtas;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kOStride = HD + 4;  // floats of a row of O in shared memory
     static constexpr int kOBytes = kWarps * kRows * kOStride * 4;
     static constexpr int kMlBytes = kWarps * kRows * 8;
-    static constexpr int kTileBytes = Tile<HD>::kBytes;
-    static constexpr int kBudget = 232448 - 1024 - 2048 - kOBytes - kMlBytes;
-    static constexpr int kFits = kBudget / (kWarps * kTileBytes);
-    static constexpr int kSlots = kFits < 16 ? kFits : 16;  // of a warp's ring
+    static constexpr int kSlotBytes = kTiles * Tile<HD>::kBytes;
+    // (of the SM's 228 KB a CTA costs 1 KB besides, and its start may not be aligned)
+    static constexpr int kBudget =
+        233472 / kCtas - 1024 - 128 - kControlBytes - kOBytes - kMlBytes;
+    static constexpr int kFits = kBudget / (kWarps * kSlotBytes);
+    static constexpr int kSlots = kFits < kMostSlots ? kFits : kMostSlots;
     static constexpr int kSmemBytes =
-        1024 + 2048 + kOBytes + kMlBytes + kWarps * kSlots * kTileBytes;
+        128 + kControlBytes + kOBytes + kMlBytes + kWarps * kSlots * kSlotBytes;
     static_assert(kSlots >= 2, "tiles in flight");
 };
 
@@ -143,18 +154,17 @@ struct Walk {
     int64_t f, f1;
     int t;
 
-    __device__ __forceinline__ void begin(const Params& p, const Start& st) {
+    __device__ __forceinline__ void begin(const Params& p, const Start& st, const SeqInfo& seq,
+                                          const View& view) {
         f = min(st.total, blockIdx.x * st.per);
         f1 = min(st.total, f + st.per);
         s = st.s;
         rt = st.rt;
         h = st.h;
         t = static_cast<int>(st.t);
-        if (f < f1) {
-            x = load_seq(p, s);
-            rts = row_tiles<R>(p, x);
-            v = view_of<R>(p, x, rt);
-        }
+        x = seq;
+        v = view;
+        rts = row_tiles<R>(p, x);
     }
     __device__ __forceinline__ bool next(const Params& p) {
         if (f >= f1) return false;
@@ -186,13 +196,14 @@ struct Walk {
     }
 };
 
+// D = A B + C
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                    uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                                    uint32_t b1, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+          "f"(c[2]), "f"(c[3]));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
@@ -201,15 +212,40 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 
-// Nibbles j and j + 4 of a word, less 8, as two bf16.
-__device__ __forceinline__ uint32_t two_codes(uint32_t w, int j) {
-    const uint32_t u = ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u;  // 128 + nibble
-    const uint32_t k136 = 0x43084308u;
-    __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
-                               *reinterpret_cast<const __nv_bfloat162*>(&k136));
+// The codes of a word as bf16, nibbles j and j + 4 in out[j]: those of j = 0 and 2 divided by 64,
+// those of 1 and 3 by 4.  The low eight bits of a bf16, the last of its exponent among them, count in
+// steps of 2^-133 from 0 on, so that a nibble in either half of them needs no shift and no
+// exponent put above it: times 2^127, less 8, in one exact operation.
+__device__ __forceinline__ uint32_t code_fma(uint32_t nibbles, uint32_t minus) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(nibbles), "r"(0x7F007F00u), "r"(minus));
+    return d;
+}
+__device__ __forceinline__ void codes_of(uint32_t (&out)[4], uint32_t w) {
+    const uint32_t t = w >> 8;
+    out[0] = code_fma(w & 0x000F000Fu, 0xBE00BE00u);  // (-1/8, -1/8)
+    out[1] = code_fma(w & 0x00F000F0u, 0xC000C000u);  // (-2, -2)
+    out[2] = code_fma(t & 0x000F000Fu, 0xBE00BE00u);
+    out[3] = code_fma(t & 0x00F000F0u, 0xC000C000u);
+}
+// Nibbles as they are, bf16 in steps of 2^-133 (the tensor cores take such numbers as well as
+// others): those of j = 1 and 3 sixteen times as large.  What multiplies them is scaled up by a
+// power of two, and their 8 is taken away by a product with these:
+__device__ __forceinline__ void raw_codes(uint32_t (&out)[4], uint32_t w) {
+    const uint32_t t = w >> 8;
+    out[0] = w & 0x000F000Fu;
+    out[1] = w & 0x00F000F0u;
+    out[2] = t & 0x000F000Fu;
+    out[3] = t & 0x00F000F0u;
+}
+constexpr uint32_t kMinus8 = 0x80088008u, kMinus128 = 0x80808080u;
+// 2^x, -126 <= x <= 127.
+__device__ __forceinline__ float pow2(int x) { return __int_as_float((x + 127) << 23); }
+__device__ __forceinline__ uint32_t times2(uint32_t two, float f) {
+    __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&two),
+                               __floats2bfloat162_rn(f, f));
     return *reinterpret_cast<uint32_t*>(&d);
 }
-
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* at) {
     if constexpr (N % 4 == 0) {
@@ -237,14 +273,20 @@ __device__ __forceinline__ float scale_at(const uint32_t (&w)[N], int i) {
 }
 
 struct alignas(8) Control {
-    uint64_t full[8 * 16];     // [warp][slot]
     uint64_t arrived, merged;  // the warps' parts of a piece are there; are joined
-    int bad[8 * 16];           // [warp][slot] the tile's block id is out of range
     int abort;
     Start start;
-    int64_t scan[8];
+    SeqInfo seq;  // of the unit where the range begins
+    View view;
+    int64_t scan[kMostWarps];
 };
-static_assert(sizeof(Control) <= 2048, "control block");
+static_assert(sizeof(Control) <= 512, "control block");
+
+// (a 64-bit division is some hundred instructions, one after another)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
 
 // Where every CTA's range begins, from a scan of the sequences' lengths.
 template <int R, int THREADS>
@@ -284,7 +326,7 @@ __device__ __forceinline__ void find_start(const Params& p, Control& ctl, int64_
         if (w < warp) before += ctl.scan[w];
         total += ctl.scan[w];
     }
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, least);
+    const int64_t per = max(divide(total + gridDim.x - 1, gridDim.x), least);
     const int64_t f0 = blockIdx.x * per;
     if (threadIdx.x == 0) {
         ctl.start.total = total;
@@ -304,9 +346,16 @@ __device__ __forceinline__ void find_start(const Params& p, Control& ctl, int64_
             }
             ctl.start.s = s;
             ctl.start.rt = rt;
-            ctl.start.h = static_cast<int>(o / cost);
-            ctl.start.t = o % cost;
+            const int64_t h = divide(o, cost);
+            ctl.start.h = static_cast<int>(h);
+            ctl.start.t = o - h * cost;
             ctl.start.cost = cost;
+            const View v = view_of<R>(p, x, rt);
+            ctl.start.q0 = x.q0;
+            ctl.start.r0 = v.r0;
+            ctl.start.live = v.live;
+            ctl.seq = x;
+            ctl.view = v;
         }
         before += n;
     }
@@ -316,10 +365,10 @@ __device__ __forceinline__ void find_start(const Params& p, Control& ctl, int64_
 
 // A finished row: out and lse.
 template <int HD>
-__device__ __forceinline__ void write_row(const Params& p, const SeqInfo& x, int r, int h, float m,
-                                          float l, const float2 (&acc)[HD / 64]) {
+__device__ __forceinline__ void write_row(const Params& p, int q0, int r, int h, float m, float l,
+                                          const float2 (&acc)[HD / 64]) {
     const int lane = threadIdx.x & 31;
-    const int64_t at = (static_cast<int64_t>(x.q0) + r / p.g) * p.nq + h * p.g + r % p.g;
+    const int64_t at = (static_cast<int64_t>(q0) + r / p.g) * p.nq + h * p.g + r % p.g;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint32_t* to = reinterpret_cast<uint32_t*>(p.out + at * HD);
 #pragma unroll
@@ -330,25 +379,35 @@ __device__ __forceinline__ void write_row(const Params& p, const SeqInfo& x, int
 }
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(Shape<HD, NT>::kThreads, 1) attend_kernel(const Params p) {
+__global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
+    attend_kernel(const Params p) {
     using S = Shape<HD, NT>;
     using T = Tile<HD>;
-    constexpr int R = S::kRows, W = S::kWarps, NG = T::kGroups;
+    constexpr int R = S::kRows, W = S::kWarps, NG = T::kGroups, TT = S::kTiles;
+    constexpr bool RAW = S::kRaw;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
+                                               ~static_cast<uintptr_t>(127));
     Control& ctl = *reinterpret_cast<Control*>(smem);
-    float* sh_o = reinterpret_cast<float*>(smem + 2048);  // [W][R][kOStride]
-    float2* sh_ml = reinterpret_cast<float2*>(smem + 2048 + S::kOBytes);  // [W][R]
+    float* sh_o = reinterpret_cast<float*>(smem + kControlBytes);  // [W][R][kOStride]
+    float2* sh_ml = reinterpret_cast<float2*>(smem + kControlBytes + S::kOBytes);  // [W][R]
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    uint8_t* ring = smem + 2048 + S::kOBytes + S::kMlBytes + warp * S::kSlots * S::kTileBytes;
-    uint64_t* full = ctl.full + warp * 16;
-    int* bad = ctl.bad + warp * 16;
+    uint8_t* ring =
+        smem + kControlBytes + S::kOBytes + S::kMlBytes + warp * S::kSlots * S::kSlotBytes;
+    // Where the warp's copies and its products are in the range (in shared memory: few of the
+    // numbers are needed from tile to tile, and registers are short).
+    static_assert(2 * W * sizeof(Walk<R>) <= kControlBytes - 512, "walks");
+    Walk<R>& ahead = reinterpret_cast<Walk<R>*>(smem + 512)[2 * warp];
+    Walk<R>& walk = reinterpret_cast<Walk<R>*>(smem + 512)[2 * warp + 1];
+    auto advance = [&](Walk<R>& w) {
+        __syncwarp();
+        bool got = false;
+        if (lane == 0) got = w.next(p);
+        return __shfl_sync(0xffffffffu, static_cast<int>(got), 0) != 0;
+    };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < W; ++i)
-            for (int k = 0; k < S::kSlots; ++k) mbar_init(&ctl.full[i * 16 + k], 1);
         mbar_init(&ctl.arrived, W);
         mbar_init(&ctl.merged, W);
         ctl.abort = 0;
@@ -356,56 +415,75 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, 1) attend_kernel(cons
     }
     grid_dependency_wait();
     grid_launch_dependents();
-    find_start<R, S::kThreads>(p, ctl, W);
+    find_start<R, S::kThreads>(p, ctl, TT * W);
     volatile int* abort_flag = &ctl.abort;
 
     // ---- the copies, a ring ahead of the products
-    Walk<R> ahead;
-    ahead.begin(p, ctl.start);
-    bool more = ahead.next(p);
-    int ahead_j = 0;        // the warp's tiles of the piece: warp, warp + W, ...
-    uint32_t issued = 0;
-    int ids = 0;            // lane i: the block of tile 32 b + i of them
+    if (lane == 0) {
+        ahead.begin(p, ctl.start, ctl.seq, ctl.view);
+        walk.begin(p, ctl.start, ctl.seq, ctl.view);
+    }
+    bool more = advance(ahead);
+    int ahead_n = ahead.n;
+    int ahead_k = TT * warp;  // the warp's tiles of the piece: TT of every TT W
+    int ahead_j = 0;          // how many of them are issued
+    int fill = 0;             // slot of the next copy
+    uint32_t there = 0;       // bit TT * slot + k: the slot's tile k is there to be seen
+    int64_t places = 0;       // lane i: where the i-th next of them lies, or -1
     auto issue = [&]() {
-        while (more && warp + ahead_j * W >= ahead.n) {
-            more = ahead.next(p);
+        while (more && ahead_k >= ahead_n) {
+            more = advance(ahead);
+            ahead_n = ahead.n;
+            ahead_k = TT * warp;
             ahead_j = 0;
         }
-        if (!more) return;
-        if (ahead_j % 32 == 0) {
-            const int k = warp + (ahead_j + lane) * W;
-            if (k < ahead.n)
-                ids = __ldg(p.table + ahead.x.e0 + ahead.v.tile(ahead.k + k) * 16 / p.bs);
-        }
-        const int id = __shfl_sync(0xffffffffu, ids, ahead_j % 32);
-        if (lane == 0) {
-            const int slot = static_cast<int>(issued % S::kSlots);
-            const bool good = id >= 0 && id < p.max_blocks;
-            bad[slot] = !good;
-            if (good) {
-                const int pos = ahead.v.tile(ahead.k + warp + ahead_j * W) * 16;
-                const int64_t at = (static_cast<int64_t>(id) * p.nkv + ahead.h) * (p.bs / 16) +
-                                   pos % p.bs / 16;
-                mbar_arrive_expect_tx(&full[slot], T::kBytes);
-                bulk_copy_g2s(ring + slot * T::kBytes, p.cache + at * T::kBytes, T::kBytes,
-                              &full[slot]);
-            } else {
-                raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
-                mbar_arrive(&full[slot]);
+        if (more) {
+            if (ahead_j % 32 == 0) {
+                const int k = ahead_k + lane / TT * (TT * W) + lane % TT;
+                places = -1;
+                if (k < ahead_n) {
+                    const int pos = ahead.v.tile(ahead.k + k) * 16;
+                    const int entry = pos / p.bs;
+                    const int id = __ldg(p.table + ahead.x.e0 + entry);
+                    if (id >= 0 && id < p.max_blocks)
+                        places = ((static_cast<int64_t>(id) * p.nkv + ahead.h) * (p.bs / 16) +
+                                  (pos - entry * p.bs) / 16) * T::kBytes;
+                    else
+                        raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
+                }
             }
+            uint32_t have = 0;
+#pragma unroll
+            for (int u = 0; u < TT; ++u) {
+                const int64_t place = __shfl_sync(0xffffffffu, places, ahead_j % 32 + u);
+                if (place < 0) continue;
+                have |= 1u << u;
+                const uint8_t* from = p.cache + place + 16 * lane;
+                uint8_t* to = ring + fill * S::kSlotBytes + u * T::kBytes + 16 * lane;
+#pragma unroll
+                for (int i = 0; i < T::kBytes; i += 512)
+                    if (i + 512 <= T::kBytes || i + 16 * lane < T::kBytes)
+                        cp_async_16(to + i, from + i);
+            }
+            there = (there & ~(((1u << TT) - 1) << (TT * fill))) | have << (TT * fill);
+            fill = fill + 1 == S::kSlots ? 0 : fill + 1;
+            ahead_j += TT;
+            ahead_k += TT * W;
         }
-        ++issued;
-        ++ahead_j;
+        cp_async_commit();  // (a group for every step, be it empty)
     };
     for (int i = 0; i < S::kSlots; ++i) issue();
 
     // ---- the products
-    Walk<R> walk;
-    walk.begin(p, ctl.start);
-    uint32_t used = 0, pieces = 0;
+    uint32_t pieces = 0;
+    int slot = 0;
     bool ok = true;
-    while (ok && walk.next(p)) {
+    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const uint32_t eight_k[4] = {kMinus8, kMinus8, kMinus128, kMinus128};
+    while (ok && advance(walk)) {
         const View& v = walk.v;
+        const int tiles = walk.n, sinks = v.sinks, k_first = walk.k, w0 = v.w0 - sinks;
+        const int tokens = walk.x.tokens;
         // Q as the second operand of the first product: column g of n-tile i is row 8 i + g.
         uint32_t q[NT][NG][4];
 #pragma unroll
@@ -424,15 +502,63 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, 1) attend_kernel(cons
                 q[i][G][3] = __byte_perm(u.y, u.w, 0x7632);  // 3, 7
             }
         }
+        // What a sum of products times scales is multiplied with, of rows 2 c and 2 c + 1.
+        float factor[NT][2];
+        float first[RAW ? NG : 1][4];  // what the sums begin with
+        if constexpr (RAW) {
+            // A row times 2^n, so that its largest element lies at 2^119: products with steps of
+            // 2^-133 are then ordinary numbers.
+            uint32_t most = 0;
+#pragma unroll
+            for (int G = 0; G < NG; ++G)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) most = __vmaxu2(most, q[0][G][k] & 0x7FFF7FFFu);
+            most = max(most & 0xFFFFu, most >> 16);
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            const int n = 246 - max(static_cast<int>(most >> 7), 1);
+            const int n1 = min(n, 120), n2 = n - n1;
+#pragma unroll
+            for (int G = 0; G < NG; ++G) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    q[0][G][k] = times2(times2(q[0][G][k], pow2(n1)),
+                                        pow2(n2 - (k & 1 ? 4 : 0)));
+                float d[4];
+                mma(d, eight_k, q[0][G][0], q[0][G][1], zero);
+                mma(first[G], eight_k, q[0][G][2], q[0][G][3], d);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int m = 133 - __shfl_sync(0xffffffffu, n, 4 * (2 * c + e));
+                factor[0][e] = p.c * pow2(min(m, 127)) * pow2(max(m - 127, 0));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+#pragma unroll
+                for (int G = 0; G < NG; ++G) {
+                    q[i][G][1] = times2(q[i][G][1], 0.0625f);  // (as codes_of has them)
+                    q[i][G][3] = times2(q[i][G][3], 0.0625f);
+                }
+                factor[i][0] = factor[i][1] = p.c * 64.0f;
+            }
+        }
+        const int open_end = min(v.at0, tokens - 1) - 15;  // the last open tile's position
+        const int window_end = v.at1 - p.window;
         int at[NT][2];  // positions of rows 8 i + 2 c and the next
-        float m[NT][2], l[NT][2], o[NT][HD / 16][4];
+        // The maximum of a row that its weights go by (0 before there is one), and the score that
+        // moves it.
+        float base[NT][2], limit[NT][2];
+        float l[NT][2], o[NT][HD / 16][4];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * i + 2 * c + e;
                 at[i][e] = r < v.live ? walk.x.ctx + (v.r0 + r) / p.g : -1;
-                m[i][e] = -INFINITY;
+                base[i][e] = 0.0f;
+                limit[i][e] = -INFINITY;
                 l[i][e] = 0.0f;
             }
 #pragma unroll
@@ -440,91 +566,109 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, 1) attend_kernel(cons
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][d][e] = 0.0f;
         }
-        for (int j = warp; j < walk.n; j += W) {
-            const int slot = static_cast<int>(used % S::kSlots);
-            ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (used / S::kSlots) & 1)) != 0;
-            if (!ok) break;
-            ++used;
-            const uint8_t* tile = ring + slot * T::kBytes;
-            const int p0 = v.tile(walk.k + j) * 16;
-            if (*(volatile int*)&bad[slot] == 0) {
+        // A slot's tiles, at positions p0[]; OPEN: every row sees all of them.
+        auto step = [&](const uint8_t* slot_at, const int* p0, int have, auto open_tag) {
+            constexpr bool OPEN = decltype(open_tag)::value;
+            // Scores: token g and rows 2 c, 2 c + 1; token g + 8 and the same.
+            float s[TT][NT][4];
+#pragma unroll
+            for (int u = 0; u < TT; ++u) {
+                const uint8_t* tile = slot_at + u * T::kBytes;
                 uint32_t k0[NG], k1[NG], ks0[NG / 2], ks1[NG / 2];
                 load_words(k0, tile + g * (HD / 2) + c * 4 * NG);
                 load_words(k1, tile + (g + 8) * (HD / 2) + c * 4 * NG);
                 load_words(ks0, tile + key_scale<HD>(0, 0) + g * 2 * NG);
                 load_words(ks1, tile + key_scale<HD>(8, 0) + g * 2 * NG);
-                // Scores: token g and rows 2 c, 2 c + 1; token g + 8 and the same.
-                float s[NT][4];
 #pragma unroll
                 for (int G = 0; G < NG; ++G) {
-                    const uint32_t a0[4] = {two_codes(k0[G], 0), two_codes(k1[G], 0),
-                                            two_codes(k0[G], 1), two_codes(k1[G], 1)};
-                    const uint32_t a1[4] = {two_codes(k0[G], 2), two_codes(k1[G], 2),
-                                            two_codes(k0[G], 3), two_codes(k1[G], 3)};
-                    const float x0 = scale_at(ks0, G) * p.c, x1 = scale_at(ks1, G) * p.c;
+                    uint32_t x0[4], x1[4];
+                    if constexpr (RAW) {
+                        raw_codes(x0, k0[G]);
+                        raw_codes(x1, k1[G]);
+                    } else {
+                        codes_of(x0, k0[G]);
+                        codes_of(x1, k1[G]);
+                    }
+                    const uint32_t a0[4] = {x0[0], x1[0], x0[1], x1[1]};
+                    const uint32_t a1[4] = {x0[2], x1[2], x0[3], x1[3]};
+                    const float f0 = scale_at(ks0, G), f1 = scale_at(ks1, G);
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma(d, a0, q[i][G][0], q[i][G][1]);
-                        mma(d, a1, q[i][G][2], q[i][G][3]);
-                        s[i][0] = G == 0 ? d[0] * x0 : fmaf(d[0], x0, s[i][0]);
-                        s[i][1] = G == 0 ? d[1] * x0 : fmaf(d[1], x0, s[i][1]);
-                        s[i][2] = G == 0 ? d[2] * x1 : fmaf(d[2], x1, s[i][2]);
-                        s[i][3] = G == 0 ? d[3] * x1 : fmaf(d[3], x1, s[i][3]);
+                        float d0[4], d[4];
+                        if constexpr (RAW)
+                            mma(d0, a0, q[i][G][0], q[i][G][1], first[G]);
+                        else
+                            mma(d0, a0, q[i][G][0], q[i][G][1], zero);
+                        mma(d, a1, q[i][G][2], q[i][G][3], d0);
+                        s[u][i][0] = G == 0 ? d[0] * f0 : fmaf(d[0], f0, s[u][i][0]);
+                        s[u][i][1] = G == 0 ? d[1] * f0 : fmaf(d[1], f0, s[u][i][1]);
+                        s[u][i][2] = G == 0 ? d[2] * f1 : fmaf(d[2], f1, s[u][i][2]);
+                        s[u][i][3] = G == 0 ? d[3] * f1 : fmaf(d[3], f1, s[u][i][3]);
                     }
                 }
-                // What a row does not see goes to -inf, and its weight below to a plain 0.
-                const bool open = p0 + 15 <= v.at0 && p0 + 15 < walk.x.tokens &&
-                                  (p0 + 15 < p.sinks || p0 > v.at1 - p.window);
-                uint32_t hidden = 0;  // bit 4 i + e: s[i][e]
-                if (!open) {
+            }
+            // What a row does not see goes to -inf, and its weight below to a plain 0.
+            uint32_t hidden = 0;  // bit 4 (NT u + i) + e: s[u][i][e]
+            bool grow = false;
+            float top[NT][2];
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int pos = p0 + g + 8 * (e >> 1), own = at[i][e & 1];
-                            const bool see = pos <= own && pos < walk.x.tokens &&
+                for (int u = 0; u < TT; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[u][i][e] *= factor[i][e & 1];
+                        if constexpr (!OPEN) {
+                            const int pos = p0[u] + g + 8 * (e >> 1), own = at[i][e & 1];
+                            const bool see = ((have >> u) & 1) && pos <= own && pos < tokens &&
                                              (pos < p.sinks || pos > own - p.window);
                             if (!see) {
-                                s[i][e] = -INFINITY;
-                                hidden |= 1u << (4 * i + e);
+                                s[u][i][e] = -INFINITY;
+                                hidden |= 1u << (4 * (NT * u + i) + e);
                             }
                         }
+                    }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    top[i][e] = fmaxf(s[0][i][e], s[0][i][e + 2]);
+                    if constexpr (TT == 2)
+                        top[i][e] = fmaxf(top[i][e], fmaxf(s[TT - 1][i][e], s[TT - 1][i][e + 2]));
+                    grow |= top[i][e] > limit[i][e];
                 }
-                bool grow = false;
+            }
+            if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        grow |= fmaxf(s[i][e], s[i][e + 2]) > m[i][e] + kLazy;
-                if (__any_sync(0xffffffffu, grow)) {
+                    for (int e = 0; e < 2; ++e) {
+                        float t = top[i][e];
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
+                        for (int k = 4; k < 32; k <<= 1)
+                            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, k));
+                        // (the same for all lanes of the row; the limit is -inf before any score)
+                        const bool none = limit[i][e] == -INFINITY;
+                        if (t > (none ? -INFINITY : base[i][e])) {
+                            const float shrink = none ? 0.0f : ex2(base[i][e] - t);
+                            l[i][e] *= shrink;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float top = fmaxf(s[i][e], s[i][e + 2]);
-#pragma unroll
-                            for (int k = 4; k < 32; k <<= 1)
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-                            if (top > m[i][e]) {  // (the same for all lanes of the row)
-                                const float shrink = ex2(m[i][e] - top);
-                                l[i][e] *= shrink;
-#pragma unroll
-                                for (int d = 0; d < HD / 16; ++d) {
-                                    o[i][d][e] *= shrink;
-                                    o[i][d][e + 2] *= shrink;
-                                }
-                                m[i][e] = top;
+                            for (int d = 0; d < HD / 16; ++d) {
+                                o[i][d][e] *= shrink;
+                                o[i][d][e + 2] *= shrink;
                             }
+                            base[i][e] = t;
+                            limit[i][e] = t + kLazy;
                         }
-                }
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < TT; ++u) {
+                const uint8_t* tile = slot_at + u * T::kBytes;
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float base = m[i][e & 1] == -INFINITY ? 0.0f : m[i][e & 1];
-                        s[i][e] = ex2(s[i][e] - base);
-                        l[i][e & 1] += s[i][e];
+                        s[u][i][e] = ex2(s[u][i][e] - base[i][e & 1]);
+                        l[i][e & 1] += s[u][i][e];
                     }
                 uint32_t vs0[NG / 2], vs1[NG / 2];
                 load_words(vs0, tile + value_scale<HD>(0, 0) + g * 2 * NG);
@@ -534,15 +678,16 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, 1) attend_kernel(cons
                     // A group's weights: the token's weight by its scale, rounded to bf16 because
                     // both operands of a product have one type (an output is off by up to
                     // 2^-9 sum p |v| for it), rows over tokens turned to tokens over rows.
-                    const float x0 = scale_at(vs0, G), x1 = scale_at(vs1, G);
+                    const float f0 = scale_at(vs0, G), f1 = scale_at(vs1, G);
                     uint32_t b[NT][2];
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        float y[4] = {s[i][0] * x0, s[i][1] * x0, s[i][2] * x1, s[i][3] * x1};
-                        if (!open) {  // (a hidden token's scale may be anything)
+                        float y[4] = {s[u][i][0] * f0, s[u][i][1] * f0, s[u][i][2] * f1,
+                                      s[u][i][3] * f1};
+                        if constexpr (!OPEN) {  // (a hidden token's scale may be anything)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if ((hidden >> (4 * i + e)) & 1) y[e] = 0.0f;
+                                if ((hidden >> (4 * (NT * u + i) + e)) & 1) y[e] = 0.0f;
                         }
                         b[i][0] = transpose8x8(pack_bf16x2(y[0], y[1]));
                         b[i][1] = transpose8x8(pack_bf16x2(y[2], y[3]));
@@ -552,18 +697,39 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, 1) attend_kernel(cons
                         tile + T::kCodes + (G / 2 * 32 + lane) * 16 + G % 2 * 8);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t word = h ? w.y : w.x;
-                        const uint32_t a[4] = {two_codes(word, 0), two_codes(word, 1),
-                                               two_codes(word, 2), two_codes(word, 3)};
+                        uint32_t a[4];
+                        codes_of(a, h ? w.y : w.x);
 #pragma unroll
-                        for (int i = 0; i < NT; ++i) mma(o[i][2 * G + h], a, b[i][0], b[i][1]);
+                        for (int i = 0; i < NT; ++i)
+                            mma(o[i][2 * G + h], a, b[i][0], b[i][1], o[i][2 * G + h]);
                     }
                 }
             }
+        };
+        // Steps from open0 on, up to open1, are seen whole by every row: tiles behind the sinks'
+        // whose tokens come after the last row's window begins and not after the first row.
+        const int open0 = max(sinks, window_end < 0 ? 0 : window_end / 16 + 1 - w0) - k_first;
+        const int open1 = min((open_end < 0 ? 0 : open_end / 16 + 1) - w0 - k_first, tiles) - TT + 1;
+        for (int j = TT * warp; j < tiles; j += TT * W) {
+            cp_async_wait_group<S::kSlots - 1>();
+            __syncwarp();  // every lane's copies are there
+            const uint8_t* slot_at = ring + slot * S::kSlotBytes;
+            const int have = static_cast<int>(there >> (TT * slot)) & ((1 << TT) - 1);
+            int p0[TT];
+            if (j >= open0 && j < open1 && have == (1 << TT) - 1) {
+                step(slot_at, p0, have, std::true_type{});
+            } else if (have != 0) {
+#pragma unroll
+                for (int u = 0; u < TT; ++u) {
+                    const int k = k_first + j + u;
+                    p0[u] = (k < sinks ? k : w0 + k) * 16;
+                }
+                step(slot_at, p0, have, std::false_type{});
+            }
             __syncwarp();  // the slot has been read
             issue();
+            slot = slot + 1 == S::kSlots ? 0 : slot + 1;
         }
-        if (!ok) break;
 
         // ---- the piece's end: the warps put together what they have
 #pragma unroll
@@ -578,18 +744,21 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, 1) attend_kernel(cons
             if (!ok) break;
         }
         float* mine = sh_o + warp * R * S::kOStride;
-        const bool some = walk.n > warp;  // else O is not looked at
+        const bool some = walk.n > TT * warp;  // else O is not looked at
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * i + 2 * c + e;
-                if (g == 0) sh_ml[warp * R + r] = make_float2(m[i][e], l[i][e]);
+                if (g == 0) sh_ml[warp * R + r] = make_float2(base[i][e], l[i][e]);
                 if (some && r < v.live) {
 #pragma unroll
                     for (int d = 0; d < HD / 16; ++d) {
-                        mine[r * S::kOStride + 16 * d + g] = o[i][d][e];
-                        mine[r * S::kOStride + 16 * d + g + 8] = o[i][d][e + 2];
+                        // (codes_of divides by 64 and 4)
+                        mine[r * S::kOStride + 16 * d + g] =
+                            o[i][d][e] * 64.0f;
+                        mine[r * S::kOStride + 16 * d + g + 8] =
+                            o[i][d][e + 2] * 4.0f;
                     }
                 }
             }
@@ -604,14 +773,14 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, 1) attend_kernel(cons
                 const float2 ml = sh_ml[w * R + r];
                 if (ml.y != 0.0f) top = fmaxf(top, ml.x);
             }
-            const float base = top == -INFINITY ? 0.0f : top;
+            const float top_or_0 = top == -INFINITY ? 0.0f : top;
             float2 acc[HD / 64];
 #pragma unroll
             for (int i = 0; i < HD / 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
             for (int w = 0; w < W; ++w) {
                 const float2 ml = sh_ml[w * R + r];
                 if (ml.y == 0.0f) continue;
-                const float wt = ex2(ml.x - base);
+                const float wt = ex2(ml.x - top_or_0);
                 sum = fmaf(wt, ml.y, sum);
                 const float* from = sh_o + (w * R + r) * S::kOStride;
 #pragma unroll
@@ -622,7 +791,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, 1) attend_kernel(cons
                 }
             }
             if (walk.whole) {
-                write_row<HD>(p, walk.x, v.r0 + r, walk.h, base, sum, acc);
+                write_row<HD>(p, walk.x.q0, v.r0 + r, walk.h, top_or_0, sum, acc);
             } else {
                 float* to = p.part_o + (part * R + r) * HD;
 #pragma unroll
@@ -640,65 +809,123 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, 1) attend_kernel(cons
             raise_error(p.dev_status, p.lib_error, HSS_ERR_DEVICE_TIMEOUT);
         *abort_flag = 1;
     }
-    // Nobody leaves before its copies have landed.
-    for (; used < issued; ++used)
-        (void)mbar_wait_for(&full[used % S::kSlots], (used / S::kSlots) & 1, 1000000);
+    cp_async_wait_group<0>();  // nobody leaves before its copies have landed
     __syncthreads();
 }
 
-// Joins the pieces of the units that were cut: CTA x looks at the cut before range x + 1, and takes
-// the unit there if this is its first cut.  A warp takes a row.
+// Joins the pieces of the units that were cut: CTA (x, y) looks at the cut before range x + 1, takes
+// the unit there if this is its first cut, and of it eight rows.  A long sequence is cut into as
+// many pieces as there are ranges to share it, so what costs is the way of their loads: a warp a
+// row finds the pieces' weights, while four elements of a row to a thread and a share of the pieces
+// are on their way already, a dozen pieces at a time.
+constexpr int kJoinThreads = 512;
+constexpr int kJoinPieces = 128;
+
 template <int HD, int NT>
-__global__ void __launch_bounds__(256) join_kernel(const Params p) {
-    constexpr int R = 8 * NT;
+__global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const Params p) {
+    constexpr int R = 8 * NT, V = HD / 4, kAtOnce = 12;
+    static_assert(8 * V <= kJoinThreads, "an element's thread");
+    __shared__ float weight[8][kJoinPieces];
+    __shared__ float shrink[8], top_of[8], sum_of[8];
+    __shared__ float4 parts[kJoinThreads];
     grid_dependency_wait();
     grid_launch_dependents();
     const int range = blockIdx.x + 1;
     const Start st = p.starts[range];
-    if (st.t == 0) return;
+    const int rows = min(st.live - 8 * static_cast<int>(blockIdx.y), 8);
+    if (st.t == 0 || rows <= 0) return;
     const int64_t f = range * st.per - st.t;  // the unit's first tile
-    if (f / st.per != range - 1) return;
-    const int last = static_cast<int>((f + st.cost - 1) / st.per);
-    const int count = last - range + 2;
-    const SeqInfo x = load_seq(p, st.s);
-    const View v = view_of<R>(p, x, st.rt);
-    const int lane = threadIdx.x & 31;
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (r >= v.live) return;
+    if (divide(f, st.per) != range - 1) return;
+    const int count = static_cast<int>(divide(f + st.cost - 1, st.per)) - range + 2;
     // piece 0 is the end of range - 1, piece k the beginning of range + k - 1
-    auto part = [&](int k) -> int64_t {
-        return (k == 0 ? 2 * (range - 1) + 1 : 2 * (range + k - 1)) * static_cast<int64_t>(R) + r;
+    auto part = [&](int k, int r) -> int64_t {
+        return (k == 0 ? 2 * (range - 1) + 1 : 2 * (range + k - 1)) * static_cast<int64_t>(R) +
+               8 * blockIdx.y + r;
     };
-    float top = -INFINITY;
-    for (int k = lane; k < count; k += 32) {
-        const float2 ml = p.part_ml[part(k)];
-        if (ml.y != 0.0f) top = fmaxf(top, ml.x);
-    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int shares = kJoinThreads / (rows * V);
+    const int share = threadIdx.x / (rows * V), at = threadIdx.x % (rows * V);
+    const int row = at / V, col = at % V * 4;
+    float4 v[kAtOnce], acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto fetch = [&](int k0, int end) {
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-    float2 acc[HD / 64];
-#pragma unroll
-    for (int i = 0; i < HD / 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-    for (int k = 0; k < count; ++k) {
-        const float2 ml = p.part_ml[part(k)];
-        const float wt = ml.y != 0.0f ? ex2(ml.x - base) : 0.0f;
-        const float* from = p.part_o + part(k) * HD;
-        float2 y[HD / 64];
-#pragma unroll
-        for (int i = 0; i < HD / 64; ++i)
-            y[i] = *reinterpret_cast<const float2*>(from + 2 * lane + 64 * i);
-        if (ml.y == 0.0f) continue;
-        sum = fmaf(wt, ml.y, sum);
-#pragma unroll
-        for (int i = 0; i < HD / 64; ++i) {
-            acc[i].x = fmaf(wt, y[i].x, acc[i].x);
-            acc[i].y = fmaf(wt, y[i].y, acc[i].y);
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int k = k0 + i * shares;
+            if (share < shares && k < end)
+                v[i] = *reinterpret_cast<const float4*>(p.part_o + part(k, row) * HD + col);
         }
+    };
+    float top = -INFINITY, sum = 0.0f;  // of the warp's row
+    for (int c0 = 0; c0 < count; c0 += kJoinPieces) {
+        const int end = min(count, c0 + kJoinPieces);
+        fetch(c0 + share, end);
+        if (warp < rows) {
+            float2 ml[kJoinPieces / 32];
+            float most = top;
+#pragma unroll
+            for (int i = 0; i < kJoinPieces / 32; ++i) {
+                const int k = c0 + 32 * i + lane;
+                ml[i] = k < end ? p.part_ml[part(k, warp)] : make_float2(0.0f, 0.0f);
+                if (ml[i].y != 0.0f) most = fmaxf(most, ml[i].x);
+            }
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1)
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
+            const float base = most == -INFINITY ? 0.0f : most;
+            const float less = top == -INFINITY ? 0.0f : ex2(top - base);
+            float here = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kJoinPieces / 32; ++i) {
+                const float w = ml[i].y != 0.0f ? ex2(ml[i].x - base) : 0.0f;
+                if (ml[i].y != 0.0f) here = fmaf(w, ml[i].y, here);
+                weight[warp][32 * i + lane] = w;
+            }
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) here += __shfl_xor_sync(0xffffffffu, here, m);
+            sum = fmaf(sum, less, here);
+            top = most;
+            if (lane == 0) {
+                shrink[warp] = less;
+                top_of[warp] = base;
+                sum_of[warp] = sum;
+            }
+        }
+        __syncthreads();
+        if (share < shares) {
+            const float less = shrink[row];
+            acc.x *= less, acc.y *= less, acc.z *= less, acc.w *= less;
+            for (int k0 = c0 + share; k0 < end; k0 += kAtOnce * shares) {
+                if (k0 != c0 + share) fetch(k0, end);
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const int k = k0 + i * shares;
+                    if (k >= end) break;
+                    const float w = weight[row][k - c0];
+                    acc.x = fmaf(w, v[i].x, acc.x);
+                    acc.y = fmaf(w, v[i].y, acc.y);
+                    acc.z = fmaf(w, v[i].z, acc.z);
+                    acc.w = fmaf(w, v[i].w, acc.w);
+                }
+            }
+        }
+        __syncthreads();
     }
-    write_row<HD>(p, x, v.r0 + r, st.h, base, sum, acc);
+    parts[threadIdx.x] = acc;
+    __syncthreads();
+    if (share != 0) return;
+    for (int k = 1; k < shares; ++k) {
+        const float4 o = parts[threadIdx.x + k * rows * V];
+        acc.x += o.x, acc.y += o.y, acc.z += o.z, acc.w += o.w;
+    }
+    const float l = sum_of[row], inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int r = st.r0 + 8 * static_cast<int>(blockIdx.y) + row;
+    const int64_t to = (static_cast<int64_t>(st.q0) + r / p.g) * p.nq + st.h * p.g + r % p.g;
+    uint2 u = make_uint2(0, 0);
+    if (l != 0.0f)
+        u = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    *reinterpret_cast<uint2*>(p.out + to * HD + col) = u;
+    if (col == 0 && p.lse != nullptr)
+        p.lse[to] = l == 0.0f ? -INFINITY : (top_of[row] + log2f(l)) * 0.693147180559945309f;
 }
 
 template <int HD, int NT>
@@ -708,9 +935,9 @@ hss_status launch_rows(const Params& p, cudaStream_t stream) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes) !=
         cudaSuccess)
         return HSS_ERR_CUDA;
-    if (launch_pdl(kern, dim3(kGrid), dim3(S::kThreads), S::kSmemBytes, stream, p) != cudaSuccess)
+    if (launch_pdl(kern, dim3(S::kRanges), dim3(S::kThreads), S::kSmemBytes, stream, p) != cudaSuccess)
         return HSS_ERR_CUDA;
-    if (launch_pdl(join_kernel<HD, NT>, dim3(kGrid - 1, NT), dim3(256), 0, stream, p) !=
+    if (launch_pdl(join_kernel<HD, NT>, dim3(S::kRanges - 1, NT), dim3(kJoinThreads), 0, stream, p) !=
         cudaSuccess)
         return HSS_ERR_CUDA;
     return HSS_OK;

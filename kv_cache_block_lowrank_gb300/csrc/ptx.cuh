@@ -45,6 +45,15 @@ __device__ __forceinline__ void cp_async_4(void* smem_dst, const void* gmem_src)
                  : "memory");
 }
 
+// Groups of a thread's copies, and the wait until at most N of the latest are on their way.
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ void cp_async_wait_all() {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
