@@ -20,7 +20,7 @@ SOURCES = ["hss_api.cu", "project_tc.cu", "score_decode.cu", "score_decode_k1.cu
            "attend_packed_64.cu", "attend_packed_128.cu", "attend_packed_192.cu",
            "attend_packed_256.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "rank_device.cuh", "score_decode_kernel.cuh", "packed.cuh",
-           "attend_packed.cuh"]
+           "attend_packed.cuh", "attend_packed_tc.cuh"]
 
 
 def nvcc() -> str:

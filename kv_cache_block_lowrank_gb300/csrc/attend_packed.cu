@@ -6,25 +6,49 @@
 namespace hss {
 namespace {
 
-// Ranges of the list, and their rows, that the workspace has room for.
-constexpr int kRanges = 4 * packed::kSms;
-constexpr int kRangeRows = 8 * kRanges;
+using packed::kSms;
+
+// Ranges of the list of the kernel for few rows, and their rows, that the workspace has room for;
+// the kernel for many has a range an SM, of one or two row tiles of 128.
+constexpr int kRanges = 2 * kSms;
+constexpr int kRangeRows = 16 * kRanges;
+
+// Rows of one sequence and kv head from which on the tensor cores' rows are filled well enough.
+constexpr int64_t kManyRows = 33;
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
-// n-tiles of 8 rows that a CTA takes at once: a tile of the cache is decoded once for all of them,
-// and O takes head_dim / 4 of a thread's registers for each.
-int n_tiles(const hss_dims& d, int64_t max_q) {
-    return max_q * (d.num_q_heads / d.num_kv_heads) <= 8 ? 1 : 2;
+int64_t rows_of(const hss_dims& d, int64_t max_q) {
+    return max_q * (d.num_q_heads / d.num_kv_heads);
 }
+int64_t many_rows(const hss_dims& d) { return d.head_dim <= 128 ? 256 : 128; }
+
+struct Layout {
+    size_t starts, ml, o, flags, many_starts, many_ml, many_o, end;
+    Layout(const hss_dims& d, bool many) {
+        size_t at = 0;
+        auto take = [&](size_t bytes) {
+            const size_t was = at;
+            at += round_up(bytes);
+            return was;
+        };
+        starts = take(kRanges * sizeof(packed::Start));
+        ml = take(2 * kRangeRows * sizeof(float2));
+        o = take(static_cast<size_t>(2 * kRangeRows) * d.head_dim * sizeof(float));
+        flags = take(kSms * sizeof(int32_t));
+        const size_t rows = many ? 2 * kSms * many_rows(d) : 0;
+        many_starts = take(kSms * sizeof(packed::Start));
+        many_ml = take(rows * sizeof(float2));
+        many_o = take(rows * d.head_dim * sizeof(float));
+        end = at;
+    }
+};
 
 }  // namespace
 
-size_t attend_packed_workspace_bytes(const hss_dims& d, int32_t, int32_t, int64_t, int32_t,
+size_t attend_packed_workspace_bytes(const hss_dims& d, int32_t, int32_t max_q, int64_t, int32_t,
                                      int32_t) {
-    return round_up(kRanges * sizeof(packed::Start)) +
-           round_up(2 * kRangeRows * sizeof(float2)) +
-           static_cast<size_t>(2 * kRangeRows) * d.head_dim * sizeof(float);
+    return Layout(d, rows_of(d, max_q) >= kManyRows).end;
 }
 
 hss_status launch_attend_packed(const PackedArgs& a, cudaStream_t stream) {
@@ -48,23 +72,32 @@ hss_status launch_attend_packed(const PackedArgs& a, cudaStream_t stream) {
     p.nkv = x.dims.num_kv_heads;
     p.g = p.nq / p.nkv;
     p.bs = x.dims.block_size;
-    p.window = x.window > 0 ? x.window : 0x7FFFFFFF;
+    p.window = x.window > 0 ? std::min(x.window, 0x7FFFFF00) : 0x7FFFFF00;
     p.sinks = x.window > 0 ? x.sinks : 0;
     p.c = x.scale * 1.44269504088896341f;
+    p.guard = nullptr;
     p.dev_status = x.dev_status;
     p.lib_error = dev->error_word;
+    const int64_t rows = rows_of(x.dims, p.max_q);
+    const bool with_many = rows >= kManyRows;
+    const Layout at(x.dims, with_many);
     uint8_t* w = static_cast<uint8_t*>(x.workspace);
-    p.starts = reinterpret_cast<packed::Start*>(w);
-    w += round_up(kRanges * sizeof(packed::Start));
-    p.part_ml = reinterpret_cast<float2*>(w);
-    w += round_up(2 * kRangeRows * sizeof(float2));
-    p.part_o = reinterpret_cast<float*>(w);
-    const int n = n_tiles(x.dims, p.max_q);
+    p.starts = reinterpret_cast<packed::Start*>(w + at.starts);
+    p.part_ml = reinterpret_cast<float2*>(w + at.ml);
+    p.part_o = reinterpret_cast<float*>(w + at.o);
+    int32_t* flags = reinterpret_cast<int32_t*>(w + at.flags);
+    packed::Params many = p;
+    many.starts = reinterpret_cast<packed::Start*>(w + at.many_starts);
+    many.part_ml = reinterpret_cast<float2*>(w + at.many_ml);
+    many.part_o = reinterpret_cast<float*>(w + at.many_o);
+    if (with_many) p.guard = flags;
+    const packed::Params* m = with_many ? &many : nullptr;
+    const int n = rows <= 8 ? 1 : 2;  // n-tiles of 8 rows that a tile of the cache is decoded for
     switch (x.dims.head_dim) {
-        case 64: return packed::launch_head_dim<64>(p, n, stream);
-        case 128: return packed::launch_head_dim<128>(p, n, stream);
-        case 192: return packed::launch_head_dim<192>(p, n, stream);
-        default: return packed::launch_head_dim<256>(p, n, stream);
+        case 64: return packed::launch_head_dim<64>(p, m, n, flags, stream);
+        case 128: return packed::launch_head_dim<128>(p, m, n, flags, stream);
+        case 192: return packed::launch_head_dim<192>(p, m, n, flags, stream);
+        default: return packed::launch_head_dim<256>(p, m, n, flags, stream);
     }
 }
 

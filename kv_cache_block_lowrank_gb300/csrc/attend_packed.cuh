@@ -28,7 +28,13 @@ namespace packed {
 
 constexpr int kSms = 152;          // GB300's; the workspace does not depend on the device
 constexpr float kLazy = 8.0f;
-constexpr int kMostWarps = 6;
+// In the list a unit is longer than its tiles by what it costs besides (its first loads, the warps'
+// meeting, its rows' way out), so that ranges of equal length take equal time: in tiles here, in
+// jobs of four for many rows.  (None, 8, 16 and 32: 64 sequences of 1k to 16k tokens 160, 156, 151
+// and 143 us; 16 windows of 4093 tokens with an empty sequence among them 62, 54, 41 and 35.)
+template <int UNIT>
+constexpr int kBeside = UNIT == 1 ? 32 : 6;
+constexpr int kScanWarps = 16;
 constexpr int kMostSlots = 4;       // of a warp's ring
 constexpr int kControlBytes = 2048;  // barriers, and from 512 on the warps' walks
 
@@ -51,7 +57,7 @@ struct Params {
     int64_t max_blocks;
     int64_t total_blocks;
     int32_t num_seqs, max_q, nq, nkv, g, bs;
-    int32_t window;  // 0x7FFFFFFF: none
+    int32_t window;  // 0x7FFFFF00 at most, which is none
     int32_t sinks;   // 0 without a window
     float c;         // scale log2(e)
     int32_t* dev_status;
@@ -60,6 +66,7 @@ struct Params {
     Start* starts;    // [ranges]
     float2* part_ml;  // [2 ranges][R] (m, l)
     float* part_o;    // [2 ranges][R][head_dim]
+    const int32_t* guard;  // [kSms] or null: nothing is done if all are 0
 };
 
 template <int HD, int NT>
@@ -113,7 +120,10 @@ struct View {
     int sinks, w0, end;  // tiles
     __device__ __forceinline__ int tiles() const { return sinks + end - w0; }
     // (a row tile that sees nothing still has its result to write)
-    __device__ __forceinline__ int cost() const { return max(tiles(), 1); }
+    template <int UNIT>
+    __device__ __forceinline__ int cost() const {
+        return max((tiles() + UNIT - 1) / UNIT, 1);
+    }
     __device__ __forceinline__ int tile(int k) const { return k < sinks ? k : w0 + (k - sinks); }
 };
 
@@ -143,13 +153,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// The pieces of a CTA's range, one unit (or the range's part of it) after another.
-template <int R>
+// The pieces of a CTA's range, one unit (or the range's part of it) after another; the list counts
+// UNIT tiles as one.
+template <int R, int UNIT>
 struct Walk {
     SeqInfo x;
     View v;
     int s, rt, rts, h;
-    int k, n;  // the piece: tiles [k, k + n) of the unit's view
+    int k, n;  // the piece: tiles [k, k + n) of the unit's view, from UNIT t on
     bool whole;
     int64_t f, f1;
     int t;
@@ -167,36 +178,36 @@ struct Walk {
         rts = row_tiles<R>(p, x);
     }
     __device__ __forceinline__ bool next(const Params& p) {
-        if (f >= f1) return false;
-        // (t is past the unit's end only after a piece)
-        while (t >= v.cost()) {
-            t = 0;
-            if (++h < p.nkv) break;
-            h = 0;
-            if (++rt >= rts) {
-                rt = 0;
-                do {
-                    if (++s >= p.num_seqs) {
-                        f = f1;
-                        return false;
-                    }
-                    x = load_seq(p, s);
-                    rts = row_tiles<R>(p, x);
-                } while (rts == 0);
+        while (f < f1) {
+            const int all = v.cost<UNIT>();
+            if (t < all) {
+                const int take = static_cast<int>(min(static_cast<int64_t>(all - t), f1 - f));
+                k = UNIT * t;
+                n = max(min(UNIT * (t + take), v.tiles()) - k, 0);
+                whole = take == all;
+                t += take;
+                f += take;
+                return true;
             }
-            v = view_of<R>(p, x, rt);
+            f += all + kBeside<UNIT> - t;
+            t = 0;
+            if (++h >= p.nkv) {
+                h = 0;
+                if (++rt >= rts) {
+                    rt = 0;
+                    do {
+                        if (++s >= p.num_seqs) return false;
+                        x = load_seq(p, s);
+                        rts = row_tiles<R>(p, x);
+                    } while (rts == 0);
+                }
+                v = view_of<R>(p, x, rt);
+            }
         }
-        const int take = static_cast<int>(min(static_cast<int64_t>(v.cost() - t), f1 - f));
-        k = t;
-        n = max(min(t + take, v.tiles()) - t, 0);
-        whole = take == v.cost();
-        t += take;
-        f += take;
-        return true;
+        return false;
     }
 };
 
-// D = A B + C
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1, const float (&c)[4]) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
@@ -278,7 +289,7 @@ struct alignas(8) Control {
     Start start;
     SeqInfo seq;  // of the unit where the range begins
     View view;
-    int64_t scan[kMostWarps];
+    int64_t scan[kScanWarps];
 };
 static_assert(sizeof(Control) <= 512, "control block");
 
@@ -289,7 +300,7 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
 }
 
 // Where every CTA's range begins, from a scan of the sequences' lengths.
-template <int R, int THREADS>
+template <int R, int UNIT, int THREADS>
 __device__ __forceinline__ void find_start(const Params& p, Control& ctl, int64_t least) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int each = (p.num_seqs + THREADS - 1) / THREADS;
@@ -298,7 +309,7 @@ __device__ __forceinline__ void find_start(const Params& p, Control& ctl, int64_
     auto length = [&](const SeqInfo& x) -> int64_t {
         const int n = row_tiles<R>(p, x);
         int64_t sum = 0;
-        for (int rt = 0; rt < n; ++rt) sum += view_of<R>(p, x, rt).cost();
+        for (int rt = 0; rt < n; ++rt) sum += view_of<R>(p, x, rt).template cost<UNIT>() + kBeside<UNIT>;
         return sum * p.nkv;
     };
     int64_t mine = 0;
@@ -339,18 +350,17 @@ __device__ __forceinline__ void find_start(const Params& p, Control& ctl, int64_
         if (before <= f0 && f0 < before + n) {
             int64_t o = f0 - before;
             int rt = 0;
-            int64_t cost = view_of<R>(p, x, 0).cost();
-            while (o >= cost * p.nkv) {
-                o -= cost * p.nkv;
-                cost = view_of<R>(p, x, ++rt).cost();
+            View v = view_of<R>(p, x, 0);
+            while (o >= static_cast<int64_t>(v.cost<UNIT>() + kBeside<UNIT>) * p.nkv) {
+                o -= static_cast<int64_t>(v.cost<UNIT>() + kBeside<UNIT>) * p.nkv;
+                v = view_of<R>(p, x, ++rt);
             }
+            const int64_t h = divide(o, v.cost<UNIT>() + kBeside<UNIT>);
             ctl.start.s = s;
             ctl.start.rt = rt;
-            const int64_t h = divide(o, cost);
             ctl.start.h = static_cast<int>(h);
-            ctl.start.t = o - h * cost;
-            ctl.start.cost = cost;
-            const View v = view_of<R>(p, x, rt);
+            ctl.start.t = o - h * (v.cost<UNIT>() + kBeside<UNIT>);
+            ctl.start.cost = v.cost<UNIT>();
             ctl.start.q0 = x.q0;
             ctl.start.r0 = v.r0;
             ctl.start.live = v.live;
@@ -361,6 +371,14 @@ __device__ __forceinline__ void find_start(const Params& p, Control& ctl, int64_
     }
     __syncthreads();
     if (threadIdx.x == 0) p.starts[blockIdx.x] = ctl.start;
+}
+
+// Whether the kernel has something to do (see Params::guard).
+__device__ __forceinline__ bool wanted(const Params& p) {
+    if (p.guard == nullptr) return true;
+    int any = 0;
+    for (int i = threadIdx.x; i < kSms; i += blockDim.x) any |= p.guard[i];
+    return __syncthreads_or(any) != 0;
 }
 
 // A finished row: out and lse.
@@ -397,13 +415,14 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
         smem + kControlBytes + S::kOBytes + S::kMlBytes + warp * S::kSlots * S::kSlotBytes;
     // Where the warp's copies and its products are in the range (in shared memory: few of the
     // numbers are needed from tile to tile, and registers are short).
-    static_assert(2 * W * sizeof(Walk<R>) <= kControlBytes - 512, "walks");
-    Walk<R>& ahead = reinterpret_cast<Walk<R>*>(smem + 512)[2 * warp];
-    Walk<R>& walk = reinterpret_cast<Walk<R>*>(smem + 512)[2 * warp + 1];
-    auto advance = [&](Walk<R>& w) {
+    static_assert(2 * W * sizeof(Walk<R, 1>) <= kControlBytes - 512, "walks");
+    Walk<R, 1>& ahead = reinterpret_cast<Walk<R, 1>*>(smem + 512)[2 * warp];
+    Walk<R, 1>& walk = reinterpret_cast<Walk<R, 1>*>(smem + 512)[2 * warp + 1];
+    auto advance = [&](Walk<R, 1>& w) {
         __syncwarp();
         bool got = false;
         if (lane == 0) got = w.next(p);
+        __syncwarp();
         return __shfl_sync(0xffffffffu, static_cast<int>(got), 0) != 0;
     };
 
@@ -415,7 +434,8 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
     }
     grid_dependency_wait();
     grid_launch_dependents();
-    find_start<R, S::kThreads>(p, ctl, TT * W);
+    if (!wanted(p)) return;
+    find_start<R, 1, S::kThreads>(p, ctl, TT * W);
     volatile int* abort_flag = &ctl.abort;
 
     // ---- the copies, a ring ahead of the products
@@ -814,118 +834,124 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
 }
 
 // Joins the pieces of the units that were cut: CTA (x, y) looks at the cut before range x + 1, takes
-// the unit there if this is its first cut, and of it eight rows.  A long sequence is cut into as
+// the unit there if this is its first cut, and of it every gridDim.y-th eight rows.  A long sequence is cut into as
 // many pieces as there are ranges to share it, so what costs is the way of their loads: a warp a
 // row finds the pieces' weights, while four elements of a row to a thread and a share of the pieces
 // are on their way already, a dozen pieces at a time.
 constexpr int kJoinThreads = 512;
 constexpr int kJoinPieces = 128;
 
-template <int HD, int NT>
+template <int HD, int R>
 __global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const Params p) {
-    constexpr int R = 8 * NT, V = HD / 4, kAtOnce = 12;
+    constexpr int V = HD / 4, kAtOnce = 12;
     static_assert(8 * V <= kJoinThreads, "an element's thread");
     __shared__ float weight[8][kJoinPieces];
     __shared__ float shrink[8], top_of[8], sum_of[8];
     __shared__ float4 parts[kJoinThreads];
     grid_dependency_wait();
     grid_launch_dependents();
+    if (!wanted(p)) return;
     const int range = blockIdx.x + 1;
     const Start st = p.starts[range];
-    const int rows = min(st.live - 8 * static_cast<int>(blockIdx.y), 8);
-    if (st.t == 0 || rows <= 0) return;
+    if (st.t == 0 || st.t >= st.cost) return;  // (no cut, or behind the tiles)
     const int64_t f = range * st.per - st.t;  // the unit's first tile
     if (divide(f, st.per) != range - 1) return;
     const int count = static_cast<int>(divide(f + st.cost - 1, st.per)) - range + 2;
-    // piece 0 is the end of range - 1, piece k the beginning of range + k - 1
-    auto part = [&](int k, int r) -> int64_t {
-        return (k == 0 ? 2 * (range - 1) + 1 : 2 * (range + k - 1)) * static_cast<int64_t>(R) +
-               8 * blockIdx.y + r;
-    };
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int shares = kJoinThreads / (rows * V);
-    const int share = threadIdx.x / (rows * V), at = threadIdx.x % (rows * V);
-    const int row = at / V, col = at % V * 4;
-    float4 v[kAtOnce], acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto fetch = [&](int k0, int end) {
+    for (int r0 = 8 * blockIdx.y; r0 < st.live; r0 += 8 * gridDim.y) {
+        const int rows = min(st.live - r0, 8);
+        // piece 0 is the end of range - 1, piece k the beginning of range + k - 1
+        auto part = [&](int k, int r) -> int64_t {
+            return (k == 0 ? 2 * (range - 1) + 1 : 2 * (range + k - 1)) * static_cast<int64_t>(R) +
+                   r0 + r;
+        };
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int shares = kJoinThreads / (rows * V);
+        const int share = threadIdx.x / (rows * V), at = threadIdx.x % (rows * V);
+        const int row = at / V, col = at % V * 4;
+        float4 v[kAtOnce], acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        auto fetch = [&](int k0, int end) {
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const int k = k0 + i * shares;
-            if (share < shares && k < end)
-                v[i] = *reinterpret_cast<const float4*>(p.part_o + part(k, row) * HD + col);
-        }
-    };
-    float top = -INFINITY, sum = 0.0f;  // of the warp's row
-    for (int c0 = 0; c0 < count; c0 += kJoinPieces) {
-        const int end = min(count, c0 + kJoinPieces);
-        fetch(c0 + share, end);
-        if (warp < rows) {
-            float2 ml[kJoinPieces / 32];
-            float most = top;
-#pragma unroll
-            for (int i = 0; i < kJoinPieces / 32; ++i) {
-                const int k = c0 + 32 * i + lane;
-                ml[i] = k < end ? p.part_ml[part(k, warp)] : make_float2(0.0f, 0.0f);
-                if (ml[i].y != 0.0f) most = fmaxf(most, ml[i].x);
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int k = k0 + i * shares;
+                if (share < shares && k < end)
+                    v[i] = *reinterpret_cast<const float4*>(p.part_o + part(k, row) * HD + col);
             }
+        };
+        float top = -INFINITY, sum = 0.0f;  // of the warp's row
+        for (int c0 = 0; c0 < count; c0 += kJoinPieces) {
+            const int end = min(count, c0 + kJoinPieces);
+            fetch(c0 + share, end);
+            if (warp < rows) {
+                float2 ml[kJoinPieces / 32];
+                float most = top;
 #pragma unroll
-            for (int m = 1; m < 32; m <<= 1)
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
-            const float base = most == -INFINITY ? 0.0f : most;
-            const float less = top == -INFINITY ? 0.0f : ex2(top - base);
-            float here = 0.0f;
+                for (int i = 0; i < kJoinPieces / 32; ++i) {
+                    const int k = c0 + 32 * i + lane;
+                    ml[i] = k < end ? p.part_ml[part(k, warp)] : make_float2(0.0f, 0.0f);
+                    if (ml[i].y != 0.0f) most = fmaxf(most, ml[i].x);
+                }
 #pragma unroll
-            for (int i = 0; i < kJoinPieces / 32; ++i) {
-                const float w = ml[i].y != 0.0f ? ex2(ml[i].x - base) : 0.0f;
-                if (ml[i].y != 0.0f) here = fmaf(w, ml[i].y, here);
-                weight[warp][32 * i + lane] = w;
-            }
+                for (int m = 1; m < 32; m <<= 1)
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
+                const float base = most == -INFINITY ? 0.0f : most;
+                const float less = top == -INFINITY ? 0.0f : ex2(top - base);
+                float here = 0.0f;
 #pragma unroll
-            for (int m = 1; m < 32; m <<= 1) here += __shfl_xor_sync(0xffffffffu, here, m);
-            sum = fmaf(sum, less, here);
-            top = most;
-            if (lane == 0) {
-                shrink[warp] = less;
-                top_of[warp] = base;
-                sum_of[warp] = sum;
-            }
-        }
-        __syncthreads();
-        if (share < shares) {
-            const float less = shrink[row];
-            acc.x *= less, acc.y *= less, acc.z *= less, acc.w *= less;
-            for (int k0 = c0 + share; k0 < end; k0 += kAtOnce * shares) {
-                if (k0 != c0 + share) fetch(k0, end);
+                for (int i = 0; i < kJoinPieces / 32; ++i) {
+                    const float w = ml[i].y != 0.0f ? ex2(ml[i].x - base) : 0.0f;
+                    if (ml[i].y != 0.0f) here = fmaf(w, ml[i].y, here);
+                    weight[warp][32 * i + lane] = w;
+                }
 #pragma unroll
-                for (int i = 0; i < kAtOnce; ++i) {
-                    const int k = k0 + i * shares;
-                    if (k >= end) break;
-                    const float w = weight[row][k - c0];
-                    acc.x = fmaf(w, v[i].x, acc.x);
-                    acc.y = fmaf(w, v[i].y, acc.y);
-                    acc.z = fmaf(w, v[i].z, acc.z);
-                    acc.w = fmaf(w, v[i].w, acc.w);
+                for (int m = 1; m < 32; m <<= 1) here += __shfl_xor_sync(0xffffffffu, here, m);
+                sum = fmaf(sum, less, here);
+                top = most;
+                if (lane == 0) {
+                    shrink[warp] = less;
+                    top_of[warp] = base;
+                    sum_of[warp] = sum;
                 }
             }
+            __syncthreads();
+            if (share < shares) {
+                const float less = shrink[row];
+                acc.x *= less, acc.y *= less, acc.z *= less, acc.w *= less;
+                for (int k0 = c0 + share; k0 < end; k0 += kAtOnce * shares) {
+                    if (k0 != c0 + share) fetch(k0, end);
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) {
+                        const int k = k0 + i * shares;
+                        if (k >= end) break;
+                        const float w = weight[row][k - c0];
+                        if (w == 0.0f) continue;  // (without weight O may be anything)
+                        acc.x = fmaf(w, v[i].x, acc.x);
+                        acc.y = fmaf(w, v[i].y, acc.y);
+                        acc.z = fmaf(w, v[i].z, acc.z);
+                        acc.w = fmaf(w, v[i].w, acc.w);
+                    }
+                }
+            }
+            __syncthreads();
         }
+        parts[threadIdx.x] = acc;
         __syncthreads();
+        if (share == 0) {
+            for (int k = 1; k < shares; ++k) {
+                const float4 o = parts[threadIdx.x + k * rows * V];
+                acc.x += o.x, acc.y += o.y, acc.z += o.z, acc.w += o.w;
+            }
+            const float l = sum_of[row], inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const int r = st.r0 + r0 + row;
+            const int64_t to = (static_cast<int64_t>(st.q0) + r / p.g) * p.nq + st.h * p.g + r % p.g;
+            uint2 u = make_uint2(0, 0);
+            if (l != 0.0f)
+                u = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            *reinterpret_cast<uint2*>(p.out + to * HD + col) = u;
+            if (col == 0 && p.lse != nullptr)
+                p.lse[to] = l == 0.0f ? -INFINITY : (top_of[row] + log2f(l)) * 0.693147180559945309f;
+        }
+        __syncthreads();  // (what the next rows write has been read)
     }
-    parts[threadIdx.x] = acc;
-    __syncthreads();
-    if (share != 0) return;
-    for (int k = 1; k < shares; ++k) {
-        const float4 o = parts[threadIdx.x + k * rows * V];
-        acc.x += o.x, acc.y += o.y, acc.z += o.z, acc.w += o.w;
-    }
-    const float l = sum_of[row], inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int r = st.r0 + 8 * static_cast<int>(blockIdx.y) + row;
-    const int64_t to = (static_cast<int64_t>(st.q0) + r / p.g) * p.nq + st.h * p.g + r % p.g;
-    uint2 u = make_uint2(0, 0);
-    if (l != 0.0f)
-        u = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2*>(p.out + to * HD + col) = u;
-    if (col == 0 && p.lse != nullptr)
-        p.lse[to] = l == 0.0f ? -INFINITY : (top_of[row] + log2f(l)) * 0.693147180559945309f;
 }
 
 template <int HD, int NT>
@@ -937,15 +963,17 @@ hss_status launch_rows(const Params& p, cudaStream_t stream) {
         return HSS_ERR_CUDA;
     if (launch_pdl(kern, dim3(S::kRanges), dim3(S::kThreads), S::kSmemBytes, stream, p) != cudaSuccess)
         return HSS_ERR_CUDA;
-    if (launch_pdl(join_kernel<HD, NT>, dim3(S::kRanges - 1, NT), dim3(kJoinThreads), 0, stream, p) !=
+    if (launch_pdl(join_kernel<HD, 8 * NT>, dim3(S::kRanges - 1, NT), dim3(kJoinThreads), 0, stream, p) !=
         cudaSuccess)
         return HSS_ERR_CUDA;
     return HSS_OK;
 }
 
-// Of each head_dim's unit.
+// Of each head_dim's unit.  With `many` the kernel for many rows comes first (attend_packed_tc.cuh),
+// and p, for few, is guarded by the flags that it writes.
 template <int HD>
-hss_status launch_head_dim(const Params& p, int n_tiles, cudaStream_t stream);
+hss_status launch_head_dim(const Params& p, const Params* many, int n_tiles, int32_t* flags,
+                           cudaStream_t stream);
 
 }  // namespace packed
 }  // namespace hss

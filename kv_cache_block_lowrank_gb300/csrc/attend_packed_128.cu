@@ -1,11 +1,13 @@
 // attend_packed_128.cu -- the packed cache's attention for heads of 128 elements.
-#include "attend_packed.cuh"
+#include "attend_packed_tc.cuh"
 
 namespace hss {
 namespace packed {
 
 template <>
-hss_status launch_head_dim<128>(const Params& p, int n_tiles, cudaStream_t stream) {
+hss_status launch_head_dim<128>(const Params& p, const Params* many, int n_tiles, int32_t* flags,
+                                cudaStream_t stream) {
+    if (many != nullptr) return launch_many<128>(*many, p, flags, stream);
     return n_tiles == 1 ? launch_rows<128, 1>(p, stream) : launch_rows<128, 2>(p, stream);
 }
 

@@ -1,8 +1,8 @@
 """hss_attend_packed against softmax and sums in 64 bits over the cache's values.
 
-Tolerances, from the kernel's arithmetic.  A weight times its value's scale is rounded to bf16, half
-a step or 2^-8 of it at most, and the result once more: 2^-8 sum p |v| + 2^-8 |out|, where |out| <=
-sum p |v|.  A score is a sum of head_dim exact products in fp32, off by less than (head_dim + 8)
+Tolerances, from the kernels' arithmetic.  A weight times its value's scale is rounded to bf16, half
+a step or 2^-8 of it at most (many rows: the weight alone, to fp16), and the result once more: 2^-8
+sum p |v| + 2^-8 |out|, where |out| <= sum p |v|.  A score is a sum of head_dim exact products in fp32, off by less than (head_dim + 8)
 2^-23 of the sum of their sizes; exp2 and the sums of up to a few hundred weights a thread add less
 than 4e-5: that much of lse, and of sum p |v| once more.
 """
@@ -105,6 +105,20 @@ CASES = [
     dict(hd=128, nq=5, nkv=1, bs=16, ctx=[90, 0], rows=[61, 130]),
     dict(hd=64, nq=14, nkv=2, bs=16, ctx=[200], rows=[40]),
     dict(hd=128, nq=128, nkv=1, bs=16, ctx=[50], rows=[3]),
+    # many rows: one and several row tiles, ends inside a job, rows of nothing among them
+    dict(hd=64, nq=4, nkv=1, bs=32, ctx=[700, 0, 33], rows=[9, 150, 0]),
+    dict(hd=128, nq=8, nkv=1, bs=16, ctx=[1000], rows=[100]),
+    dict(hd=128, nq=3, nkv=1, bs=48, ctx=[65, 400], rows=[13, 90]),
+    dict(hd=192, nq=8, nkv=2, bs=16, ctx=[129, 5], rows=[40, 70]),
+    dict(hd=256, nq=4, nkv=1, bs=16, ctx=[300, 64], rows=[50, 9]),
+    dict(hd=256, nq=1, nkv=1, bs=128, ctx=[77], rows=[140]),
+    dict(hd=128, nq=2, nkv=2, bs=16, ctx=[50, 60, 70, 80] * 10, rows=[20, 17, 1, 33] * 10),
+    dict(hd=64, nq=2, nkv=2, bs=32, ctx=[600, 20], rows=[130, 200], window=100, sinks=20),
+    dict(hd=128, nq=8, nkv=1, bs=16, ctx=[900], rows=[80], window=256, sinks=4),
+    dict(hd=256, nq=2, nkv=1, bs=16, ctx=[333], rows=[66], window=1, sinks=0),
+    dict(hd=192, nq=5, nkv=1, bs=64, ctx=[700], rows=[30], window=64, sinks=100),
+    dict(hd=128, nq=4, nkv=1, bs=16, ctx=[100], rows=[30], scale=-0.2),
+    dict(hd=64, nq=4, nkv=1, bs=16, ctx=[100], rows=[30], scale=0.0),
     # windows: shorter and longer than a tile, than the rows; sinks inside the window
     dict(hd=128, nq=8, nkv=2, bs=16, ctx=[500, 3, 0], rows=[1, 1, 1], window=100, sinks=4),
     dict(hd=64, nq=4, nkv=4, bs=32, ctx=[300], rows=[9], window=1, sinks=0),
@@ -147,11 +161,13 @@ def test_long_and_short_together(rows):
         assert torch.equal(a, b)  # the same bits, whatever the workspace holds
 
 
-@pytest.mark.parametrize("hd,window", [(64, 0), (128, 50), (256, 0)])
-def test_hidden_places_hold_anything(hd, window):
+@pytest.mark.parametrize("hd,window,more", [(64, 0, 1), (128, 50, 1), (256, 0, 1), (64, 50, 20),
+                                            (128, 0, 20), (192, 50, 20), (256, 0, 20)])
+def test_hidden_places_hold_anything(hd, window, more):
     """NaN scales past the end, in front of the window and in rows' futures; pages that no row sees
     with ids that do not exist."""
-    c = Case(hd, 4, 2, 16, [130, 40, 7], [3, 2, 1], window=window, sinks=3 if window else 0)
+    c = Case(hd, 4, 2, 16, [130, 40, 7], [3 * more, 2 * more, more], window=window,
+             sinks=3 if window else 0)
     clean = [t.clone() for t in c.call()]
     cache = c.cache.clone().view(c.max_blocks, 2, 1, -1)
     table, offs = c.table.clone(), c.offs.tolist()
@@ -203,6 +219,40 @@ def test_a_row_sees_no_later_rows_values():
     assert torch.isfinite(got[1:, :, :32]).all() and torch.isfinite(got[1:, :, 64:]).all()
 
 
+@pytest.mark.parametrize("hd,value,scale", [
+    (128, True, float("nan")), (64, False, float("nan")), (256, True, 1000.0),
+    (128, False, 2.0 ** -20), (192, True, 2.0 ** 30), (128, False, 3.0e38)])
+def test_scales_that_fp16_has_no_place_for(hd, value, scale):
+    """Many rows, one group of one token with a scale outside what the tensor cores' operands hold:
+    rows before the token as without it, the others as the definition has them."""
+    c = Case(hd, 4, 1, 16, [40, 90], [30, 40])
+    clean = [t.clone() for t in c.call()]
+    cache = c.cache.clone()
+    t = 40 + 11                                    # the first sequence's row 11
+    tile = cache[c.table[t // 16].item()].view(-1)
+    at = 2 * P.scale_place(t % 16, 1, hd, value)
+    tile[at:at + 2] = torch.tensor([scale], dtype=torch.bfloat16, device=DEV).view(torch.uint8)
+    byte, _ = (P.value_place if value else P.key_place)(t % 16, 32, hd)
+    out, lse = c.call(cache=cache)
+    torch.cuda.synchronize()
+    assert hss.hss_read_device_error() == 0
+    if scale != scale:
+        got = out.cpu()
+        assert torch.isfinite(got[:11]).all() and torch.isfinite(got[30:]).all()
+        if value:
+            assert torch.isnan(got[11:30, :, 32:64]).all()
+            assert torch.isfinite(got[11:30, :, :32]).all()
+        else:
+            assert torch.isnan(got[11:30]).all() and torch.isnan(lse.cpu()[11:30]).all()
+        for a, b in zip((out, lse), clean):
+            assert torch.allclose(a[:11].float(), b[:11].float(), atol=0.05)
+    elif scale < 1e10:
+        c.check(out, lse, cache=cache)
+    else:
+        assert torch.isfinite(out.cpu()[:11].float()).all()
+        assert torch.isfinite(out.cpu()[30:].float()).all()
+
+
 def test_device_errors_hide_tokens():
     c = Case(128, 4, 2, 16, [100, 60], [2, 2])
     table = c.table.clone()
@@ -212,6 +262,14 @@ def test_device_errors_hide_tokens():
     torch.cuda.synchronize()
     assert status.item() == hss.HSS_ERR_OUT_OF_RANGE
     assert hss.hss_read_device_error() == hss.HSS_ERR_OUT_OF_RANGE
+    c.check(out, lse, table=table)
+    c = Case(128, 4, 1, 16, [100, 60], [20, 12])
+    table = c.table.clone()
+    table[2], table[9] = -1, c.max_blocks
+    status.zero_()
+    out, lse = c.call(table=table, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == hss.HSS_ERR_OUT_OF_RANGE == hss.hss_read_device_error()
     c.check(out, lse, table=table)
     # tables too short: one that ends before the rows, and a sequence without any
     for kw in (dict(ctx=[100, 40], rows=[2, 3]), dict(ctx=[10, 3], rows=[1, 2])):
@@ -230,6 +288,27 @@ def test_device_errors_hide_tokens():
     assert status.item() == hss.HSS_ERR_INVALID_ARGUMENT
     assert (out[5] == 7).all() and (lse[5] == 7).all()
     hss.hss_read_device_error()
+
+
+def test_many_rows_captured_and_repeated():
+    """The same bits on every call and replay, whatever the workspace held."""
+    c = Case(128, 8, 2, 16, [3000, 500], [90, 40], window=700, sinks=9)
+    first = [t.clone() for t in c.call()]
+    c.check(*first)
+    work = torch.zeros(1 << 27, device=DEV, dtype=torch.uint8)
+    second = c.call(work=work)
+    torch.cuda.synchronize()
+    for a, b in zip(first, second):
+        assert torch.equal(a, b)
+    out, lse = torch.empty_like(c.q), torch.empty_like(first[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.kept(c.q, c.cache, out, lse)
+        c.kept(c.q, c.cache, out, lse)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(first, (out, lse)):
+        assert torch.equal(a, b)
 
 
 def test_captured_replayed_and_on_two_streams():
