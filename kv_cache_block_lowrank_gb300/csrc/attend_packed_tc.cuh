@@ -17,8 +17,8 @@
 // reach 2^15), so that fp16's range serves both; a weight below 2^-31 of the largest counts as 0 in
 // the product with V, in l as it is.
 //
-// Roles (16 warps): 0-3 copy and decode; 4, 5 issue the products of a row tile each; 8-15 softmax,
-// four to a row tile.  One row tile's exponentials run under the other's products.
+// Roles (20 warps): 0-7 copy and decode; 8, 9 issue the products of a row tile each; 12-19 softmax,
+// four to a row tile, with registers that the others hand over.  One row tile's exponentials run under the other's products.
 //
 // Split: as for few rows (attend_packed.cuh), the list counted in jobs.
 #pragma once
@@ -32,15 +32,15 @@ namespace packed {
 
 template <int HD>
 struct Many {
-    static constexpr int kThreads = 512;
+    static constexpr int kThreads = 640;
     static constexpr int kGroups = HD <= 128 ? 2 : 1;  // row tiles: O takes HD columns for each
     static constexpr int kRows = 128 * kGroups;
-    static constexpr int kStages = HD == 64 ? 4 : (HD == 256 ? 2 : 3);  // jobs decoded ahead
+    static constexpr int kStages = HD <= 128 ? 4 : (HD == 192 ? 3 : 2);  // jobs decoded ahead
     static constexpr int kRawSlots = HD == 256 ? 1 : (HD == 192 ? 2 : 3);
     static constexpr int kOperand = 64 * HD * 2;  // bytes of a job's K, and of its V
     static constexpr int kQBytes = kRows * HD * 2;
     static constexpr int kRawBytes = 4 * Tile<HD>::kBytes;
-    static constexpr int kControl = 4096;
+    static constexpr int kControl = 5120;
     static constexpr int kSmemBytes =
         1024 + kQBytes + 2 * kStages * kOperand + kRawSlots * kRawBytes + kControl;
     static constexpr int kOCols = kGroups * 128;  // where O begins in tensor memory
@@ -50,7 +50,7 @@ struct Many {
 
 struct ManyBarriers {
     uint64_t full[4], empty[4];
-    uint64_t raw_full, raw_read;  // the four copying warps' copies are there; have been read
+    uint64_t raw_full, raw_read;  // the copying warps' copies are there; have been read
     uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];
     uint32_t hidden[4];  // [stage] tiles that nobody sees: missing, or with a bad id
     uint32_t tmem;
@@ -75,6 +75,17 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* b, uint32_t parity,
         if (t0 == 0) t0 = t;
         if (t - t0 > kWaitLimitNs) return false;
     }
+}
+
+// Registers of a warpgroup: 256 threads at 72, 128 at 40 and 256 at 144 come to 60,416 of the
+// 61,440 that 640 threads of 96 were launched with.
+template <int N>
+__device__ __forceinline__ void shrink_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void grow_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -142,22 +153,22 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
     Control& ctl = *reinterpret_cast<Control*>(rest);
     ManyBarriers& bar = *reinterpret_cast<ManyBarriers*>(rest + 512);
     using MyWalk = Walk<R, 4>;
-    static_assert(20 * sizeof(MyWalk) <= M::kControl - 1024, "walks");
+    static_assert(28 * sizeof(MyWalk) <= M::kControl - 1024, "walks");
     MyWalk* walks = reinterpret_cast<MyWalk*>(rest + 1024);
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
 
-    if (warp == 4) {
+    if (warp == 8) {
         tmem_alloc(&bar.tmem, 512);
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&bar.full[i], 4);
+            mbar_init(&bar.full[i], 8);
             mbar_init(&bar.empty[i], M::kGroups);
         }
-        mbar_init(&bar.raw_full, 4);
-        mbar_init(&bar.raw_read, 4);
+        mbar_init(&bar.raw_full, 8);
+        mbar_init(&bar.raw_read, 8);
         for (int w = 0; w < 2; ++w) {
             mbar_init(&bar.q_full[w], 4);
             for (int b = 0; b < 2; ++b) {
@@ -198,9 +209,10 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
     if (lane == 0) walk.begin(p, ctl.start, ctl.seq, ctl.view);
     bool ok = true;
 
-    if (warp < 4) {
+    if (warp < 8) {
+        shrink_registers<72>();
         // ---------------------------------------------------------------- copies and codes
-        MyWalk& ahead = walks[16 + warp];
+        MyWalk& ahead = walks[20 + warp];
         if (lane == 0) ahead.begin(p, ctl.start, ctl.seq, ctl.view);
         const int tid = threadIdx.x;
         bool more = advance(ahead);
@@ -237,7 +249,7 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
                 const uint32_t have = __ballot_sync(0xffffffffu, good) & 15u;
                 constexpr int kVecs = T::kBytes / 16;
 #pragma unroll
-                for (int i0 = 0; i0 < 4 * kVecs; i0 += 128) {
+                for (int i0 = 0; i0 < 4 * kVecs; i0 += 256) {
                     const int i = i0 + tid;  // (whole warps are in or out)
                     if (i0 + (tid & ~31) >= 4 * kVecs) break;
                     const int u = i / kVecs;
@@ -260,14 +272,20 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
         bool unfit = false;
         int slot = 0;
         uint32_t job = 0;
-        // A bf16 scale as a float, or 0 where nobody sees the token or it does not fit.
-        auto fit = [&](uint32_t bits, bool seen) -> float {
-            const float s = __uint_as_float(bits);
-            if (!seen) return 0.0f;
-            if (s == 0.0f || (s >= 7.62939453125e-6f && s <= 64.0f)) return s;
-            unfit = true;
-            return 0.0f;
+        // A bf16 scale times 2^9 in fp16, or 0 where nobody sees the token or it does not fit.
+        auto fit = [&](uint16_t bits, bool seen) -> uint32_t {
+            const float s = __uint_as_float(static_cast<uint32_t>(bits) << 16);
+            const bool fits = s == 0.0f || (s >= 7.62939453125e-6f && s <= 64.0f);
+            unfit |= seen && !fits;
+            return half2_bits(seen && fits ? s * 512.0f : 0.0f, 0.0f);
         };
+        // Where the thread's parts of a job go.  K: tile, token and quarter of its words; 16-byte
+        // pieces of even and odd groups, two groups to a 128-byte column.
+        const int ku = tid >> 6, kt = (tid >> 2) & 15, kc = tid & 3;
+        const int k_row = 16 * ku + kt % 8 / 2 * 4 + kt % 2 + kt / 8 * 2;
+        const uint32_t k_even = swizzled_offset(k_row, 16 * kc, 128);
+        const uint32_t k_odd = swizzled_offset(k_row, 16 * (4 + kc), 128);
+        const int vg = lane >> 2, vc = lane & 3;
         while (ok && advance(walk)) {
             const View& v = walk.v;
             const int n = walk.n, tokens = walk.x.tokens, at1 = v.at1;
@@ -289,63 +307,60 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
                 auto seen = [&](int pos) {
                     return pos <= at1 && pos < tokens && (pos < p.sinks || pos > window_end);
                 };
+                {
+                    const uint8_t* tile = from + ku * T::kBytes;
+                    uint32_t w[NG], s9[(NG + 3) / 4];
+                    load_words(w, tile + kt * (HD / 2) + kc * 4 * NG);
+                    // (a token's scales by its four lanes, handed on by shuffles)
+                    const bool there = ((have >> ku) & 1) && seen(position(ku) + kt);
 #pragma unroll
-                for (int i0 = 0; i0 < 256; i0 += 128) {
-                    const int i = i0 + tid, u = i >> 6, t = (i >> 2) & 15, c = i & 3;
-                    const uint8_t* tile = from + u * T::kBytes;
-                    uint32_t w[NG], s[NG / 2];
-                    load_words(w, tile + t * (HD / 2) + c * 4 * NG);
-                    load_words(s, tile + key_scale<HD>(0, 0) + t * 2 * NG);
-                    const bool there = ((have >> u) & 1) && seen(position(u) + t);
-                    const int row = 16 * u + t % 8 / 2 * 4 + t % 2 + t / 8 * 2;
+                    for (int i = 0; i < (NG + 3) / 4; ++i) {
+                        const int G = 4 * i + kc < NG ? 4 * i + kc : 0;
+                        s9[i] = fit(*reinterpret_cast<const uint16_t*>(
+                                        tile + key_scale<HD>(0, 0) + (kt * NG + G) * 2),
+                                    there);
+                    }
 #pragma unroll
                     for (int G = 0; G < NG; ++G) {
-                        const float f = fit(G & 1 ? s[G / 2] & 0xFFFF0000u : s[G / 2] << 16, there);
-                        const uint32_t s9 = half2_bits(f * 512.0f, f * 512.0f);
-                        const uint32_t s5 = half2_bits(f * 32.0f, f * 32.0f);
+                        const uint32_t s = __byte_perm(
+                            __shfl_sync(0xffffffffu, s9[G / 4], (lane & ~3) | (G % 4)), 0, 0x1010);
+                        const uint32_t s5 = half_mul(s, 0x2C002C00u);  // 2^-4
                         uint32_t y[4];
-                        decode_word(y, w[G], s9, s5, s9, s5);
-                        const int chunk = 4 * G + c;
-                        *reinterpret_cast<uint4*>(sK + (chunk >> 3) * 8192 +
-                                                  swizzled_offset(row, 16 * (chunk & 7), 128)) =
+                        decode_word(y, w[G], s, s5, s, s5);
+                        *reinterpret_cast<uint4*>(sK + (G & 1 ? k_odd : k_even) + G / 2 * 8192) =
                             make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
+                // V: a warp takes 64 elements of a tile, a lane four words of them.
 #pragma unroll
-                for (int i0 = 0; i0 < 2 * HD; i0 += 128) {
-                    const int i = i0 + tid, u = i / (HD / 2), q = i / 32 % kChunks;
-                    const int g = (i & 31) >> 2, c = i & 3;
+                for (int i0 = 0; i0 < 2 * HD; i0 += 256) {
+                    const int i = i0 / 32 + warp, u = i / kChunks, q = i % kChunks;
+                    if (i >= HD / 16) break;
                     const uint8_t* tile = from + u * T::kBytes;
                     uint32_t w[4];
-                    load_words(w, tile + T::kCodes + (q * 32 + (i & 31)) * 16);
-                    const int p0 = position(u);
-                    float f[2][4];  // [group][token]
-#pragma unroll
-                    for (int k4 = 0; k4 < 4; ++k4) {
-                        const int t = 2 * c + (k4 & 1) + 8 * (k4 >> 1);
-                        const bool there = ((have >> u) & 1) && seen(p0 + t);
-                        const uint32_t s = *reinterpret_cast<const uint32_t*>(
-                            tile + value_scale<HD>(0, 0) + (t * NG + 2 * q) * 2);
-                        f[0][k4] = fit(s << 16, there);
-                        f[1][k4] = fit(s & 0xFFFF0000u, there);
-                    }
+                    load_words(w, tile + T::kCodes + (q * 32 + lane) * 16);
+                    const int t = lane & 15;
+                    const bool there = ((have >> u) & 1) && seen(position(u) + t);
+                    uint32_t s9 = fit(*reinterpret_cast<const uint16_t*>(
+                                          tile + value_scale<HD>(0, 0) +
+                                          (t * NG + 2 * q + (lane >> 4)) * 2),
+                                      there);
+                    // (even lanes: their token's scale and the next one's)
+                    s9 = __byte_perm(s9, __shfl_down_sync(0xffffffffu, s9, 1), 0x5410);
+                    uint8_t* to = sV + swizzled_offset(64 * q + vg, 32 * u + 8 * vc, 128);
 #pragma unroll
                     for (int G = 0; G < 2; ++G) {
-                        const uint32_t lo9 = half2_bits(f[G][0] * 512.0f, f[G][1] * 512.0f);
-                        const uint32_t lo5 = half2_bits(f[G][0] * 32.0f, f[G][1] * 32.0f);
-                        const uint32_t hi9 = half2_bits(f[G][2] * 512.0f, f[G][3] * 512.0f);
-                        const uint32_t hi5 = half2_bits(f[G][2] * 32.0f, f[G][3] * 32.0f);
+                        const uint32_t lo = __shfl_sync(0xffffffffu, s9, 16 * G + 2 * vc);
+                        const uint32_t hi = __shfl_sync(0xffffffffu, s9, 16 * G + 2 * vc + 8);
+                        const uint32_t lo5 = half_mul(lo, 0x2C002C00u);
+                        const uint32_t hi5 = half_mul(hi, 0x2C002C00u);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             uint32_t y[4];
-                            decode_word(y, w[2 * G + e], lo9, lo5, hi9, hi5);
-                            const int d = 16 * (4 * q + 2 * G + e) + g;
-                            *reinterpret_cast<uint2*>(sV +
-                                                      swizzled_offset(d, 32 * u + 8 * c, 128)) =
-                                make_uint2(y[0], y[2]);
-                            *reinterpret_cast<uint2*>(
-                                sV + swizzled_offset(d + 8, 32 * u + 8 * c, 128)) =
-                                make_uint2(y[1], y[3]);
+                            decode_word(y, w[2 * G + e], lo, lo5, hi, hi5);
+                            uint8_t* at = to + (2 * G + e) * 2048;  // 16 rows on
+                            *reinterpret_cast<uint2*>(at) = make_uint2(y[0], y[2]);
+                            *reinterpret_cast<uint2*>(at + 1024) = make_uint2(y[1], y[3]);
                         }
                     }
                 }
@@ -365,9 +380,10 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
         if (unfit) *(volatile int*)&bar.unfit = 1;
         cp_async_wait_group<0>();
         if (!ok) give_up();
-    } else if (warp < 8) {
+    } else if (warp < 12) {
+        shrink_registers<40>();
         // ---------------------------------------------------------------- products of row tile w
-        const int w = warp - 4;
+        const int w = warp - 8;
         if (w < M::kGroups) {
             constexpr uint32_t idesc_s = idesc_f16_f32(128, 64);
             constexpr uint32_t idesc_o = idesc_f16_f32(128, HD);
@@ -429,8 +445,9 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
             if (!ok) give_up();
         }
     } else {
+        grow_registers<144>();
         // ---------------------------------------------------------------- softmax
-        const int w = (warp - 8) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const int w = (warp - 12) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         if (w < M::kGroups) {
             const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
             const uint32_t s_cols = lanes + w * 128, o_cols = lanes + M::kOCols + w * HD;
@@ -640,7 +657,7 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     if (threadIdx.x == 0) flags[blockIdx.x] = bar.unfit;
-    if (warp == 4) {
+    if (warp == 8) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
     }
