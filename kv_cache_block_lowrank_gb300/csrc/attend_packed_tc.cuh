@@ -17,8 +17,8 @@
 // reach 2^15), so that fp16's range serves both; a weight below 2^-31 of the largest counts as 0 in
 // the product with V, in l as it is.
 //
-// Roles (20 warps): 0-7 copy and decode; 8, 9 issue the products of a row tile each; 12-19 softmax,
-// four to a row tile, with registers that the others hand over.  One row tile's exponentials run under the other's products.
+// Roles (20 warps): 10 copies; 0-7 decode; 8, 9 issue the products of a row tile each; 12-19
+// softmax, four to a row tile, with registers that the others hand over.  One row tile's exponentials run under the other's products.
 //
 // Split: as for few rows (attend_packed.cuh), the list counted in jobs.
 #pragma once
@@ -50,8 +50,9 @@ struct Many {
 
 struct ManyBarriers {
     uint64_t full[4], empty[4];
-    uint64_t raw_full, raw_read;  // the copying warps' copies are there; have been read
+    uint64_t raw_full[3], raw_empty[3];
     uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];
+    uint32_t have[3];    // [raw slot] tiles that are there
     uint32_t hidden[4];  // [stage] tiles that nobody sees: missing, or with a bad id
     uint32_t tmem;
     int abort, unfit;
@@ -77,8 +78,8 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* b, uint32_t parity,
     }
 }
 
-// Registers of a warpgroup: 256 threads at 72, 128 at 40 and 256 at 144 come to 60,416 of the
-// 61,440 that 640 threads of 96 were launched with.
+// Registers of a warpgroup: 256 threads at 72, 128 at 48 and 256 at 144 come to 61,440, what 640
+// threads of 96 were launched with.
 template <int N>
 __device__ __forceinline__ void shrink_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -167,8 +168,10 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
             mbar_init(&bar.full[i], 8);
             mbar_init(&bar.empty[i], M::kGroups);
         }
-        mbar_init(&bar.raw_full, 8);
-        mbar_init(&bar.raw_read, 8);
+        for (int i = 0; i < RD; ++i) {
+            mbar_init(&bar.raw_full[i], 1);
+            mbar_init(&bar.raw_empty[i], 8);
+        }
         for (int w = 0; w < 2; ++w) {
             mbar_init(&bar.q_full[w], 4);
             for (int b = 0; b < 2; ++b) {
@@ -211,67 +214,11 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
 
     if (warp < 8) {
         shrink_registers<72>();
-        // ---------------------------------------------------------------- copies and codes
-        MyWalk& ahead = walks[20 + warp];
-        if (lane == 0) ahead.begin(p, ctl.start, ctl.seq, ctl.view);
+        // ---------------------------------------------------------------- codes
         const int tid = threadIdx.x;
-        bool more = advance(ahead);
-        int ahead_n = ahead.n, ahead_k = 0;
-        int id = -1, sub = 0, head = 0;  // lane u: tile u of the next job to be copied
-        bool mine = false;
-        // The next job's block ids are asked for when the one before it is copied.
-        auto prepare = [&]() {
-            while (more && ahead_k >= ahead_n) {
-                more = advance(ahead);
-                ahead_n = ahead.n;
-                ahead_k = 0;
-            }
-            mine = more && lane < 4 && ahead_k + lane < ahead_n;
-            if (mine) {
-                const int pos = ahead.v.tile(ahead.k + ahead_k + lane) * 16;
-                const int entry = pos / p.bs;
-                sub = (pos - entry * p.bs) / 16;
-                id = __ldg(p.table + ahead.x.e0 + entry);
-            }
-            if (more) head = ahead.h;
-        };
-        uint32_t have_ring = 0;  // four bits a job, the latest lowest: tiles that are there
-        int fill = 0;
-        auto issue = [&]() {
-            if (more) {
-                const bool good = mine && id >= 0 && id < p.max_blocks;
-                if (mine && !good && warp == 0)
-                    raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
-                const int64_t place =
-                    good ? ((static_cast<int64_t>(id) * p.nkv + head) * (p.bs / 16) + sub) *
-                               T::kBytes
-                         : 0;
-                const uint32_t have = __ballot_sync(0xffffffffu, good) & 15u;
-                constexpr int kVecs = T::kBytes / 16;
-#pragma unroll
-                for (int i0 = 0; i0 < 4 * kVecs; i0 += 256) {
-                    const int i = i0 + tid;  // (whole warps are in or out)
-                    if (i0 + (tid & ~31) >= 4 * kVecs) break;
-                    const int u = i / kVecs;
-                    const int64_t at = __shfl_sync(0xffffffffu, place, u);
-                    if ((have >> u) & 1)
-                        cp_async_16(raw + fill * M::kRawBytes + i * 16,
-                                    p.cache + at + (i - u * kVecs) * 16);
-                }
-                have_ring = (have_ring << 4) | have;
-                fill = fill + 1 == RD ? 0 : fill + 1;
-                ahead_k += 4;
-                prepare();
-            } else {
-                have_ring <<= 4;
-            }
-            cp_async_commit();
-        };
-        prepare();
-        for (int i = 0; i < (RD > 1 ? RD - 1 : 1); ++i) issue();
         bool unfit = false;
         int slot = 0;
-        uint32_t job = 0;
+        uint32_t raw_parity = 0, job = 0;
         // A bf16 scale times 2^9 in fp16, or 0 where nobody sees the token or it does not fit.
         auto fit = [&](uint16_t bits, bool seen) -> uint32_t {
             const float s = __uint_as_float(static_cast<uint32_t>(bits) << 16);
@@ -290,23 +237,22 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
             const View& v = walk.v;
             const int n = walk.n, tokens = walk.x.tokens, at1 = v.at1;
             const int window_end = v.at0 - p.window;
+            const int k_first = walk.k, sinks = v.sinks, w0 = v.w0 - v.sinks;
+            auto seen = [&](int pos) {
+                return pos <= at1 && pos < tokens && (pos < p.sinks || pos > window_end);
+            };
             for (int k = 0; k < n; k += 4, ++job) {
-                cp_async_wait_group<(RD > 1 ? RD - 2 : 0)>();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.raw_full);
-                if (!(ok = wait(&bar.raw_full, job & 1))) break;
-                if constexpr (RD > 1) issue();  // (into the slot that everybody has left)
-                const uint32_t have =
-                    (have_ring >> (RD > 1 ? 4 * (RD - 1) : 0)) & 15u;
                 const int stage = static_cast<int>(job % NS);
+                auto position = [&](int u) {
+                    const int i = k_first + k + u;
+                    return (i < sinks ? i : w0 + i) * 16;
+                };
+                if (!(ok = wait(&bar.raw_full[slot], raw_parity))) break;
                 if (!(ok = wait(&bar.empty[stage], (job / NS + 1) & 1))) break;
+                const uint32_t have = *(volatile uint32_t*)&bar.have[slot];
                 const uint8_t* from = raw + slot * M::kRawBytes;
                 uint8_t* sK = sKV + 2 * stage * M::kOperand;
                 uint8_t* sV = sK + M::kOperand;
-                auto position = [&](int u) { return v.tile(walk.k + k + u) * 16; };
-                auto seen = [&](int pos) {
-                    return pos <= at1 && pos < tokens && (pos < p.sinks || pos > window_end);
-                };
                 {
                     const uint8_t* tile = from + ku * T::kBytes;
                     uint32_t w[NG], s9[(NG + 3) / 4];
@@ -368,20 +314,17 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.full[stage]);
-                slot = slot + 1 == RD ? 0 : slot + 1;
-                if constexpr (RD == 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.raw_read);
-                    if (!(ok = wait(&bar.raw_read, job & 1))) break;
-                    issue();
+                if (lane == 0) mbar_arrive(&bar.raw_empty[slot]);
+                if (++slot == RD) {
+                    slot = 0;
+                    raw_parity ^= 1;
                 }
             }
         }
         if (unfit) *(volatile int*)&bar.unfit = 1;
-        cp_async_wait_group<0>();
         if (!ok) give_up();
     } else if (warp < 12) {
-        shrink_registers<40>();
+        shrink_registers<48>();
         // ---------------------------------------------------------------- products of row tile w
         const int w = warp - 8;
         if (w < M::kGroups) {
@@ -443,6 +386,63 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
                 job += jobs;
             }
             if (!ok) give_up();
+        } else if (w == 2) {
+            // ------------------------------------------------------------ copies
+            // A bulk copy for each of a job's tiles, a lane each; the block ids of a job are asked
+            // for when the one before it is copied.
+            bool more = advance(walk);
+            int n = walk.n, k = 0, slot = 0, id = -1, sub = 0, head = 0;
+            uint32_t parity = 1, job = 0;
+            bool mine = false;
+            auto prepare = [&]() {
+                while (more && k >= n) {
+                    more = advance(walk);
+                    n = walk.n;
+                    k = 0;
+                }
+                mine = more && lane < 4 && k + lane < n;
+                if (mine) {
+                    const int pos = walk.v.tile(walk.k + k + lane) * 16;
+                    const int entry = pos / p.bs;
+                    sub = (pos - entry * p.bs) / 16;
+                    id = __ldg(p.table + walk.x.e0 + entry);
+                }
+                if (more) head = walk.h;
+            };
+            prepare();
+            for (; more; ++job) {
+                const bool good = mine && id >= 0 && id < p.max_blocks;
+                if (mine && !good) raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
+                const int64_t place =
+                    ((static_cast<int64_t>(id) * p.nkv + head) * (p.bs / 16) + sub) * T::kBytes;
+                const uint32_t have = __ballot_sync(0xffffffffu, good);
+                if (!(ok = wait(&bar.raw_empty[slot], parity))) break;
+                if (lane == 0) {
+                    bar.have[slot] = have;
+                    if (have != 0)
+                        mbar_arrive_expect_tx(&bar.raw_full[slot], __popc(have) * T::kBytes);
+                    else
+                        mbar_arrive(&bar.raw_full[slot]);
+                }
+                __syncwarp();
+                if (good)
+                    bulk_copy_g2s(raw + slot * M::kRawBytes + lane * T::kBytes, p.cache + place,
+                                  T::kBytes, &bar.raw_full[slot]);
+                __syncwarp();
+                if (++slot == RD) {
+                    slot = 0;
+                    parity ^= 1;
+                }
+                k += 4;
+                prepare();
+            }
+            if (!ok) give_up();
+            // Nobody leaves before the copies have landed: the last use of every slot.
+            for (uint32_t i = 0; i < RD && i < job; ++i) {
+                const uint32_t use = job - 1 - i;
+                (void)mbar_wait_for(&bar.raw_full[use % RD], (use / RD) & 1,
+                                    ok ? kWaitLimitNs : 1000000);
+            }
         }
     } else {
         grow_registers<144>();
