@@ -119,6 +119,10 @@ CASES = [
     dict(hd=192, nq=5, nkv=1, bs=64, ctx=[700], rows=[30], window=64, sinks=100),
     dict(hd=128, nq=4, nkv=1, bs=16, ctx=[100], rows=[30], scale=-0.2),
     dict(hd=64, nq=4, nkv=1, bs=16, ctx=[100], rows=[30], scale=0.0),
+    dict(hd=64, nq=4, nkv=1, bs=32, ctx=[5000], rows=[70]),
+    dict(hd=128, nq=4, nkv=1, bs=16, ctx=[5000], rows=[70]),
+    dict(hd=192, nq=4, nkv=1, bs=16, ctx=[5000], rows=[40]),
+    dict(hd=256, nq=4, nkv=1, bs=16, ctx=[5000], rows=[40]),
     # windows: shorter and longer than a tile, than the rows; sinks inside the window
     dict(hd=128, nq=8, nkv=2, bs=16, ctx=[500, 3, 0], rows=[1, 1, 1], window=100, sinks=4),
     dict(hd=64, nq=4, nkv=4, bs=32, ctx=[300], rows=[9], window=1, sinks=0),
