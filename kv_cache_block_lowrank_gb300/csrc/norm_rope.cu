@@ -96,7 +96,7 @@ __device__ __forceinline__ float sum_squares(const uint4& u, float s) {
     return s;
 }
 
-// Vector v of a head, normed: x inv (w + offset).
+// Vector v of a head, normed: x (w inv + offset), with the offset times inv already.
 __device__ __forceinline__ void scale8(float* x, float inv, const uint16_t* weight, int v,
                                        float offset) {
     if (weight == nullptr) {
@@ -106,30 +106,38 @@ __device__ __forceinline__ void scale8(float* x, float inv, const uint16_t* weig
         float w[8];
         unpack8(load16(weight + 8 * v), w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= inv * (w[e] + offset);
+        for (int e = 0; e < 8; ++e) x[e] *= fmaf(w[e], inv, offset);
     }
 }
 
+__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
+    const float x = a;
+    a = x * c - b * s;
+    b = b * c + x * s;
+}
+
 __device__ __forceinline__ void turn_interleaved(float* x, int v, int rot, const float2* cs) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int pair = 4 * v + e;
-        if (2 * pair < rot) {
-            const float a = x[2 * e], b = x[2 * e + 1];
-            const float2 c = cs[pair];
-            x[2 * e] = a * c.x - b * c.y;
-            x[2 * e + 1] = b * c.x + a * c.y;
-        }
+    if (8 * v + 8 <= rot) {
+        const float4 c0 = *reinterpret_cast<const float4*>(cs + 4 * v);
+        const float4 c1 = *reinterpret_cast<const float4*>(cs + 4 * v + 2);
+        turn_pair(x[0], x[1], c0.x, c0.y);
+        turn_pair(x[2], x[3], c0.z, c0.w);
+        turn_pair(x[4], x[5], c1.x, c1.y);
+        turn_pair(x[6], x[7], c1.z, c1.w);
+        return;
     }
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (8 * v + 2 * e < rot)
+            turn_pair(x[2 * e], x[2 * e + 1], cs[4 * v + e].x, cs[4 * v + e].y);
 }
 
 __device__ __forceinline__ void turn_half(float* x, float* y, int j, const float2* cs) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float a = x[e], b = y[e];
-        const float2 c = cs[8 * j + e];
-        x[e] = a * c.x - b * c.y;
-        y[e] = b * c.x + a * c.y;
+    for (int e = 0; e < 8; e += 2) {
+        const float4 c = *reinterpret_cast<const float4*>(cs + 8 * j + e);
+        turn_pair(x[e], y[e], c.x, c.y);
+        turn_pair(x[e + 1], y[e + 1], c.z, c.w);
     }
 }
 
@@ -154,11 +162,11 @@ __device__ __forceinline__ void turn_half_odd(float* x, const uint16_t* head,
 }
 
 template <int HD, int MODE>
-__global__ void __launch_bounds__(kMostThreads) norm_rope_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kMostThreads, 4) norm_rope_kernel(const NormParams p) {
     using D = Deal<HD>;
     constexpr int kLanes = D::kLanes, kPairs = D::kPairs, kBatch = D::kBatch;
     const int threads = static_cast<int>(blockDim.x);
-    __shared__ float2 cs[128];
+    __shared__ alignas(16) float2 cs[128];
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t token = blockIdx.x;
@@ -240,8 +248,8 @@ __global__ void __launch_bounds__(kMostThreads) norm_rope_kernel(const NormParam
                     float a[8], b[8];
                     unpack8(x[u][i][0], a);
                     unpack8(x[u][i][1], b);
-                    scale8(a, inv, weight, v0, p.offset);
-                    scale8(b, inv, weight, v1, p.offset);
+                    scale8(a, inv, weight, v0, p.offset * inv);
+                    scale8(b, inv, weight, v1, p.offset * inv);
                     if constexpr (MODE == kHalf) {
                         if (j < p.rot / 16) {
                             turn_half(a, b, j, cs);
