@@ -293,12 +293,6 @@ struct alignas(8) Control {
 };
 static_assert(sizeof(Control) <= 512, "control block");
 
-// (a 64-bit division is some hundred instructions, one after another)
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
 // Where every CTA's range begins, from a scan of the sequences' lengths.
 template <int R, int UNIT, int THREADS>
 __device__ __forceinline__ void find_start(const Params& p, Control& ctl, int64_t least) {

@@ -15,10 +15,16 @@ struct Tile {
     static_assert(kBytes == 18 * HD, "as documented");
 };
 
+// (a 64-bit division is some hundred instructions, one after another)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // Bytes from the cache's start to the tile that holds a slot of a head.
 template <int HD>
 __device__ __forceinline__ int64_t tile_at(int64_t slot, int head, int nkv, int bs) {
-    const int64_t block = slot / bs;
+    const int64_t block = divide(slot, bs);
     const int in_block = static_cast<int>(slot - block * bs) / 16;
     return ((block * nkv + head) * (bs / 16) + in_block) * Tile<HD>::kBytes;
 }
@@ -57,19 +63,43 @@ __device__ __forceinline__ uint32_t group_scale(const uint4& x) {
     return pack_bf16x2(s, 0.0f) & 0xFFFFu;
 }
 
-// The codes + 8 of 8 elements, nibble by nibble.
+// group_codes for scales whose reciprocal might not be a number, by division.
+static __device__ __noinline__ uint32_t group_codes_tiny(const uint4 x, uint32_t scale) {
+    const float s = __uint_as_float(scale << 16);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t codes = 0;
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t half = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+        const int c = __float2int_rn(__fdiv_rn(__uint_as_float(half << 16), s));
+        codes |= static_cast<uint32_t>(max(-7, min(7, c)) + 8) << (4 * i);
+    }
+    return codes;
+}
+
+// The codes + 8 of 8 elements, nibble by nibble: rint(x / scale), ties to even, without a division
+// for each.  x and the scale have 8 bits each, so a quotient within 2^-16 of a half is one, and x
+// times the scale's reciprocal is nearer than that: what it rounds to is right but for exact halves,
+// and those the remainder shows, which is exact.
 __device__ __forceinline__ uint32_t group_codes(const uint4& x, uint32_t scale) {
     if (scale == 0 || scale >= 0x7F80u) return 0x88888888u;
     const float s = __uint_as_float(scale << 16);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t codes = 0;
+    if (scale < 0x0800u) return group_codes_tiny(x, scale);  // below 2^-111
+    // Adding 1.5 2^23 leaves the rounded quotient in a float's low bits.
+    constexpr float kAdd = 12582912.0f;
+    constexpr uint32_t kAddBits = 0x4B400000u;
+    const float inverse = __frcp_rn(s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float e = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-        const int c = max(-7, min(7, __float2int_rn(__fdiv_rn(e, s))));
-        codes |= static_cast<uint32_t>(c + 8) << (4 * i);
+        uint32_t q = __float_as_uint(fmaf(e, inverse, kAdd));
+        const float rest = fmaf(kAdd - __uint_as_float(q), s, e);
+        if (fabsf(rest) * 2.0f == s && (q & 1)) q += rest > 0.0f ? 1u : ~0u;
+        codes += q << (4 * i);
     }
-    return codes;
+    // (every nibble holds its code, with what was added to all of them taken away and 8 added)
+    return codes - kAddBits * 0x11111111u + 0x88888888u;
 }
 
 }  // namespace hss

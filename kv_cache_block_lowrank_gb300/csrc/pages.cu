@@ -22,10 +22,18 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;
 constexpr int kSums = 3;
+constexpr int kHeldOffsets = 2048;  // of the new tables, kept in shared memory if they fit
+
+// (a 64-bit division is some hundred instructions, one after another)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
 
 struct PlanShared {
     int64_t warp[kSums][kWarps];
     int64_t cta[kSums];  // this CTA's totals, read by the others
+    int32_t offsets[kHeldOffsets];
 };
 
 __device__ __forceinline__ int64_t warp_before(int64_t x, int64_t& all) {
@@ -110,22 +118,25 @@ __device__ __forceinline__ Heir heir_of(const ForkArgs& f, int i) {
     }
     const int64_t room = max(__ldg(f.room + i), 0);
     x.length = min(static_cast<int64_t>(max(__ldg(f.lengths + i), 0)), has * f.block_size);
-    x.kept = (x.length + f.block_size - 1) / f.block_size;
-    x.n = (x.length + room + f.block_size - 1) / f.block_size;
-    x.writes = room > 0 && x.length % f.block_size != 0;
+    x.kept = divide(x.length + f.block_size - 1, f.block_size);
+    x.n = divide(x.length + room + f.block_size - 1, f.block_size);
+    x.writes = room > 0 && x.length != x.kept * f.block_size;
     return x;
 }
 
-// The last sequence whose entries begin at or before e.
-__device__ __forceinline__ int owner_of(const int32_t* offsets, int n, int64_t e) {
-    int lo = 0, hi = n - 1;
+// The last sequence whose entries begin at or before e, and where they begin.
+__device__ __forceinline__ int owner_of(const ForkArgs& f, const PlanShared& sh, int64_t e,
+                                        int64_t& begin) {
+    const bool held = f.num_new <= kHeldOffsets;
+    int lo = 0, hi = f.num_new - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (__ldcg(offsets + mid) <= e)
+        if ((held ? sh.offsets[mid] : __ldcg(f.new_offsets + mid)) <= e)
             lo = mid;
         else
             hi = mid - 1;
     }
+    begin = held ? sh.offsets[lo] : __ldcg(f.new_offsets + lo);
     return lo;
 }
 
@@ -214,11 +225,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster.sync();
 
     // What is kept.
+    if (f.num_new <= kHeldOffsets) {
+        for (int i = threadIdx.x; i < f.num_new; i += kThreads)
+            sh.offsets[i] = __ldcg(f.new_offsets + i);
+        __syncthreads();
+    }
     const int64_t table_end = min(new_total, f.table_room);
     for (int64_t e = at; e < table_end; e += stride) {
-        const int i = owner_of(f.new_offsets, f.num_new, e);
+        int64_t begin;
+        const int i = owner_of(f, sh, e, begin);
         const Heir x = heir_of(f, i);
-        const int64_t j = e - __ldcg(f.new_offsets + i);
+        const int64_t j = e - begin;
         if (j < x.kept) {
             const int32_t id = __ldg(f.table + x.from + j);
             if (page_ok(id)) atomicAdd(f.new_refs + id, 1);
@@ -284,9 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             f.new_table[e] = -1;
             continue;
         }
-        const int i = owner_of(f.new_offsets, f.num_new, e);
+        int64_t begin;
+        const int i = owner_of(f, sh, e, begin);
         const Heir x = heir_of(f, i);
-        const int64_t j = e - __ldcg(f.new_offsets + i);
+        const int64_t j = e - begin;
         const int32_t mark = __ldcg(copy_before + i);
         const int64_t first_fresh = x.kept - (mark < 0 ? 1 : 0);
         int32_t id;
@@ -449,9 +467,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs c, in
     const int64_t per_pair = pieces * pools * c.num_layers;
     const int64_t total = copies * per_pair;
     for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
-        const int64_t pair = w / per_pair, in = w - pair * per_pair;
-        const int64_t piece = in % pieces;
-        const int rest = static_cast<int>(in / pieces);
+        const int64_t pair = divide(w, per_pair), in = w - pair * per_pair;
+        const int rest = static_cast<int>(divide(in, pieces));
+        const int64_t piece = in - rest * pieces;
         const int32_t src = c.src[pair], dst = c.dst[pair];
         if (src < 0 || dst < 0) continue;
         if (src >= c.max_blocks || dst >= c.max_blocks) {

@@ -30,7 +30,9 @@ def same(got, want):
 @pytest.mark.parametrize("hd,nkv,bs,tokens,order", [
     (128, 8, 16, 1, "any"), (128, 2, 32, 77, "run"), (64, 3, 48, 100, "run"),
     (64, 1, 16, 16, "run"), (192, 3, 16, 45, "any"), (192, 2, 128, 300, "run"),
-    (256, 1, 64, 33, "any"), (256, 5, 16, 64, "run"), (128, 1, 256, 513, "run")])
+    (256, 1, 64, 33, "any"), (256, 5, 16, 64, "run"), (128, 1, 256, 513, "run"), (64, 9, 16, 700, "run"),
+    (192, 2, 48, 500, "run"), (256, 3, 16, 400, "run"), (128, 8, 32, 300, "any"),
+    (128, 3, 16, 600, "parts"), (64, 2, 64, 1000, "parts")])
 def test_round_trip(hd, nkv, bs, tokens, order):
     g = torch.Generator(device=DEV).manual_seed(hd * tokens + bs)
     blocks = tokens // bs + 3
@@ -43,10 +45,16 @@ def test_round_trip(hd, nkv, bs, tokens, order):
     if order == "run":  # tokens in a row, from inside a page on
         at = torch.arange(tokens, device=DEV) + bs // 2
         slots = torch.randperm(blocks, generator=g, device=DEV)[at // bs] * bs + at % bs
+    elif order == "parts":  # runs of many lengths, as prompts' ends lie side by side
+        cuts = torch.randint(0, 40, (blocks,), generator=g, device=DEV)
+        free = torch.arange(blocks * bs, device=DEV)
+        slots = free[(free // bs * 7 + free % bs) % 11 != cuts[free // bs] % 11][:tokens]
+        tokens = len(slots)
+        k, v = k[:tokens].contiguous(), v[:tokens].contiguous()
     else:
         slots = torch.randperm(blocks * bs, generator=g, device=DEV)[:tokens]
     pad = torch.zeros(tokens, dtype=torch.bool, device=DEV)
-    pad[1::9] = True
+    pad[1::9 if tokens < 100 else 97] = True
     slots[pad] = -1
     d = hss.hss_dims(1, nkv, nkv, hd, 16, bs, blocks)
     size = hss.hss_packed_page_bytes(d)
