@@ -652,8 +652,8 @@ typedef struct hss_pack_args {
  *   cache     device, one layer's pages, 16-byte aligned
  * A negative slot marks padding; a slot >= max_blocks * block_size is skipped and raises
  * HSS_ERR_OUT_OF_RANGE in *dev_status and the library's device error word.  Name a slot once: what
- * two tokens of one call leave in it is a mixture of both.  (One call packs whole tiles where 16
- * tokens in a row fill one, so that tokens in the order of their slots are written fastest.)
+ * two tokens of one call leave in it is a mixture of both.  (From 4096 tokens on, 16 tokens in a row
+ * that fill a tile are packed together: give tokens in the order of their slots.)
  */
 hss_status hss_pack_kv_tokens(const hss_pack_args* args, const uint16_t* K, const uint16_t* V,
                               uint8_t* cache, void* stream);
@@ -689,7 +689,9 @@ typedef struct hss_packed_args {
 } hss_packed_args;
 
 /* Bytes of the workspace: enough for every call with these dims, window and sinks and these counts
- * or smaller ones (0 if a count is negative or the dims are not valid). */
+ * or smaller ones (0 if a count is negative or the dims are not valid).  It goes by head_dim and by
+ * whether there are more than 32 rows of a sequence and kv head together: 5 or 45 MB for head_dim
+ * 128, 10 or 50 for 256. */
 size_t hss_attend_packed_workspace_bytes(const hss_dims* dims, int32_t num_seqs, int32_t max_q,
                                          int64_t total_blocks, int32_t window, int32_t sinks);
 
@@ -712,11 +714,19 @@ size_t hss_attend_packed_workspace_bytes(const hss_dims* dims, int32_t num_seqs,
  *   cache    device, one layer's pages, 16-byte aligned
  *   out      device, [total_q, num_q_heads, head_dim] bf16, 16-byte aligned
  *   lse      device, [total_q, num_q_heads] f32, or NULL
- * Scores, softmax statistics and sums are fp32.  The weights exp(s - m), each times its value's
- * scale, enter the product with the codes rounded to bf16; the statistics take them unrounded.
- * One more launch follows the attention itself on the stream (the join of what several CTAs have
- * of a row); a pipeline wait that runs out raises HSS_ERR_DEVICE_TIMEOUT like those of the other
- * kernels.
+ * Scores, softmax statistics and sums are fp32; the statistics take the weights exp(s - m)
+ * unrounded.  Up to 32 rows of a sequence and kv head together (rows times num_q_heads /
+ * num_kv_heads, by max_q): a weight times its value's scale enters the product with the codes
+ * rounded to bf16; an element of out is off by at most 2^-8 sum_p exp(s - lse) |v_p| for it, beside
+ * the rounding of out itself.  More rows run on the tensor cores of tcgen05 with K, V and the weights
+ * in fp16: K and V lose nothing, a weight 2^-12 of itself at most.  There a scale that fp16 has no
+ * place for (above 64, or below 2^-17 but not 0, or not finite) makes the whole call run by the
+ * first method after all, which is correct for every scale but several times slower.
+ * The join of what several CTAs have of a row follows the attention itself on the stream, for many
+ * rows with the two launches of that second attempt, which end at once if it is not needed.  A
+ * pipeline wait that runs out raises HSS_ERR_DEVICE_TIMEOUT like those of the other kernels.
+ * Single tokens in one call with a chunk of many rows cost as much as row tiles of 128: call them
+ * apart.
  * Supported: num_q_heads / num_kv_heads <= 128, at most 2^30 rows of a sequence and kv head
  * together; window, sinks >= 0; positions below 2^31 - 512.  Device-side errors
  * (*dev_status and the library's device error word): a block id outside [0, max_blocks) of a page

@@ -72,9 +72,10 @@ hss_status launch_attend_packed(const PackedArgs& a, cudaStream_t stream) {
     p.nkv = x.dims.num_kv_heads;
     p.g = p.nq / p.nkv;
     p.bs = x.dims.block_size;
-    p.window = x.window > 0 ? std::min(x.window, 0x7FFFFF00) : 0x7FFFFF00;
+    p.window = x.window > 0 ? std::min(x.window, packed::kNoWindow) : packed::kNoWindow;
     p.sinks = x.window > 0 ? x.sinks : 0;
     p.c = x.scale * 1.44269504088896341f;
+    p.row_tiles = 0;
     p.guard = nullptr;
     p.dev_status = x.dev_status;
     p.lib_error = dev->error_word;

@@ -19,6 +19,7 @@
 // goes to the workspace and a second kernel joins it.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "packed.cuh"
@@ -28,6 +29,14 @@ namespace packed {
 
 constexpr int kSms = 152;          // GB300's; the workspace does not depend on the device
 constexpr float kLazy = 8.0f;
+constexpr int32_t kNoWindow = 0x7FFFFF00;
+// Short contexts (as far as the host can tell: by the table or the window) of not too many units: a
+// CTA takes a unit, and there is neither a list nor a join.  (32 heads on 8 of 128; with the list and
+// so: one sequence of 500 tokens 14.4 and 11.2 us, of 2000 14.4 and 20.5; windows of 500 tokens of 16
+// sequences 19.3 and 12.3, of 64 29.8 and 23.0, of 256 77 and 83; of 2000 tokens of 16 24.7 and 20.7.)
+__host__ __device__ constexpr bool by_units(int64_t tiles, int64_t units) {
+    return units <= 1024 && tiles <= (units >= 128 ? 128 : 64);
+}
 // In the list a unit is longer than its tiles by what it costs besides (its first loads, the warps'
 // meeting, its rows' way out), so that ranges of equal length take equal time: in tiles here, in
 // jobs of four for many rows.  (None, 8, 16 and 32: 64 sequences of 1k to 16k tokens 160, 156, 151
@@ -57,8 +66,9 @@ struct Params {
     int64_t max_blocks;
     int64_t total_blocks;
     int32_t num_seqs, max_q, nq, nkv, g, bs;
-    int32_t window;  // 0x7FFFFF00 at most, which is none
+    int32_t window;  // kNoWindow at most, which is none
     int32_t sinks;   // 0 without a window
+    int32_t row_tiles;  // 0: the list; else a CTA takes a unit of this many row tiles a sequence
     float c;         // scale log2(e)
     int32_t* dev_status;
     int32_t* lib_error;
@@ -111,6 +121,13 @@ __device__ __forceinline__ SeqInfo load_seq(const Params& p, int s) {
     x.tokens = static_cast<int>(min(room, want));
     x.cut = room < want;
     return x;
+}
+
+// What is wrong with a sequence.
+__device__ __forceinline__ void report(const Params& p, int s, const SeqInfo& x) {
+    if (__ldg(p.q_offsets + s + 1) - x.q0 > p.max_q)
+        raise_error(p.dev_status, p.lib_error, HSS_ERR_INVALID_ARGUMENT);
+    if (x.cut && x.rows > 0) raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
 }
 
 // What a row tile sees: tiles [0, sinks) and [w0, end).
@@ -176,6 +193,20 @@ struct Walk {
         x = seq;
         v = view;
         rts = row_tiles<R>(p, x);
+    }
+    // One unit and no list.
+    __device__ __forceinline__ void begin_unit(const Params& p, int unit) {
+        h = unit % p.nkv;
+        rt = unit / p.nkv % p.row_tiles;
+        s = unit / p.nkv / p.row_tiles;
+        x = load_seq(p, s);
+        rts = row_tiles<R>(p, x);
+        t = 0;
+        f = f1 = 0;
+        if (rt < rts) {
+            v = view_of<R>(p, x, rt);
+            f1 = v.cost<UNIT>();
+        }
     }
     __device__ __forceinline__ bool next(const Params& p) {
         while (f < f1) {
@@ -311,11 +342,7 @@ __device__ __forceinline__ void find_start(const Params& p, Control& ctl, int64_
     for (int s = s0; s < s1; ++s) {
         x = load_seq(p, s);
         mine += length(x);
-        if (blockIdx.x == 0) {
-            if (__ldg(p.q_offsets + s + 1) - x.q0 > p.max_q)
-                raise_error(p.dev_status, p.lib_error, HSS_ERR_INVALID_ARGUMENT);
-            if (x.cut && x.rows > 0) raise_error(p.dev_status, p.lib_error, HSS_ERR_OUT_OF_RANGE);
-        }
+        if (blockIdx.x == 0) report(p, s, x);
     }
     int64_t before = mine;
 #pragma unroll
@@ -426,17 +453,24 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
         ctl.abort = 0;
         fence_mbarrier_init();
     }
+    __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
     if (!wanted(p)) return;
-    find_start<R, 1, S::kThreads>(p, ctl, TT * W);
+    if (p.row_tiles == 0) {
+        find_start<R, 1, S::kThreads>(p, ctl, TT * W);
+        if (lane == 0) {
+            ahead.begin(p, ctl.start, ctl.seq, ctl.view);
+            walk.begin(p, ctl.start, ctl.seq, ctl.view);
+        }
+    } else if (lane == 0) {
+        walk.begin_unit(p, blockIdx.x);
+        ahead = walk;
+        if (warp == 0 && walk.h == 0 && walk.rt == 0) report(p, walk.s, walk.x);
+    }
     volatile int* abort_flag = &ctl.abort;
 
     // ---- the copies, a ring ahead of the products
-    if (lane == 0) {
-        ahead.begin(p, ctl.start, ctl.seq, ctl.view);
-        walk.begin(p, ctl.start, ctl.seq, ctl.view);
-    }
     bool more = advance(ahead);
     int ahead_n = ahead.n;
     int ahead_k = TT * warp;  // the warp's tiles of the piece: TT of every TT W
@@ -949,18 +983,34 @@ __global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const Params p) {
 }
 
 template <int HD, int NT>
-hss_status launch_rows(const Params& p, cudaStream_t stream) {
+hss_status launch_rows(const Params& many_units, cudaStream_t stream) {
     using S = Shape<HD, NT>;
     auto kern = attend_kernel<HD, NT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes) !=
         cudaSuccess)
         return HSS_ERR_CUDA;
-    if (launch_pdl(kern, dim3(S::kRanges), dim3(S::kThreads), S::kSmemBytes, stream, p) != cudaSuccess)
-        return HSS_ERR_CUDA;
-    if (launch_pdl(join_kernel<HD, 8 * NT>, dim3(S::kRanges - 1, NT), dim3(kJoinThreads), 0, stream, p) !=
+    Params p = many_units;
+    int64_t tiles = (p.total_blocks * p.bs + 15) / 16;
+    if (p.window < kNoWindow)
+        tiles = std::min<int64_t>(
+            tiles, (static_cast<int64_t>(p.window) + p.sinks + p.max_q) / 16 + 4);
+    const int64_t row_tiles = (static_cast<int64_t>(p.max_q) * p.g + S::kRows - 1) / S::kRows;
+    const int64_t units = p.num_seqs * row_tiles * p.nkv;
+    if (p.guard == nullptr && by_units(tiles, units)) {
+        p.row_tiles = static_cast<int32_t>(row_tiles);
+        return launch_pdl(kern, dim3(static_cast<unsigned>(units)), dim3(S::kThreads),
+                          S::kSmemBytes, stream, p) == cudaSuccess
+                   ? HSS_OK
+                   : HSS_ERR_CUDA;
+    }
+    p.row_tiles = 0;
+    if (launch_pdl(kern, dim3(S::kRanges), dim3(S::kThreads), S::kSmemBytes, stream, p) !=
         cudaSuccess)
         return HSS_ERR_CUDA;
-    return HSS_OK;
+    return launch_pdl(join_kernel<HD, 8 * NT>, dim3(S::kRanges - 1, NT), dim3(kJoinThreads), 0,
+                      stream, p) == cudaSuccess
+               ? HSS_OK
+               : HSS_ERR_CUDA;
 }
 
 // Of each head_dim's unit.  With `many` the kernel for many rows comes first (attend_packed_tc.cuh),

@@ -165,6 +165,22 @@ def test_long_and_short_together(rows):
         assert torch.equal(a, b)  # the same bits, whatever the workspace holds
 
 
+@pytest.mark.parametrize("hd,nq,nkv,seqs,rows", [(64, 2, 1, 700, 1), (128, 4, 2, 530, 2),
+                                                (256, 2, 2, 300, 1), (128, 32, 2, 20, 1)])
+@pytest.mark.parametrize("window", [20, 700])
+def test_windows_of_many_short_sequences(hd, nq, nkv, seqs, rows, window):
+    """Around the number of units and the length from which on they are listed."""
+    g = np.random.default_rng(seqs + window)
+    ctx = g.integers(0, 400 if seqs > 100 else 3000, seqs).tolist()
+    c = Case(hd, nq, nkv, 32, ctx, g.integers(0, rows + 1, seqs).tolist(), window=window, sinks=5,
+             max_q=rows)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = c.call(status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    c.check(out, lse)
+
+
 @pytest.mark.parametrize("hd,window,more", [(64, 0, 1), (128, 50, 1), (256, 0, 1), (64, 50, 20),
                                             (128, 0, 20), (192, 50, 20), (256, 0, 20)])
 def test_hidden_places_hold_anything(hd, window, more):

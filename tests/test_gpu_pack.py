@@ -32,7 +32,10 @@ def same(got, want):
     (64, 1, 16, 16, "run"), (192, 3, 16, 45, "any"), (192, 2, 128, 300, "run"),
     (256, 1, 64, 33, "any"), (256, 5, 16, 64, "run"), (128, 1, 256, 513, "run"), (64, 9, 16, 700, "run"),
     (192, 2, 48, 500, "run"), (256, 3, 16, 400, "run"), (128, 8, 32, 300, "any"),
-    (128, 3, 16, 600, "parts"), (64, 2, 64, 1000, "parts")])
+    (128, 3, 16, 600, "parts"), (64, 2, 64, 1000, "parts"),
+    # enough for whole tiles to be taken together
+    (64, 2, 16, 4500, "run"), (128, 2, 48, 5000, "parts"), (192, 1, 16, 4100, "any"),
+    (256, 1, 32, 4200, "run"), (128, 5, 16, 4096, "run"), (192, 3, 128, 5200, "parts")])
 def test_round_trip(hd, nkv, bs, tokens, order):
     g = torch.Generator(device=DEV).manual_seed(hd * tokens + bs)
     blocks = tokens // bs + 3
