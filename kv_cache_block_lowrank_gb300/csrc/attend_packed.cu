@@ -35,7 +35,7 @@ struct Layout {
         starts = take(kRanges * sizeof(packed::Start));
         ml = take(2 * kRangeRows * sizeof(float2));
         o = take(static_cast<size_t>(2 * kRangeRows) * d.head_dim * sizeof(float));
-        flags = take(kSms * sizeof(int32_t));
+        flags = take(packed::kMostGuards * sizeof(int32_t));
         const size_t rows = many ? 2 * kSms * many_rows(d) : 0;
         many_starts = take(kSms * sizeof(packed::Start));
         many_ml = take(rows * sizeof(float2));
@@ -77,6 +77,7 @@ hss_status launch_attend_packed(const PackedArgs& a, cudaStream_t stream) {
     p.c = x.scale * 1.44269504088896341f;
     p.row_tiles = 0;
     p.guard = nullptr;
+    p.guards = 0;
     p.dev_status = x.dev_status;
     p.lib_error = dev->error_word;
     const int64_t rows = rows_of(x.dims, p.max_q);

@@ -37,6 +37,18 @@ constexpr int32_t kNoWindow = 0x7FFFFF00;
 __host__ __device__ constexpr bool by_units(int64_t tiles, int64_t units) {
     return units <= 1024 && tiles <= (units >= 128 ? 128 : 64);
 }
+// The same for many rows, up to as many units as there are flags for.  (8 heads on 2 of 128: one
+// sequence of 12 rows over 500 tokens 28 us with the list and 23 so, over 1500 29 and 43; 16 of 200
+// rows over 1500 tokens, which is 128 units, 93 and 55.)
+constexpr int kMostGuards = 2048;
+__host__ __device__ constexpr bool many_by_units(int64_t tiles, int64_t units) {
+    return units <= kMostGuards && tiles <= (units >= 100 ? 256 : 40);
+}
+// A unit this short is not cut: the range that it begins in takes all of it.  (Cut and so: 64 single
+// tokens over 300 tokens 24.9 and 21.5 us, 16 chunks of 200 rows over 500 70 and 43.  A few units of
+// twice this length are better cut: one chunk of 12 rows over 1500 tokens 29 and 45.)
+template <int UNIT>
+constexpr int kUncut = UNIT == 1 ? 48 : 20;
 // In the list a unit is longer than its tiles by what it costs besides (its first loads, the warps'
 // meeting, its rows' way out), so that ranges of equal length take equal time: in tiles here, in
 // jobs of four for many rows.  (None, 8, 16 and 32: 64 sequences of 1k to 16k tokens 160, 156, 151
@@ -76,7 +88,8 @@ struct Params {
     Start* starts;    // [ranges]
     float2* part_ml;  // [2 ranges][R] (m, l)
     float* part_o;    // [2 ranges][R][head_dim]
-    const int32_t* guard;  // [kSms] or null: nothing is done if all are 0
+    const int32_t* guard;  // [guards] or null: nothing is done if all are 0
+    int32_t guards;
 };
 
 template <int HD, int NT>
@@ -211,8 +224,10 @@ struct Walk {
     __device__ __forceinline__ bool next(const Params& p) {
         while (f < f1) {
             const int all = v.cost<UNIT>();
-            if (t < all) {
-                const int take = static_cast<int>(min(static_cast<int64_t>(all - t), f1 - f));
+            const bool uncut = all <= kUncut<UNIT>;
+            if (t < all && !(uncut && t > 0)) {
+                const int take =
+                    uncut ? all : static_cast<int>(min(static_cast<int64_t>(all - t), f1 - f));
                 k = UNIT * t;
                 n = max(min(UNIT * (t + take), v.tiles()) - k, 0);
                 whole = take == all;
@@ -398,7 +413,7 @@ __device__ __forceinline__ void find_start(const Params& p, Control& ctl, int64_
 __device__ __forceinline__ bool wanted(const Params& p) {
     if (p.guard == nullptr) return true;
     int any = 0;
-    for (int i = threadIdx.x; i < kSms; i += blockDim.x) any |= p.guard[i];
+    for (int i = threadIdx.x; i < p.guards; i += blockDim.x) any |= p.guard[i];
     return __syncthreads_or(any) != 0;
 }
 
@@ -862,31 +877,31 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
 }
 
 // Joins the pieces of the units that were cut: CTA (x, y) looks at the cut before range x + 1, takes
-// the unit there if this is its first cut, and of it every gridDim.y-th eight rows.  A long sequence is cut into as
+// the unit there if this is its first cut, and of it every gridDim.y-th ROWS rows.  A long sequence is cut into as
 // many pieces as there are ranges to share it, so what costs is the way of their loads: a warp a
 // row finds the pieces' weights, while four elements of a row to a thread and a share of the pieces
 // are on their way already, a dozen pieces at a time.
 constexpr int kJoinThreads = 512;
 constexpr int kJoinPieces = 128;
 
-template <int HD, int R>
-__global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const Params p) {
+template <int HD, int R, int UNIT>
+__device__ __forceinline__ void join_pieces(const Params& p) {
     constexpr int V = HD / 4, kAtOnce = 12;
-    static_assert(8 * V <= kJoinThreads, "an element's thread");
-    __shared__ float weight[8][kJoinPieces];
-    __shared__ float shrink[8], top_of[8], sum_of[8];
+    // Few rows: eight, and many pieces.  Many rows: as many as there are threads for, few pieces.
+    constexpr int ROWS = R <= 16 ? 8 : kJoinThreads / V;
+    constexpr int kWarpRows = (ROWS + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+    __shared__ float weight[ROWS][kJoinPieces];
+    __shared__ float shrink[ROWS], top_of[ROWS], sum_of[ROWS];
     __shared__ float4 parts[kJoinThreads];
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (!wanted(p)) return;
     const int range = blockIdx.x + 1;
     const Start st = p.starts[range];
-    if (st.t == 0 || st.t >= st.cost) return;  // (no cut, or behind the tiles)
+    // (no cut, or behind the tiles, or in a unit that is not cut)
+    if (st.t == 0 || st.t >= st.cost || st.cost <= kUncut<UNIT>) return;
     const int64_t f = range * st.per - st.t;  // the unit's first tile
     if (divide(f, st.per) != range - 1) return;
     const int count = static_cast<int>(divide(f + st.cost - 1, st.per)) - range + 2;
-    for (int r0 = 8 * blockIdx.y; r0 < st.live; r0 += 8 * gridDim.y) {
-        const int rows = min(st.live - r0, 8);
+    for (int r0 = ROWS * blockIdx.y; r0 < st.live; r0 += ROWS * gridDim.y) {
+        const int rows = min(st.live - r0, ROWS);
         // piece 0 is the end of range - 1, piece k the beginning of range + k - 1
         auto part = [&](int k, int r) -> int64_t {
             return (k == 0 ? 2 * (range - 1) + 1 : 2 * (range + k - 1)) * static_cast<int64_t>(R) +
@@ -905,39 +920,47 @@ __global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const Params p) {
                     v[i] = *reinterpret_cast<const float4*>(p.part_o + part(k, row) * HD + col);
             }
         };
-        float top = -INFINITY, sum = 0.0f;  // of the warp's row
+        float top[kWarpRows], sum[kWarpRows];  // of the warp's rows
+#pragma unroll
+        for (int n = 0; n < kWarpRows; ++n) {
+            top[n] = -INFINITY;
+            sum[n] = 0.0f;
+        }
         for (int c0 = 0; c0 < count; c0 += kJoinPieces) {
             const int end = min(count, c0 + kJoinPieces);
             fetch(c0 + share, end);
-            if (warp < rows) {
+#pragma unroll
+            for (int n = 0; n < kWarpRows; ++n) {
+                const int r = warp + n * (kJoinThreads / 32);
+                if (r >= rows) break;
                 float2 ml[kJoinPieces / 32];
-                float most = top;
+                float most = top[n];
 #pragma unroll
                 for (int i = 0; i < kJoinPieces / 32; ++i) {
                     const int k = c0 + 32 * i + lane;
-                    ml[i] = k < end ? p.part_ml[part(k, warp)] : make_float2(0.0f, 0.0f);
+                    ml[i] = k < end ? p.part_ml[part(k, r)] : make_float2(0.0f, 0.0f);
                     if (ml[i].y != 0.0f) most = fmaxf(most, ml[i].x);
                 }
 #pragma unroll
                 for (int m = 1; m < 32; m <<= 1)
                     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
                 const float base = most == -INFINITY ? 0.0f : most;
-                const float less = top == -INFINITY ? 0.0f : ex2(top - base);
+                const float less = top[n] == -INFINITY ? 0.0f : ex2(top[n] - base);
                 float here = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kJoinPieces / 32; ++i) {
                     const float w = ml[i].y != 0.0f ? ex2(ml[i].x - base) : 0.0f;
                     if (ml[i].y != 0.0f) here = fmaf(w, ml[i].y, here);
-                    weight[warp][32 * i + lane] = w;
+                    weight[r][32 * i + lane] = w;
                 }
 #pragma unroll
                 for (int m = 1; m < 32; m <<= 1) here += __shfl_xor_sync(0xffffffffu, here, m);
-                sum = fmaf(sum, less, here);
-                top = most;
+                sum[n] = fmaf(sum[n], less, here);
+                top[n] = most;
                 if (lane == 0) {
-                    shrink[warp] = less;
-                    top_of[warp] = base;
-                    sum_of[warp] = sum;
+                    shrink[r] = less;
+                    top_of[r] = base;
+                    sum_of[r] = sum[n];
                 }
             }
             __syncthreads();
@@ -982,33 +1005,50 @@ __global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const Params p) {
     }
 }
 
+template <int HD, int R>
+__global__ void __launch_bounds__(kJoinThreads, 1) join_kernel(const Params p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    join_pieces<HD, R, 1>(p);
+}
+
+// The most tiles that a unit can have, as far as the host can tell.
+inline int64_t tiles_bound(const Params& p) {
+    const int64_t tiles = (p.total_blocks * p.bs + 15) / 16;
+    if (p.window >= kNoWindow) return tiles;
+    return std::min<int64_t>(tiles,
+                             (static_cast<int64_t>(p.window) + p.sinks + p.max_q) / 16 + 4);
+}
+inline int64_t row_tiles_bound(const Params& p, int rows) {
+    return (static_cast<int64_t>(p.max_q) * p.g + rows - 1) / rows;
+}
+
+// The attention of few rows without its join, which *joined says is needed.
 template <int HD, int NT>
-hss_status launch_rows(const Params& many_units, cudaStream_t stream) {
+hss_status launch_few(const Params& args, bool* joined, cudaStream_t stream) {
     using S = Shape<HD, NT>;
     auto kern = attend_kernel<HD, NT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes) !=
         cudaSuccess)
         return HSS_ERR_CUDA;
-    Params p = many_units;
-    int64_t tiles = (p.total_blocks * p.bs + 15) / 16;
-    if (p.window < kNoWindow)
-        tiles = std::min<int64_t>(
-            tiles, (static_cast<int64_t>(p.window) + p.sinks + p.max_q) / 16 + 4);
-    const int64_t row_tiles = (static_cast<int64_t>(p.max_q) * p.g + S::kRows - 1) / S::kRows;
+    Params p = args;
+    const int64_t row_tiles = row_tiles_bound(p, S::kRows);
     const int64_t units = p.num_seqs * row_tiles * p.nkv;
-    if (p.guard == nullptr && by_units(tiles, units)) {
-        p.row_tiles = static_cast<int32_t>(row_tiles);
-        return launch_pdl(kern, dim3(static_cast<unsigned>(units)), dim3(S::kThreads),
-                          S::kSmemBytes, stream, p) == cudaSuccess
-                   ? HSS_OK
-                   : HSS_ERR_CUDA;
-    }
-    p.row_tiles = 0;
-    if (launch_pdl(kern, dim3(S::kRanges), dim3(S::kThreads), S::kSmemBytes, stream, p) !=
-        cudaSuccess)
-        return HSS_ERR_CUDA;
-    return launch_pdl(join_kernel<HD, 8 * NT>, dim3(S::kRanges - 1, NT), dim3(kJoinThreads), 0,
-                      stream, p) == cudaSuccess
+    *joined = !by_units(tiles_bound(p), units);
+    p.row_tiles = *joined ? 0 : static_cast<int32_t>(row_tiles);
+    const dim3 grid(*joined ? S::kRanges : static_cast<unsigned>(units));
+    return launch_pdl(kern, grid, dim3(S::kThreads), S::kSmemBytes, stream, p) == cudaSuccess
+               ? HSS_OK
+               : HSS_ERR_CUDA;
+}
+
+template <int HD, int NT>
+hss_status launch_rows(const Params& p, cudaStream_t stream) {
+    bool joined;
+    const hss_status st = launch_few<HD, NT>(p, &joined, stream);
+    if (st != HSS_OK || !joined) return st;
+    return launch_pdl(join_kernel<HD, 8 * NT>, dim3(Shape<HD, NT>::kRanges - 1, NT),
+                      dim3(kJoinThreads), 0, stream, p) == cudaSuccess
                ? HSS_OK
                : HSS_ERR_CUDA;
 }

@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
     const uint32_t tmem = bar.tmem;
     grid_dependency_wait();
     grid_launch_dependents();
-    find_start<R, 4, M::kThreads>(p, ctl, 2);
+    if (p.row_tiles == 0) find_start<R, 4, M::kThreads>(p, ctl, 2);
     volatile int* abort_flag = &bar.abort;
 
     auto advance = [&](MyWalk& w) {
@@ -209,7 +209,14 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
         *abort_flag = 1;
     };
     MyWalk& walk = walks[warp];
-    if (lane == 0) walk.begin(p, ctl.start, ctl.seq, ctl.view);
+    if (lane == 0) {
+        if (p.row_tiles == 0) {
+            walk.begin(p, ctl.start, ctl.seq, ctl.view);
+        } else {
+            walk.begin_unit(p, blockIdx.x);
+            if (warp == 0 && walk.h == 0 && walk.rt == 0) report(p, walk.s, walk.x);
+        }
+    }
     bool ok = true;
 
     if (warp < 8) {
@@ -663,22 +670,45 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
     }
 }
 
+// What is left of a row in several pieces, of the kernel that did the work.
 template <int HD>
-hss_status launch_many(const Params& many, const Params& few, int32_t* flags,
+__global__ void __launch_bounds__(kJoinThreads, 1)
+    join_either_kernel(const Params many, const Params few, bool many_joined, bool few_joined) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (wanted(few)) {
+        if (few_joined && blockIdx.y < 2) join_pieces<HD, 16, 1>(few);
+    } else if (many_joined && blockIdx.x < kSms - 1) {
+        join_pieces<HD, Many<HD>::kRows, 4>(many);
+    }
+}
+
+template <int HD>
+hss_status launch_many(const Params& args, const Params& few, int32_t* flags,
                        cudaStream_t stream) {
     using M = Many<HD>;
     auto kern = many_kernel<HD>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, M::kSmemBytes) !=
         cudaSuccess)
         return HSS_ERR_CUDA;
-    if (launch_pdl(kern, dim3(kSms), dim3(M::kThreads), M::kSmemBytes, stream, many, flags) !=
-        cudaSuccess)
-        return HSS_ERR_CUDA;
-    if (launch_pdl(join_kernel<HD, M::kRows>, dim3(kSms - 1, 4), dim3(kJoinThreads), 0, stream,
-                   many) != cudaSuccess)
+    Params many = args, guarded = few;
+    const int64_t row_tiles = row_tiles_bound(many, M::kRows);
+    const int64_t units = many.num_seqs * row_tiles * many.nkv;
+    const bool many_joined = !many_by_units(tiles_bound(many), units);
+    many.row_tiles = many_joined ? 0 : static_cast<int32_t>(row_tiles);
+    guarded.guards = many_joined ? kSms : static_cast<int32_t>(units);
+    if (launch_pdl(kern, dim3(guarded.guards), dim3(M::kThreads), M::kSmemBytes, stream, many,
+                   flags) != cudaSuccess)
         return HSS_ERR_CUDA;
     // (does nothing unless a scale did not fit)
-    return launch_rows<HD, 2>(few, stream);
+    bool few_joined;
+    const hss_status st = launch_few<HD, 2>(guarded, &few_joined, stream);
+    if (st != HSS_OK || (!many_joined && !few_joined)) return st;
+    return launch_pdl(join_either_kernel<HD>, dim3(Shape<HD, 2>::kRanges - 1, 8),
+                      dim3(kJoinThreads), 0, stream, many, guarded, many_joined,
+                      few_joined) == cudaSuccess
+               ? HSS_OK
+               : HSS_ERR_CUDA;
 }
 
 }  // namespace packed
