@@ -1,22 +1,37 @@
 // attend_packed.cuh -- attention of few rows over the packed cache: one pass over 4-bit tiles with
-// warp-level matrix products.
+// warp-level matrix products; and the join that many rows (attend_packed_tc.cuh) share.
 //
 // A row is a (query row, query head of the group) pair; the rows of one sequence that share a kv
 // head are taken R = 8 NT at a time.  Over the tokens they see, in tiles of 16,
 //   S^T = K Q^T,  P = exp2(c S - m),  O^T = V^T P^T,  l = sum P
 // with mma.m16n8k16: tokens (of V^T: elements) are the 16 rows of the product and query rows its 8
 // columns, so that K and V, which are what there is much of, are the operand that goes from packed
-// words straight into registers, and eight query rows fill an instruction.  A group's scale
-// multiplies what the group adds to S, and for V the weight of its token: P is scaled, rounded to
-// bf16 and transposed (movmatrix) once for each group of 32 elements.
+// words straight into registers, and eight query rows fill an instruction.  (tcgen05 would want
+// 128 rows and its operands in shared memory, where this kernel keeps nothing but the packed bytes.)
+// A group's scale multiplies what the group adds to S, and for V the weight of its token: P is
+// scaled, rounded to bf16 and transposed (movmatrix) once for each group of 32 elements.
 //
 // The maximum m lags: it is one for the whole warp and a row, and moves only when a score passes it
 // by 2^8, so that a tile costs a vote and no shuffles.
 //
 // Split.  All (sequence, row tile, kv head, tile) form one list, cut into equal contiguous ranges, a
-// CTA each.  Within a CTA the warps take the tiles of a unit (sequence, row tile, head) in turn,
-// each with a ring of its own that its asynchronous copies fill, and put m, l and O together in shared memory at the unit's end or the range's.  What a range does not have whole
-// goes to the workspace and a second kernel joins it.
+// CTA each (two to an SM).  Within a CTA the warps take the tiles of a unit (sequence, row tile,
+// head) in turn, each with a ring of its own that its asynchronous copies fill, and put m, l and O
+// together in shared memory at the unit's end or the range's.  What a range does not have whole goes
+// to the workspace and a second kernel joins it.  Short units are not cut, and if all are short there
+// is no list: a CTA takes a unit.
+//
+// What bounds it, and what it reaches on GB300 (HBM 6.8 TB/s measured): instructions.  A tile of 16
+// tokens of one head takes 300 of them for its 2304 bytes, of which the cache's bandwidth leaves
+// time for 390 at the full rate; 12 warps an SM issue 54 % (ncu), more of them with fewer registers
+// each were slower (16: 154 us where 12 take 145).  64 sequences of 1k to 16k tokens, 32 query heads on
+// 8 of 128: 143 us, 4.5 TB/s; 152 sequences of 4096 tokens 154 us, their copies alone 116.  One of
+// 32768 tokens 22.6 us: 6 of them its tiles, the rest one way through memory after another (lengths,
+// block ids, first tiles, pieces, join).  One of 500 tokens 11 us.
+// What helped, on those 64 sequences: nibbles into the products without shifts for half of them,
+// exact as bf16 counts them (240 to 193 us), scores begun with what the nibbles' 8 comes to, two tiles
+// a step and twelve warps (160), cp.async without barriers in place of bulk copies (the same step),
+// and units that weigh more than their tiles (143).
 #pragma once
 
 #include <algorithm>

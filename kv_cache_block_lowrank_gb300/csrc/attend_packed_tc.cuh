@@ -21,6 +21,15 @@
 // softmax, four to a row tile, with registers that the others hand over.  One row tile's exponentials run under the other's products.
 //
 // Split: as for few rows (attend_packed.cuh), the list counted in jobs.
+//
+// What bounds it, and what it reaches: shared memory.  A job of two row tiles reads Q (64 KB), K and V
+// (64 KB for both) from it and writes 32 KB of decoded operands, 1300 cycles at 128 bytes a cycle,
+// where the products alone take 1000 to 1250 and the exponentials 1000; it takes 2000.  512 rows of 64
+// heads over 32768 tokens 511 us, 1.08 PFLOP/s, 56 % of what a large bf16 product reaches (over a bf16
+// cache hss_attend_tree takes 211 us for half the context).  Steps there: four warps that copied and
+// decoded 1310 us; eight that hand scales on by shuffles 825; a warp of its own for the copies 537
+// (their issue, 64-bit addresses and divisions in it, had taken 1500 of a job's 3400 cycles); a join of
+// 16 rows at a time 511.  Tried and not kept: waiting for a job's operands before its weights (554).
 #pragma once
 
 #include <cuda_fp16.h>

@@ -8,7 +8,11 @@
 // and store follow without the element leaving its register.  Everything is fp32 until the one
 // rounding at the end.
 //
-// What bounds it: few tokens, the launch; many, HBM.
+// What bounds it: few tokens, the launch (16 tokens 4.8 us); many, HBM and the instructions beside
+// it: 8192 tokens of 64 + 8 turned heads of 128, each with weights, 59 to 62 us, 5.4 TB/s, 80 % of the
+// copy rate; 1070 instructions a warp and token, issued at 66 % of the rate (ncu).  Four CTAs of 256
+// threads an SM by the registers (64) and four items a thread in flight: with 80 registers 66 us, two
+// items and 320 threads 63, one and 640 70.  Packed fp32 operations changed nothing (64).
 #include <cuda_runtime.h>
 
 #include "ptx.cuh"

@@ -10,7 +10,9 @@
 // and go out (or come in) as whole 16-byte pieces of the page; V's bytes, which hold a token each,
 // change places with the elements in shared memory.  What else there is goes token by token.
 //
-// What bounds it: few tokens, the launch; many, HBM and the divisions.
+// What bounds it: few tokens, the launch (64 tokens 4 us to pack and 4 to read back); many, latency:
+// 8191 tokens of 8 heads of 128, packed and read back, 33 to 36 us for 86 MB, 2.6 TB/s, token by token
+// 43; ncu shows 62 % of the issue rate and 40 % of the warps there can be.
 #include <cuda_runtime.h>
 
 #include "packed.cuh"
