@@ -719,12 +719,13 @@ size_t hss_attend_packed_workspace_bytes(const hss_dims* dims, int32_t num_seqs,
  * num_kv_heads, by max_q): a weight times its value's scale enters the product with the codes
  * rounded to bf16; an element of out is off by at most 2^-8 sum_p exp(s - lse) |v_p| for it, beside
  * the rounding of out itself.  More rows run on the tensor cores of tcgen05 with K, V and the weights
- * in fp16: K and V lose nothing, a weight 2^-12 of itself at most.  There a scale that fp16 has no
+ * in fp16: K and V lose nothing, a weight 2^-11 of itself at most.  There a scale that fp16 has no
  * place for (above 64, or below 2^-17 but not 0, or not finite) makes the whole call run by the
  * first method after all, which is correct for every scale but several times slower.
- * The join of what several CTAs have of a row follows the attention itself on the stream, for many
- * rows with the two launches of that second attempt, which end at once if it is not needed.  A
- * pipeline wait that runs out raises HSS_ERR_DEVICE_TIMEOUT like those of the other kernels.
+ * A call is one to three launches on the stream: for few rows the attention and, unless contexts are
+ * short, the join of what several CTAs have of a row; for many rows the attention, that second
+ * attempt, which ends at once if it is not needed, and at most one join for both.  A pipeline wait
+ * that runs out raises HSS_ERR_DEVICE_TIMEOUT like those of the other kernels.
  * Single tokens in one call with a chunk of many rows cost as much as row tiles of 128: call them
  * apart.
  * Supported: num_q_heads / num_kv_heads <= 128, at most 2^30 rows of a sequence and kv head

@@ -25,8 +25,9 @@
 // tokens of one head takes 300 of them for its 2304 bytes, of which the cache's bandwidth leaves
 // time for 390 at the full rate; 12 warps an SM issue 54 % (ncu), more of them with fewer registers
 // each were slower (16: 154 us where 12 take 145).  64 sequences of 1k to 16k tokens, 32 query heads on
-// 8 of 128: 143 us, 4.5 TB/s; 152 sequences of 4096 tokens 154 us, their copies alone 116.  One of
-// 32768 tokens 22.6 us: 6 of them its tiles, the rest one way through memory after another (lengths,
+// 8 of 128: 143 us, 4.5 TB/s; 152 sequences of 4096 tokens 154 us (a copy of an earlier
+// version without its arithmetic, 116).  One of
+// 32768 tokens 22.6 us: its tiles are 5.6 at HBM's rate, the rest is one way through memory after another (lengths,
 // block ids, first tiles, pieces, join).  One of 500 tokens 11 us.
 // What helped, on those 64 sequences: nibbles into the products without shifts for half of them,
 // exact as bf16 counts them (240 to 193 us), scores begun with what the nibbles' 8 comes to, two tiles
@@ -892,8 +893,8 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
 }
 
 // Joins the pieces of the units that were cut: CTA (x, y) looks at the cut before range x + 1, takes
-// the unit there if this is its first cut, and of it every gridDim.y-th ROWS rows.  A long sequence is cut into as
-// many pieces as there are ranges to share it, so what costs is the way of their loads: a warp a
+// the unit there if this is its first cut, and of it every gridDim.y-th ROWS rows.  A long sequence is
+// cut into as many pieces as there are ranges to share it, so what costs is the way of their loads: a warp a
 // row finds the pieces' weights, while four elements of a row to a thread and a share of the pieces
 // are on their way already, a dozen pieces at a time.
 constexpr int kJoinThreads = 512;
@@ -1011,7 +1012,8 @@ __device__ __forceinline__ void join_pieces(const Params& p) {
             const int64_t to = (static_cast<int64_t>(st.q0) + r / p.g) * p.nq + st.h * p.g + r % p.g;
             uint2 u = make_uint2(0, 0);
             if (l != 0.0f)
-                u = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                u = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                               pack_bf16x2(acc.z * inv, acc.w * inv));
             *reinterpret_cast<uint2*>(p.out + to * HD + col) = u;
             if (col == 0 && p.lse != nullptr)
                 p.lse[to] = l == 0.0f ? -INFINITY : (top_of[row] + log2f(l)) * 0.693147180559945309f;

@@ -3,7 +3,7 @@
 // Row tiles of 128 rows (one or two to a CTA) against jobs of 64 tokens:
 //   S = Q K^T,  P = exp2(c S - m),  O = P V,  l = sum P
 // with S and O in tensor memory, a row to a lane, P written back over S as the first operand of the
-// second product.  Four warps decode a job's packed tiles, once for both row tiles, into shared
+// second product.  Eight warps decode a job's packed tiles, once for both row tiles, into shared
 // memory as the tensor cores read them:
 //   - in fp16, where a bf16 scale (8 bits) times a code (3 bits) has a place for every bit, so that
 //     K and V enter the products exactly.  Scales outside [2^-17, 2^6] (but for 0), or not finite,
@@ -18,15 +18,16 @@
 // the product with V, in l as it is.
 //
 // Roles (20 warps): 10 copies; 0-7 decode; 8, 9 issue the products of a row tile each; 12-19
-// softmax, four to a row tile, with registers that the others hand over.  One row tile's exponentials run under the other's products.
+// softmax, four to a row tile, with registers that the others hand over.  One row tile's exponentials
+// run under the other's products.
 //
 // Split: as for few rows (attend_packed.cuh), the list counted in jobs.
 //
 // What bounds it, and what it reaches: shared memory.  A job of two row tiles reads Q (64 KB), K and V
 // (64 KB for both) from it and writes 32 KB of decoded operands, 1300 cycles at 128 bytes a cycle,
 // where the products alone take 1000 to 1250 and the exponentials 1000; it takes 2000.  512 rows of 64
-// heads over 32768 tokens 511 us, 1.08 PFLOP/s, 56 % of what a large bf16 product reaches (over a bf16
-// cache hss_attend_tree takes 211 us for half the context).  Steps there: four warps that copied and
+// heads over 32768 tokens 511 us in a graph, 1.08 PFLOP/s, 56 % of what a large bf16 product reaches (over a bf16
+// cache hss_attend_tree takes 209 us for half the context).  Steps there: four warps that copied and
 // decoded 1310 us; eight that hand scales on by shuffles 825; a warp of its own for the copies 537
 // (their issue, 64-bit addresses and divisions in it, had taken 1500 of a job's 3400 cycles); a join of
 // 16 rows at a time 511.  Tried and not kept: waiting for a job's operands before its weights (554).
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
                         const float e = ex2(fmaf(__uint_as_float(x[2 * d + 1]), c, -base));
                         sum0 += a;
                         sum1 += e;
-                        // (fp16, as V: a weight is off by up to 2^-12 of itself)
+                        // (fp16, as V: a weight is off by up to 2^-11 of itself)
                         packed[d] = half2_bits(a, e);
                     }
                     l += sum0 + sum1;

@@ -273,6 +273,22 @@ def test_scales_that_fp16_has_no_place_for(hd, value, scale):
         assert torch.isfinite(out.cpu()[30:].float()).all()
 
 
+@pytest.mark.parametrize("hd,value,scale", [
+    (64, True, 1000.0), (128, False, 2.0 ** -20), (192, True, 1000.0), (256, False, 2.0 ** -20)])
+def test_such_a_scale_in_a_long_context(hd, value, scale):
+    """The same where several CTAs share a row, so that the second attempt's pieces are joined."""
+    c = Case(hd, 8, 2, 16, [5000, 3], [70, 12])
+    cache = c.cache.clone()
+    at = 2 * P.scale_place(4000 % 16, 1, hd, value)
+    tile = cache[c.table[4000 // 16].item()].view(-1)
+    tile[at:at + 2] = torch.tensor([scale], dtype=torch.bfloat16, device=DEV).view(torch.uint8)
+    out, lse = c.call(cache=cache)
+    torch.cuda.synchronize()
+    assert hss.hss_read_device_error() == 0
+    c.check(out, lse, cache=cache)
+    assert torch.equal(out, c.call(cache=cache)[0])
+
+
 def test_device_errors_hide_tokens():
     c = Case(128, 4, 2, 16, [100, 60], [2, 2])
     table = c.table.clone()
