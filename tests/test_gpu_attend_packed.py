@@ -376,6 +376,39 @@ def test_captured_replayed_and_on_two_streams():
             x.check(*y)
 
 
+@pytest.mark.parametrize("hd,rows", [(128, [1, 1]), (64, [2, 1]), (128, [70, 12])])
+def test_long_contexts_replayed_with_other_lengths_and_scales(hd, rows):
+    """A graph over one workspace follows the lengths and the cache from replay to replay: nothing is
+    left of a replay that cut its sequences elsewhere or that had to run by the other method."""
+    c = Case(hd, 8, 2, 16, [5000, 900], rows)
+    c.call()
+    ctx = torch.tensor(c.ctx, dtype=torch.int32, device=DEV)
+    size = hss.hss_attend_packed_workspace_bytes(c.dims, 2, c.max_q, c.total, 0, 0)
+    work = torch.full((size,), 0xFF, device=DEV, dtype=torch.uint8)
+    call = hss.AttendPacked(c.dims, c.q_offs.to(DEV), c.total_q, c.max_q, c.table.to(DEV),
+                            c.offs.to(DEV), ctx, 2, c.total, 0, 0, c.scale, work, size)
+    out, lse = torch.empty_like(c.q), torch.empty(c.total_q, c.nq, device=DEV)
+    at = 2 * P.scale_place(3, 0, hd, True)
+    tile = c.cache[c.table[1].item()].view(-1)      # tokens 16 to 31 of the first sequence
+    fit = tile[at:at + 2].clone()
+    unfit = torch.tensor([1000.0], dtype=torch.bfloat16, device=DEV).view(torch.uint8)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(c.q, c.cache, out, lse)
+    for lengths, scale in (([5000, 900], fit), ([40, 0], unfit), ([5000, 900], unfit),
+                           ([0, 900], fit), ([4987, 1], fit)):
+        c.ctx = lengths
+        ctx.copy_(torch.tensor(lengths, dtype=torch.int32))
+        tile[at:at + 2] = scale
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert hss.hss_read_device_error() == 0
+        c.check(out, lse)
+
+
 def test_pages_past_32_bits():
     """Pages whose bytes lie behind the first 2^32 of the cache."""
     hd, nkv, bs = 128, 8, 256
