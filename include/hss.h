@@ -775,9 +775,10 @@ size_t hss_compact_pages_workspace_bytes(int64_t max_blocks);
  * an id outside [0, max_blocks) in a present table or (but for -1) in released, which is counted
  * nowhere and kept as it is.  If there are not enough free pages, the last entries are -1 (a copy
  * to such an entry has copy_dst -1) and HSS_ERR_OUT_OF_RANGE is raised; if the new tables need more
- * than table_room entries, HSS_ERR_INVALID_ARGUMENT is, and nothing but counts[0] and new_offsets
- * is then of use; so is it if a page has a smaller count than the present tables and released give
- * up of it, and its page may then be handed out.
+ * than table_room entries, HSS_ERR_INVALID_ARGUMENT is, nothing but counts[0] and new_offsets is
+ * then of use, and every copy_dst is -1.  HSS_ERR_INVALID_ARGUMENT is raised as well if a page has a
+ * smaller count than the present tables and released give up of it; the page may then be handed out
+ * although it is held.
  * num_seqs, num_new <= 2^20, total_blocks, table_room, num_released, max_blocks <= 2^30.
  */
 hss_status hss_fork_pages(const int32_t* block_table, const int32_t* seq_offsets,

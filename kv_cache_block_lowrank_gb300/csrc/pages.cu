@@ -279,9 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fresh_before[i] = clip(fresh);
         copy_before[i] = copy ? -1 - static_cast<int32_t>(copies) : 0;
         if (copy) {
-            const int32_t page = written_page(x);
-            f.copy_src[copies] = page;
-            atomicSub(f.new_refs + page, 1);  // (others hold it still: no page becomes free here)
+            f.copy_src[copies] = written_page(x);
+            f.copy_dst[copies] = -1;  // (what it stays if the tables do not fit)
         }
         fresh += x.n - x.kept + (copy ? 1 : 0);
         copies += copy ? 1 : 0;
@@ -298,7 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     cluster.sync();
 
-    // The new tables.
+    // The new tables; and the old pages of the copies lose a reference.  (Not while the free pages are
+    // listed: given counts that are too small, a page that was counted as free could then be missing
+    // from the list, and a word of it that nobody wrote would be taken for an id.)
+    for (int i = i0; i < i1; ++i)
+        if (copy_before[i] < 0) atomicSub(f.new_refs + written_page(heir_of(f, i)), 1);
     for (int64_t e = at; e < f.table_room; e += stride) {
         if (e >= table_end) {
             f.new_table[e] = -1;
@@ -317,7 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t k = __ldcg(fresh_before + i) + (j - first_fresh);
             id = k < free_all ? __ldcg(free_list + k) : -1;
             if (id >= 0) f.new_refs[id] = 1;
-            if (mark < 0 && j == first_fresh) f.copy_dst[-1 - mark] = id;
+            // (without room for all, pages that the missing entries hold are not known as held)
+            if (mark < 0 && j == first_fresh && new_total <= f.table_room)
+                f.copy_dst[-1 - mark] = id;
         }
         f.new_table[e] = id;
     }

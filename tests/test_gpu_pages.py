@@ -62,7 +62,8 @@ def plan_fork(tables, refs, released, parents, lengths, room, bs):
     return new, refs, copies, missing
 
 
-def run_fork(tables, refs, released, parents, lengths, room, bs, table_room=None, total=None):
+def run_fork(tables, refs, released, parents, lengths, room, bs, table_room=None, total=None,
+             fill=0xEE):
     flat = [p for t in tables for p in t]
     offs = np.cumsum([0] + [len(t) for t in tables])
     need = sum(-(-(min(max(n, 0), len(tables[p]) * bs if 0 <= p < len(tables) else 0)
@@ -75,14 +76,14 @@ def run_fork(tables, refs, released, parents, lengths, room, bs, table_room=None
            dict(table=table_room, offs=new + 1, refs=len(refs), src=new, dst=new,
                 counts=4).items()}
     size = hss.hss_fork_pages_workspace_bytes(new, len(refs))
-    work = torch.full((size + 8,), 0xEE, dtype=torch.uint8, device=DEV)
+    work = torch.full((size + 8,), fill, dtype=torch.uint8, device=DEV)
     status = torch.zeros(1, **I32)
     hss.hss_fork_pages(t(flat), t(offs), len(tables), len(flat), t(refs), len(refs),
                        t(released) if len(released) else None, len(released), t(parents),
                        t(lengths), t(room), new, bs, table_room, out["table"], out["offs"],
                        out["refs"], out["src"], out["dst"], out["counts"], work, size, status)
     torch.cuda.synchronize()
-    assert (work[size:] == 0xEE).all()
+    assert (work[size:] == fill).all()
     got = {}
     for k, v in out.items():
         v = v.tolist()
@@ -187,6 +188,33 @@ def test_fork_errors():
     # nothing at all
     got, status, _ = run_fork([], [0, 2], [], [], [], [], 16, table_room=2)
     assert status == 0 and got["table"] == [-1, -1] and got["counts"] == [0, 0, 1, 0]
+
+
+@pytest.mark.parametrize("held,writers,pages", [(2, 2, 4), (3, 2, 40), (2, 5, 5000), (40, 41, 9000)])
+def test_fork_counts_too_small(held, writers, pages):
+    """Counts below what the tables give up are an error, and every id is still one of the pool's,
+    whatever the workspace held (here words that read as ids far behind it)."""
+    tables = [[1]] * held + [[3]]
+    parents = [0] * writers + [held]
+    for count in range(-1, held):
+        refs = [0] * pages
+        refs[1], refs[3] = count, 1
+        room = [1] * writers + [16 * pages]        # all that is free is handed out
+        got, status, _ = run_fork(tables, refs, [], parents, [5] * writers + [16], room, 16,
+                                  fill=0x7F)
+        assert status in (hss.HSS_ERR_INVALID_ARGUMENT, hss.HSS_ERR_OUT_OF_RANGE)
+        assert all(-1 <= p < pages for k in ("table", "src", "dst") for p in got[k])
+    hss.hss_read_device_error()
+
+
+def test_fork_without_room_for_the_table():
+    """Copies into entries that the new table has no room for have nowhere to go."""
+    got, status, _ = run_fork([[1, 2]], [0, 1, 1, 0, 0, 0], [], [0, 0, 0], [20] * 3, [1] * 3, 16,
+                              table_room=2)
+    assert status == hss.HSS_ERR_INVALID_ARGUMENT
+    assert got["counts"][0] == 6 and got["offs"] == [0, 2, 4, 6]
+    assert got["dst"] == [-1] * 3
+    hss.hss_read_device_error()
 
 
 def run_compact(table, refs, move_room):
