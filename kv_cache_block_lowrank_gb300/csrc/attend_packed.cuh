@@ -71,7 +71,7 @@ constexpr int kUncut = UNIT == 1 ? 48 : 20;
 // and 143 us; 16 windows of 4093 tokens with an empty sequence among them 62, 54, 41 and 35.)
 template <int UNIT>
 constexpr int kBeside = UNIT == 1 ? 32 : 6;
-constexpr int kScanWarps = 16;
+constexpr int kScanWarps = 20;      // of the largest CTA that looks for its range
 constexpr int kMostSlots = 4;       // of a warp's ring
 constexpr int kControlBytes = 2048;  // barriers, and from 512 on the warps' walks
 
@@ -358,6 +358,7 @@ static_assert(sizeof(Control) <= 512, "control block");
 // Where every CTA's range begins, from a scan of the sequences' lengths.
 template <int R, int UNIT, int THREADS>
 __device__ __forceinline__ void find_start(const Params& p, Control& ctl, int64_t least) {
+    static_assert(THREADS % 32 == 0 && THREADS / 32 <= kScanWarps, "a sum for every warp");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int each = (p.num_seqs + THREADS - 1) / THREADS;
     const int s0 = min(static_cast<int>(threadIdx.x) * each, p.num_seqs);
