@@ -680,7 +680,7 @@ typedef struct hss_packed_args {
     const int32_t* ctx_len;     /* device, [num_seqs]: cached tokens before the rows */
     int64_t total_blocks;
     int32_t num_seqs;
-    float scale;                /* factor on the scores, finite; usually head_dim^-0.5 */
+    float scale;                /* factor on the scores, -2^100 .. 2^100; usually head_dim^-0.5 */
     void* workspace;            /* device, 256-byte aligned,
                                    hss_attend_packed_workspace_bytes(...); what it holds does not
                                    matter.  Calls that share one must not run at the same time. */

@@ -72,6 +72,7 @@ constexpr int kUncut = UNIT == 1 ? 48 : 20;
 template <int UNIT>
 constexpr int kBeside = UNIT == 1 ? 32 : 6;
 constexpr int kScanWarps = 20;      // of the largest CTA that looks for its range
+constexpr int kRowWarps = 6;         // of a CTA that takes few rows
 constexpr int kMostSlots = 4;       // of a warp's ring
 constexpr int kControlBytes = 2048;  // barriers, and from 512 on the warps' walks
 
@@ -113,7 +114,7 @@ struct Shape {
     static constexpr int kRows = 8 * NT;
     // Few rows: nibbles go into the products as they are (see raw_codes), two tiles at a time.
     static constexpr bool kRaw = NT == 1 && HD <= 128;
-    static constexpr int kWarps = kRaw ? 6 : 4;
+    static constexpr int kWarps = kRaw ? kRowWarps : 4;
     static constexpr int kTiles = kRaw ? 2 : 1;  // of a step, and of a ring's slot
     static constexpr int kCtas = 2;   // of an SM
     static constexpr int kRanges = kSms * kCtas;
@@ -352,6 +353,7 @@ struct alignas(8) Control {
     SeqInfo seq;  // of the unit where the range begins
     View view;
     int64_t scan[kScanWarps];
+    alignas(8) float rest[kRowWarps][8];  // [warp][row] a part of a factor that is past fp32
 };
 static_assert(sizeof(Control) <= 512, "control block");
 
@@ -585,6 +587,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
         // What a sum of products times scales is multiplied with, of rows 2 c and 2 c + 1.
         float factor[NT][2];
         float first[RAW ? NG : 1][4];  // what the sums begin with
+        bool far = false;  // factors in two parts, the first in shared memory
         if constexpr (RAW) {
             // A row times 2^n, so that its largest element lies at 2^119: products with steps of
             // 2^-133 are then ordinary numbers.
@@ -612,6 +615,18 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
             for (int e = 0; e < 2; ++e) {
                 const int m = 133 - __shfl_sync(0xffffffffu, n, 4 * (2 * c + e));
                 factor[0][e] = p.c * pow2(min(m, 127)) * pow2(max(m - 127, 0));
+                far |= isinf(factor[0][e]);
+            }
+            // A row that large (from 2^117 on, with the usual scale) times small keys may have scores
+            // of ordinary size.  (|c| <= 2^101, so that neither part is past fp32.)
+            far = __any_sync(0xffffffffu, far);
+            if (far) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int m = 133 - __shfl_sync(0xffffffffu, n, 4 * (2 * c + e));
+                    factor[0][e] = pow2(max(m - 26, 0));
+                    if (g == 0) ctl.rest[warp][2 * c + e] = p.c * pow2(min(m, 26));
+                }
             }
         } else {
 #pragma unroll
@@ -686,6 +701,13 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
                         s[u][i][3] = G == 0 ? d[3] * f1 : fmaf(d[3], f1, s[u][i][3]);
                     }
                 }
+            }
+            if (RAW && far) {
+                const float2 rest = *reinterpret_cast<const float2*>(&ctl.rest[warp][2 * c]);
+#pragma unroll
+                for (int u = 0; u < TT; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[u][0][e] *= e & 1 ? rest.y : rest.x;
             }
             // What a row does not see goes to -inf, and its weight below to a plain 0.
             uint32_t hidden = 0;  // bit 4 (NT u + i) + e: s[u][i][e]

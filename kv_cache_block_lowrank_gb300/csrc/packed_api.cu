@@ -11,6 +11,7 @@ namespace {
 
 constexpr int64_t kMostPages = int64_t{1} << 30;
 constexpr int32_t kMostSeqs = 1 << 20;
+constexpr float kMostScale = 0x1p100f;  // (the kernels multiply it by what a row was shifted by)
 
 bool misaligned(const void* p, uintptr_t to) {
     return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0;
@@ -86,7 +87,7 @@ hss_status hss_attend_packed(const hss_packed_args* args, const uint16_t* Q, con
     if (args->num_seqs < 0 || args->max_q < 0 || outside(args->total_q, 0x7FFFFFFF) ||
         outside(args->total_blocks, 0x7FFFFFFF) || args->window < 0 || args->sinks < 0 ||
         args->total_q > static_cast<int64_t>(args->num_seqs) * args->max_q ||
-        (args->num_seqs == 0 && args->total_blocks != 0) || !std::isfinite(args->scale))
+        (args->num_seqs == 0 && args->total_blocks != 0) || !(std::fabs(args->scale) <= kMostScale))
         return HSS_ERR_INVALID_ARGUMENT;
     // (rows of one kv head are counted in 32 bits)
     if (std::min<int64_t>(args->max_q, args->total_q) * (d.num_q_heads / d.num_kv_heads) >

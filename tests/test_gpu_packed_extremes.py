@@ -1,0 +1,48 @@
+"""The packed cache's attention of queries, factors and values near the ends of fp32's range, against
+64 bits (packed_check.py has the tolerances)."""
+import numpy as np
+import pytest
+import torch
+
+import kv_cache_block_lowrank_gb300 as hss
+import packed_util as P
+from packed_check import check
+from test_gpu_attend_packed import DEV, Case, built  # noqa: F401  (the library, built once)
+
+pytestmark = pytest.mark.gpu
+
+
+def scales_of(c, value):
+    """The scales of K or V of all tiles, a view of the cache."""
+    words = c.cache.view(torch.bfloat16).view(-1, 9 * c.hd)
+    n = 16 * (c.hd // 32)
+    return words[:, 8 * c.hd + (n if value else 0):][:, :n]
+
+
+@pytest.mark.parametrize("hd,up,down,scale", [
+    (64, 112, -112, None), (64, 117, -117, None), (128, 118, -118, None), (64, 114, -117, 1.0),
+    (128, 120, -120, 0.01), (128, 126, -118, None), (64, 100, -117, 2.0 ** 17),
+    (128, 113, -60, 2.0 ** -55), (64, 60, -117, 2.0 ** 57), (192, 118, -118, None),
+    (256, 120, -120, -0.05)])
+@pytest.mark.parametrize("ctx", [[300, 7], [5000, 40]])
+def test_queries_of_any_size(hd, up, down, scale, ctx):
+    """Queries of 2^up over keys of 2^down; rows of other sizes beside them."""
+    c = Case(hd, 4, 2, 16, ctx, [2, 1], scale=scale)
+    scales_of(c, False).mul_(2.0 ** down)
+    size = torch.tensor([up, up, up - 3, -126], device=DEV).double().exp2()
+    c.q = (c.q.double().clamp(-1.9, 1.9) * size[None, :, None]).bfloat16()
+    assert torch.isfinite(c.q).all()
+    out, lse = c.call()
+    torch.cuda.synchronize()
+    assert hss.hss_read_device_error() == 0
+    check(c, out, lse)
+
+
+def test_one_large_query_among_ordinary_ones():
+    """Its scores are finite and the largest takes all.  (Its neighbours' bits may differ from those
+    without it: the maximum that weights go by moves for all rows of a warp at once.)"""
+    c = Case(128, 4, 1, 16, [700], [2])
+    c.q[0, 2] = (c.q[0, 2].double() * 2.0 ** 118).bfloat16()
+    out, lse = c.call()
+    torch.cuda.synchronize()
+    check(c, out, lse)
