@@ -11,8 +11,8 @@
 // A group's scale multiplies what the group adds to S, and for V the weight of its token: P is
 // scaled, rounded to bf16 and transposed (movmatrix) once for each group of 32 elements.
 //
-// The maximum m lags: it is one for the whole warp and a row, and moves only when a score passes it
-// by 2^8, so that a tile costs a vote and no shuffles.
+// m is 8 above a row's maximum (in powers of two) and lags: it is one for the whole warp and a row, and
+// moves only when a score passes it, so that a tile costs a vote and no shuffles.
 //
 // Split.  All (sequence, row tile, kv head, tile) form one list, cut into equal contiguous ranges, a
 // CTA each (two to an SM).  Within a CTA the warps take the tiles of a unit (sequence, row tile,
@@ -642,8 +642,9 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
         const int open_end = min(v.at0, tokens - 1) - 15;  // the last open tile's position
         const int window_end = v.at1 - p.window;
         int at[NT][2];  // positions of rows 8 i + 2 c and the next
-        // The maximum of a row that its weights go by (0 before there is one), and the score that
-        // moves it.
+        // What is taken from a row's scores (0 before there is a maximum), and the score that moves it:
+        // 8 above the maximum when it was last looked at, so that no weight is above 1 and its product
+        // with a scale is never past the scale.
         float base[NT][2], limit[NT][2];
         float l[NT][2], o[NT][HD / 16][4];
 #pragma unroll
@@ -749,16 +750,15 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
                             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, k));
                         // (the same for all lanes of the row; the limit is -inf before any score)
                         const bool none = limit[i][e] == -INFINITY;
-                        if (t > (none ? -INFINITY : base[i][e])) {
-                            const float shrink = none ? 0.0f : ex2(base[i][e] - t);
+                        if (t > (none ? -INFINITY : base[i][e] - kLazy)) {
+                            const float shrink = none ? 0.0f : ex2(base[i][e] - (t + kLazy));
                             l[i][e] *= shrink;
 #pragma unroll
                             for (int d = 0; d < HD / 16; ++d) {
                                 o[i][d][e] *= shrink;
                                 o[i][d][e + 2] *= shrink;
                             }
-                            base[i][e] = t;
-                            limit[i][e] = t + kLazy;
+                            base[i][e] = limit[i][e] = t + kLazy;
                         }
                     }
             }

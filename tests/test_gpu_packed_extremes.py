@@ -46,3 +46,28 @@ def test_one_large_query_among_ordinary_ones():
     out, lse = c.call()
     torch.cuda.synchronize()
     check(c, out, lse)
+
+
+@pytest.mark.parametrize("hd,nq", [(64, 2), (128, 8), (64, 12), (192, 1), (256, 4)])
+@pytest.mark.parametrize("ctx", [900, 3000])
+def test_values_near_the_end(hd, nq, ctx):
+    """Weights that are 2^7.5 times those of the first tokens, over values of up to 2^125."""
+    c = Case(hd, nq, 1, 16, [ctx], [1])
+    scales_of(c, True).mul_(2.0 ** 122)
+    c.q[:] = c.q[0, 0].clone()
+    table = c.table.numpy()
+    t = np.arange(200, ctx, 7)
+    slots = table[t // 16] * 16 + t % 16
+    k, _ = P.read_tokens(c.cache, 1, 16, hd, slots)
+    score = k[:, 0] @ c.q[0, 0].double().cpu().numpy() * c.scale / np.log(2)
+    few = np.flatnonzero(score > 1.0)[:8]
+    assert len(few) >= 3
+    keys = scales_of(c, False)
+    old = keys.clone().view(c.max_blocks * 16, hd // 32)
+    keys.zero_()                                # every score is 0 but for a few that are 7.5
+    for x, at in zip(score[few], slots[few]):
+        keys[at // 16, at % 16 * (hd // 32):][:hd // 32] = (old[at].double() * 7.5 / x).bfloat16()
+    out, lse = c.call()
+    torch.cuda.synchronize()
+    assert torch.isfinite(out).all()
+    check(c, out, lse)
