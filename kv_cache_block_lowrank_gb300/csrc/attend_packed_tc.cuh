@@ -7,7 +7,8 @@
 // memory as the tensor cores read them:
 //   - in fp16, where a bf16 scale (8 bits) times a code (3 bits) has a place for every bit, so that
 //     K and V enter the products exactly.  Scales outside [2^-17, 2^6] (but for 0), or not finite,
-//     do not fit: the call's flags then ask the kernel for few rows to do all of it (Params::guard);
+//     do not fit: the call's flags then ask the kernel for few rows to do all of it (Params::guard),
+//     as they do for queries whose scores may pass fp32;
 //   - a 16-byte piece of K is one word's eight elements in the order 0 4 1 5 2 6 3 7, as they come
 //     out of the nibbles' places, and Q is laid out the same;
 //   - tokens lie in the order 2c, 2c + 1, 2c + 8, 2c + 9 (c = 0 .. 3) of a tile's 16, in which a
@@ -503,6 +504,9 @@ __global__ void __launch_bounds__(Many<HD>::kThreads, 1)
                     // (c is never 0: times what is hidden, -inf, it has to be -inf)
                     const float up = p.c < 0.0f ? -pow2(e) : (p.c > 0.0f ? pow2(e) : 0.0f);
                     c = p.c == 0.0f ? 1.0f : fmaxf(fabsf(p.c) * pow2(-e), 1.2e-38f);
+                    // Scores here are below 2^28, so that times c they may be past fp32: then the
+                    // kernel for few rows, which does not shift rows so, says what they come to.
+                    if (here && c > 0x1p98f && most < 0x7F80u) *(volatile int*)&bar.unfit = 1;
 #pragma unroll 2
                     for (int i = 0; i < HD / 8; ++i) {
                         uint4 u = make_uint4(0, 0, 0, 0);

@@ -71,3 +71,26 @@ def test_values_near_the_end(hd, nq, ctx):
     torch.cuda.synchronize()
     assert torch.isfinite(out).all()
     check(c, out, lse)
+
+
+@pytest.mark.parametrize("hd,nq,rows", [(64, 4, 20), (128, 8, 9), (192, 2, 40), (256, 1, 50)])
+def test_many_rows_whose_factor_is_past_fp32(hd, nq, rows):
+    """Scores of 0 in spite of a query of 2^126 and a factor of 2^12: the keys are 0."""
+    c = Case(hd, nq, 1, 16, [200], [rows], scale=2.0 ** 12)
+    scales_of(c, False).zero_()
+    c.q[:, :, 5] = 2.0 ** 126
+    out, lse = c.call()
+    torch.cuda.synchronize()
+    assert hss.hss_read_device_error() == 0
+    assert torch.isfinite(out).all()
+    check(c, out, lse)
+
+
+@pytest.mark.parametrize("hd,rows", [(64, 1), (128, 20), (256, 3)])
+def test_scores_past_fp32_are_not_taken_for_nothing(hd, rows):
+    """A row with a score past 3.4e38 is not a number; it does not read as a row that sees nothing."""
+    c = Case(hd, 2, 1, 16, [100], [rows], scale=2.0 ** 12)
+    c.q[0, 1] = (c.q[0, 1].double() * 2.0 ** 124).bfloat16()
+    out, lse = c.call()
+    torch.cuda.synchronize()
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
