@@ -603,7 +603,8 @@ typedef struct hss_norm_rope_args {
  *   y[i] = x[i] / sqrt(mean_j x[j]^2 + eps) * (weight[i] + weight_offset),
  * over the whole head (head_dim elements, the ones past rot_dim too), then rotated and written as
  * there.  Values are not normed.  Norm and rotation are computed in fp32 and rounded once to bf16;
- * the sum of squares is fp32 too, so that a head whose sum passes 3.4e38 comes out as 0.
+ * the sum of squares is fp32 too, so that a head whose sum passes 3.4e38 comes out as 0 (small heads
+ * lose nothing, with eps 0 either, where a head of zeros alone is NaN, 0 / 0).
  *   q_weight, k_weight  device, [head_dim] or, with a stride, [heads, head_dim] bf16, 16-byte
  *             aligned; NULL: 1 (weight_offset is then not added)
  * The other arguments, the refusals and the device-side errors are those of hss_rope_tokens.

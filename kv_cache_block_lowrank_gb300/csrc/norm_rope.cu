@@ -21,6 +21,7 @@ namespace hss {
 namespace {
 
 constexpr int kMostThreads = 256;
+constexpr float kSmallest = 0x1p-100f;  // of a mean square whose bits are all there
 
 enum RopeMode { kInterleaved, kHalf, kHalfOdd };
 
@@ -90,6 +91,13 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
     return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                       pack_bf16x2(x[6], x[7]));
 }
+// Both of a word times 2^100, which is exact.
+__device__ __forceinline__ uint32_t raise2(uint32_t u) {
+    return pack_bf16x2(low(u) * 0x1p100f, high(u) * 0x1p100f);
+}
+__device__ __forceinline__ uint4 raise8(const uint4& u) {
+    return make_uint4(raise2(u.x), raise2(u.y), raise2(u.z), raise2(u.w));
+}
 __device__ __forceinline__ float sum_squares(const uint4& u, float s) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -148,8 +156,8 @@ __device__ __forceinline__ void turn_half(float* x, float* y, int j, const float
 // Half layout whose halves are not whole vectors: each element's partner is fetched by itself,
 // and normed here.
 __device__ __forceinline__ void turn_half_odd(float* x, const uint16_t* head,
-                                              const uint16_t* weight, float inv, float offset,
-                                              int v, int rot, const float2* cs) {
+                                              const uint16_t* weight, float up, float inv,
+                                              float offset, int v, int rot, const float2* cs) {
     const int half = rot / 2;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -157,7 +165,7 @@ __device__ __forceinline__ void turn_half_odd(float* x, const uint16_t* head,
         if (i >= rot) break;
         const bool first = i < half;
         const int other = first ? i + half : i - half;
-        float o = __uint_as_float(static_cast<uint32_t>(__ldg(head + other)) << 16) * inv;
+        float o = __uint_as_float(static_cast<uint32_t>(__ldg(head + other)) << 16) * up * inv;
         if (weight != nullptr)
             o *= __uint_as_float(static_cast<uint32_t>(__ldg(weight + other)) << 16) + offset;
         const float2 c = cs[first ? i : other];
@@ -165,7 +173,8 @@ __device__ __forceinline__ void turn_half_odd(float* x, const uint16_t* head,
     }
 }
 
-template <int HD, int MODE>
+// SMALL: eps is below kSmallest, so that a head's mean square may be.
+template <int HD, int MODE, bool SMALL>
 __global__ void __launch_bounds__(kMostThreads, 4) norm_rope_kernel(const NormParams p) {
     using D = Deal<HD>;
     constexpr int kLanes = D::kLanes, kPairs = D::kPairs, kBatch = D::kBatch;
@@ -235,9 +244,30 @@ __global__ void __launch_bounds__(kMostThreads, 4) norm_rope_kernel(const NormPa
             // (by all lanes of the warp: a head's are neighbours, and what is past the end is 0)
 #pragma unroll
             for (int m = 1; m < kLanes; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-            if (item >= end) continue;
             const bool turned = h < p.q_heads + p.k_heads;
-            const float inv = rsqrtf(sum * (1.0f / HD) + p.eps);
+            float inv = rsqrtf(sum * (1.0f / HD) + p.eps);
+            bool tiny = false;
+            if constexpr (SMALL) {
+                // A head may be so small that its squares lose their bits, or are 0: its elements are
+                // then taken times 2^100 (below 2^-46 they all are), eps times 2^200.
+                tiny = item < end && turned && sum * (1.0f / HD) + p.eps < kSmallest;
+                if (__any_sync(0xffffffffu, tiny)) {
+                    sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i) {
+                        if (tiny) {
+                            x[u][i][0] = raise8(x[u][i][0]);
+                            x[u][i][1] = raise8(x[u][i][1]);
+                            sum = sum_squares(x[u][i][1], sum_squares(x[u][i][0], sum));
+                        }
+                    }
+#pragma unroll
+                    for (int m = 1; m < kLanes; m <<= 1)
+                        sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                    if (tiny) inv = rsqrtf(sum * (1.0f / HD) + p.eps * 0x1p100f * 0x1p100f);
+                }
+            }
+            if (item >= end) continue;
             const uint16_t* weight =
                 h < p.q_heads ? (p.q_weight == nullptr ? nullptr : p.q_weight + h * p.q_weight_stride)
                               : (p.k_weight == nullptr
@@ -262,8 +292,8 @@ __global__ void __launch_bounds__(kMostThreads, 4) norm_rope_kernel(const NormPa
                         turn_interleaved(a, v0, p.rot, cs);
                         turn_interleaved(b, v1, p.rot, cs);
                     } else {
-                        turn_half_odd(a, head[u], weight, inv, p.offset, v0, p.rot, cs);
-                        turn_half_odd(b, head[u], weight, inv, p.offset, v1, p.rot, cs);
+                        turn_half_odd(a, head[u], weight, tiny ? 0x1p100f : 1.0f, inv, p.offset, v0, p.rot, cs);
+                        turn_half_odd(b, head[u], weight, tiny ? 0x1p100f : 1.0f, inv, p.offset, v1, p.rot, cs);
                     }
                     x[u][i][0] = pack8(a);
                     x[u][i][1] = pack8(b);
@@ -287,11 +317,11 @@ __global__ void __launch_bounds__(kMostThreads, 4) norm_rope_kernel(const NormPa
     }
 }
 
-template <int HD>
+template <int HD, bool SMALL>
 auto kernel_for(int mode) {
-    return mode == kInterleaved ? norm_rope_kernel<HD, kInterleaved>
-           : mode == kHalf      ? norm_rope_kernel<HD, kHalf>
-                                : norm_rope_kernel<HD, kHalfOdd>;
+    return mode == kInterleaved ? norm_rope_kernel<HD, kInterleaved, SMALL>
+           : mode == kHalf      ? norm_rope_kernel<HD, kHalf, SMALL>
+                                : norm_rope_kernel<HD, kHalfOdd, SMALL>;
 }
 
 template <int HD>
@@ -311,7 +341,9 @@ hss_status launch(const NormParams& p, int64_t tokens, int mode, int num_sms, cu
     const int each = splits > 1 ? 1 : D::kBatch;
     int threads = ((q.split_items + each - 1) / each + 31) / 32 * 32;
     threads = threads < 64 ? 64 : (threads > kMostThreads ? kMostThreads : threads);
-    return launch_pdl(kernel_for<HD>(mode), grid, dim3(threads), 0, stream, q) == cudaSuccess
+    // (in a kernel of its own: the check makes 8192 tokens of 64 + 8 heads 63.5 us, not 62.3)
+    const auto kern = q.eps < kSmallest ? kernel_for<HD, true>(mode) : kernel_for<HD, false>(mode);
+    return launch_pdl(kern, grid, dim3(threads), 0, stream, q) == cudaSuccess
                ? HSS_OK
                : HSS_ERR_CUDA;
 }
