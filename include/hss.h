@@ -653,8 +653,9 @@ typedef struct hss_pack_args {
  *   cache     device, one layer's pages, 16-byte aligned
  * A negative slot marks padding; a slot >= max_blocks * block_size is skipped and raises
  * HSS_ERR_OUT_OF_RANGE in *dev_status and the library's device error word.  Name a slot once: what
- * two tokens of one call leave in it is a mixture of both.  (From 4096 tokens on, 16 tokens in a row
- * that fill a tile are packed together: give tokens in the order of their slots.)
+ * two tokens of one call leave in it is a mixture of both.  (From 4096 tokens of 1024 elements on, K
+ * and V together, 16 tokens in a row that fill a tile are packed together: give tokens in the order of
+ * their slots.)  No output overlaps an input.
  */
 hss_status hss_pack_kv_tokens(const hss_pack_args* args, const uint16_t* K, const uint16_t* V,
                               uint8_t* cache, void* stream);

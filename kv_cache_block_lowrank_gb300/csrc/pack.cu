@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kWindowTokens = 4096;
+constexpr int kWindowElements = 1024;  // of a token, in the heads that are asked for
 
 struct PackParams {
     const uint16_t* K;
@@ -354,10 +355,12 @@ hss_status run(const hss_pack_args& a, PackParams p, bool unpack, int halves,
     p.lib_error = dev->error_word;
     p.heads = halves * p.nkv;
     const int hd = a.dims.head_dim;
-    // Whole tiles only where there are CTAs enough to hide how long one takes (packed and read back, 8
-    // heads of 128: 8191 tokens 37 us, token by token 43; 16384 tokens 61 and 78; but 1024 tokens 19
-    // and 10).
-    const bool windows = p.tokens >= kWindowTokens;
+    // Whole tiles only where there are CTAs and heads enough to hide how long one takes.  Packed so, and
+    // token by token (K and V, from graphs, us): 8 heads of 128: 2048 tokens 13.0 and 10.2, 4096 15.1
+    // and 15.7, 8191 24.5 and 26.7, 16384 40.9 and 49.2; 4 heads of 128: 4096 10.9 and 10.3, 16384 28.5
+    // and 26.8; 2 heads: 16384 21.4 and 16.0; 1 head 17.1 and 10.3; 8 heads of 64: 8191 14.3 and 15.0;
+    // 3 of 192: 16384 32.4 and 32.8.  Read back: 8 heads of 128: 4096 11.4 and 12.2, 16384 26.0 and 35.0.
+    const bool windows = p.tokens >= kWindowTokens && p.heads * hd >= kWindowElements;
     dim3 grid;
     if (windows) {
         grid = dim3(static_cast<unsigned>((p.tokens + 15) / 16), kShares);
