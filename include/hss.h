@@ -602,7 +602,8 @@ typedef struct hss_norm_rope_args {
  * in the same launch:
  *   y[i] = x[i] / sqrt(mean_j x[j]^2 + eps) * (weight[i] + weight_offset),
  * over the whole head (head_dim elements, the ones past rot_dim too), then rotated and written as
- * there.  Values are not normed.  Norm and rotation are computed in fp32 and rounded once to bf16;
+ * there.  Values are not normed.  Norm and rotation are computed in fp32 (weight + weight_offset is off
+ * by 2^-24 of the offset at most, and not at all if that is a power of two) and rounded once to bf16;
  * the sum of squares is fp32 too, so that a head whose sum passes 3.4e38 comes out as 0 (small heads
  * lose nothing, with eps 0 either, where a head of zeros alone is NaN, 0 / 0).
  *   q_weight, k_weight  device, [head_dim] or, with a stride, [heads, head_dim] bf16, 16-byte
@@ -716,14 +717,19 @@ size_t hss_attend_packed_workspace_bytes(const hss_dims* dims, int32_t num_seqs,
  *   cache    device, one layer's pages, 16-byte aligned
  *   out      device, [total_q, num_q_heads, head_dim] bf16, 16-byte aligned
  *   lse      device, [total_q, num_q_heads] f32, or NULL
- * Scores, softmax statistics and sums are fp32; the statistics take the weights exp(s - m)
- * unrounded.  Up to 32 rows of a sequence and kv head together (rows times num_q_heads /
- * num_kv_heads, by max_q): a weight times its value's scale enters the product with the codes
- * rounded to bf16; an element of out is off by at most 2^-8 sum_p exp(s - lse) |v_p| for it, beside
- * the rounding of out itself.  More rows run on the tensor cores of tcgen05 with K, V and the weights
- * in fp16: K and V lose nothing, a weight 2^-11 of itself at most.  There a scale that fp16 has no
- * place for (above 64, or below 2^-17 but not 0, or not finite) makes the whole call run by the
- * first method after all, which is correct for every scale but several times slower.
+ * No output overlaps an input.
+ * Scores, softmax statistics and sums are fp32: sums over 32 elements of q times codes, scores, and sums
+ * over tokens of weights (1 at most) times values have to stay below 3.4e38 (a row with a score above
+ * it is NaN).  The statistics take the weights exp(s - m) unrounded; a weight below 2^-118 of the
+ * row's largest counts as 0.  Up to 32 rows of a sequence and kv head together (rows times
+ * num_q_heads / num_kv_heads, by max_q): a weight times its value's scale enters the product with the
+ * codes rounded to bf16; an element of out is off by at most 2^-8 sum_p exp(s - lse) |v_p| for it,
+ * beside the rounding of out itself.  More rows run on the tensor cores of tcgen05 with K, V and the weights
+ * in fp16: K and V lose nothing, a weight 2^-11 of itself or 2^-32 of the row's largest.  There a scale
+ * that fp16 has no place for (above 64, or below 2^-17 but not 0, or not finite; also a query times the
+ * factor past 2^108) makes the whole call run by the first method after all, 16 rows at a time: of any
+ * sequence's rows, for one group that any of them sees.  That takes three to seven times as long (512
+ * rows over 32768 tokens 3.6 ms, not 0.51; 16 chunks of 64 rows over 2000 0.33, not 0.11).
  * A call is one to three launches on the stream: for few rows the attention and, unless contexts are
  * short, the join of what several CTAs have of a row; for many rows the attention, that second
  * attempt, which ends at once if it is not needed, and at most one join for both.  A pipeline wait

@@ -13,7 +13,13 @@ using packed::kSms;
 constexpr int kRanges = 2 * kSms;
 constexpr int kRangeRows = 16 * kRanges;
 
-// Rows of one sequence and kv head from which on the tensor cores' rows are filled well enough.
+// Rows of one sequence and kv head from which on the tensor cores' rows are filled well enough.  (Heads
+// of 128, by the kernel for few rows, 16 at a time, and the other.  64 sequences of 2048 tokens and 8 kv
+// heads: 24 rows 135 and 162 us, 32 137 and 164, 40 190 and 166, 64 249 and 171; 16 of 4096: 32 76 and
+// 88, 40 101 and 91; one of 32768: 32 41 and 51, 40 53 and 51, 64 66 and 53.  With 2 kv heads less is
+// there to fill: 16 of 4096 tokens 32 31 and 41, 48 38 and 43, 64 45 and 44; one of 32768 64 30 and 39, 96
+// 36 and 41.  16 of 4096, 8 kv heads of 64: 32 57 and 75, 64 94 and 77; of 192: 32 94 and 118, 64 160
+// and 129; of 256: 32 162 and 166, 40 221 and 169.)
 constexpr int64_t kManyRows = 33;
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }

@@ -21,14 +21,15 @@
 // to the workspace and a second kernel joins it.  Short units are not cut, and if all are short there
 // is no list: a CTA takes a unit.
 //
-// What bounds it, and what it reaches on GB300 (HBM 6.8 TB/s measured): instructions.  A tile of 16
-// tokens of one head takes 300 of them for its 2304 bytes, of which the cache's bandwidth leaves
-// time for 390 at the full rate; 12 warps an SM issue 54 % (ncu), more of them with fewer registers
-// each were slower (16: 154 us where 12 take 145).  64 sequences of 1k to 16k tokens, 32 query heads on
-// 8 of 128: 143 us, 4.5 TB/s; 152 sequences of 4096 tokens 154 us (a copy of an earlier
-// version without its arithmetic, 116).  One of
-// 32768 tokens 22.6 us: its tiles are 5.6 at HBM's rate, the rest is one way through memory after another (lengths,
-// block ids, first tiles, pieces, join).  One of 500 tokens 11 us.
+// What bounds it, and what it reaches on GB300 (HBM 6.8 TB/s measured): the latency of its own
+// instructions.  A tile of 16 tokens of one head takes 312 of them for its 2304 bytes; the cache's
+// bandwidth would leave time for 390 if every slot were used, but the 12 warps an SM that registers
+// leave room for (168 each, 18 % of the warps there can be) use 55 % of the issue slots and wait for
+// their own results most (ncu).  More warps with fewer registers each spill and were slower (16: 154 us
+// where 12 took 145).  64 sequences of 1k to 16k tokens, 32 query heads on 8 of 128: 145 us, 4.4 TB/s;
+// 152 sequences of 4096 tokens 157 us (a copy of an earlier version without its arithmetic, 116).  One
+// of 32768 tokens 22.7 us: its tiles are 5.6 at HBM's rate, the rest is one way through memory after
+// another (lengths, block ids, first tiles, pieces, join).  One of 500 tokens 11 us.
 // What helped, on those 64 sequences: nibbles into the products without shifts for half of them,
 // exact as bf16 counts them (240 to 193 us), scores begun with what the nibbles' 8 comes to, two tiles
 // a step and twelve warps (160), cp.async without barriers in place of bulk copies (the same step),
@@ -46,7 +47,8 @@ namespace packed {
 constexpr int kSms = 152;          // GB300's; the workspace does not depend on the device
 constexpr float kLazy = 8.0f;
 constexpr int32_t kNoWindow = 0x7FFFFF00;
-// Short contexts (as far as the host can tell: by the table or the window) of not too many units: a
+// Short contexts (as far as the host can tell: by the pages of the whole batch or by the window, so that
+// many short sequences without a window are listed) of not too many units: a
 // CTA takes a unit, and there is neither a list nor a join.  (32 heads on 8 of 128; with the list and
 // so: one sequence of 500 tokens 14.4 and 11.2 us, of 2000 14.4 and 20.5; windows of 500 tokens of 16
 // sequences 19.3 and 12.3, of 64 29.8 and 23.0, of 256 77 and 83; of 2000 tokens of 16 24.7 and 20.7.)
@@ -67,8 +69,13 @@ template <int UNIT>
 constexpr int kUncut = UNIT == 1 ? 48 : 20;
 // In the list a unit is longer than its tiles by what it costs besides (its first loads, the warps'
 // meeting, its rows' way out), so that ranges of equal length take equal time: in tiles here, in
-// jobs of four for many rows.  (None, 8, 16 and 32: 64 sequences of 1k to 16k tokens 160, 156, 151
-// and 143 us; 16 windows of 4093 tokens with an empty sequence among them 62, 54, 41 and 35.)
+// jobs of four for many rows.  (0, 16, 32, 64, 128 and 256: 64 sequences of 1k to 16k tokens 162, 153,
+// 145, 144, 149 and 159 us; 16 windows of 4093 tokens with an empty sequence among them 63, 42, 35, 37,
+// 41 and 48; 300 sequences of 300 to 1000 tokens 108, 97, 94, 94, 98 and 102; 32 of 1k to 8k with 4 kv
+// heads of 256 56, 51, 52, 56, 62 and 74.  Many rows, 0, 3, 6, 12, 24 and 48: 512 rows over 32768
+// tokens 512, 515, 512, 513, 512 and 531; 16 chunks of 200 over 2000 238, 230, 230, 222, 217 and 218; 40
+// of 10 to 40 rows over 50 to 6000 tokens 246, 236, 208, 174, 162 and 182; 4 of 100 to 300 over 2k to
+// 8k, heads of 256, 203, 193, 189, 190, 208 and 242: ragged chunks of 128 would rather have 12.)
 template <int UNIT>
 constexpr int kBeside = UNIT == 1 ? 32 : 6;
 constexpr int kScanWarps = 20;      // of the largest CTA that looks for its range
@@ -779,7 +786,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
                 for (int G = 0; G < NG; ++G) {
                     // A group's weights: the token's weight by its scale, rounded to bf16 because
                     // both operands of a product have one type (an output is off by up to
-                    // 2^-9 sum p |v| for it), rows over tokens turned to tokens over rows.
+                    // 2^-8 sum p |v| for it), rows over tokens turned to tokens over rows.
                     const float f0 = scale_at(vs0, G), f1 = scale_at(vs1, G);
                     uint32_t b[NT][2];
 #pragma unroll

@@ -15,8 +15,9 @@
 //     word of V holds them; the columns of S and P follow K's rows.  V is stored by element, tokens
 //     side by side, so both operands are K-major.
 // Q is scaled by a power of two for every row, weights by 2^7 (with the maximum's lag of 2^8 they
-// reach 2^15), so that fp16's range serves both; a weight below 2^-31 of the largest counts as 0 in
-// the product with V, in l as it is.
+// reach 2^15), so that fp16's range serves both.  A weight is off by 2^-11 of itself in the product with
+// V or, below 2^-21 of the largest, where fp16 has no full place for it, by 2^-32 of the largest; in l
+// it is as it was.
 //
 // Roles (20 warps): 10 copies; 0-7 decode; 8, 9 issue the products of a row tile each; 12-19
 // softmax, four to a row tile, with registers that the others hand over.  One row tile's exponentials

@@ -1,8 +1,8 @@
 // pack.cu -- tokens into and out of the packed cache (include/hss.h has its layout).
 //
 // A group of 32 elements is four neighbouring lanes of a warp, 8 elements (16 bytes) each: its
-// largest element takes two shuffles, and codes follow from an IEEE division, so that every
-// packing of a row gives the same bits.  Of K a lane's 8 codes are one 32-bit word of the page.  Of
+// largest element takes two shuffles, and codes are the exactly rounded quotients (packed.cuh has
+// how, mostly without a division), so that every packing of a row gives the same bits.  Of K a lane's 8 codes are one 32-bit word of the page.  Of
 // V they are nibbles of 8 bytes; neighbouring lanes hold the two nibbles of a byte, and exchange
 // halves so that each writes four whole bytes.
 //
@@ -10,9 +10,10 @@
 // and go out (or come in) as whole 16-byte pieces of the page; V's bytes, which hold a token each,
 // change places with the elements in shared memory.  What else there is goes token by token.
 //
-// What bounds it: few tokens, the launch (64 tokens 4 us to pack and 4 to read back); many, latency:
-// 8191 tokens of 8 heads of 128, packed and read back, 33 to 36 us for 86 MB, 2.6 TB/s, token by token
-// 43; ncu shows 62 % of the issue rate and 40 % of the warps there can be.
+// What bounds it: few tokens, the launch (64 tokens 4 us to pack and 4 to read back); many, latency: a
+// warp has a tile's rows in two goes of four loads and picks V's nibbles one by one.  8191 tokens of 8
+// heads of 128, packed and read back, 33 us for 86 MB, 2.6 TB/s (apart, from graphs, 24.6 and 16.4);
+// ncu shows 62 % of the issue rate and 40 % of the warps there can be.
 #include <cuda_runtime.h>
 
 #include "packed.cuh"

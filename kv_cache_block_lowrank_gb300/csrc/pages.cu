@@ -6,9 +6,11 @@
 // CTAs takes a whole plan, a cluster barrier between the steps, so that one launch does it; ranks
 // are ballots within a warp and sums over warps and CTAs (distributed shared memory).  Counts are
 // added with integer atomics, whose order does not matter, so the result is the same every time.
-// What bounds a plan is latency: six barriers and as many trips to L2 (256 sequences with 18,000
-// table entries over 23,000 pages forked 34 us, 8000 entries over 17,000 pages compacted 13); the
-// caller's host work for a call with its copies is longer (51 us with the allocations, from Python).
+// What bounds a plan is latency: six barriers and as many trips to L2, and in a fork each entry's
+// search for its sequence, whose numbers are then worked out anew from the inputs (256 sequences with
+// 18,000 table entries over 23,000 pages forked 34 us, 8000 entries over 17,000 pages compacted 13).
+// In eager calls the caller's host work with its copies is longer (51 us with the allocations, from
+// Python).
 //
 // The copies are a kernel of their own, at the rate of HBM: 4.3 GB of pages compacted, 2.1 GB moved,
 // 329 us, 6.5 TB/s.
